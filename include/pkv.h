@@ -27,6 +27,12 @@
  *    fixed-size pages anywhere in GPU memory, mapped by a per-request table).
  *    Each new token's K/V row is written into its slot of the paged pool.
  *
+ *  - pkv_prompt_attn: causal attention over whole prompts, straight from
+ *    packed q, k and v rows (no cache read).
+ *
+ *  - pkv_tables_step and pkv_tables_fork: the page pool's bookkeeping on the
+ *    GPU, for steps without a host round trip.
+ *
  *  - pkv_bm_* and pkv_copy_blocks: the page pool's bookkeeping on the host
  *    (per-sequence page tables, shared pages stored once, copy-on-write) and
  *    the page copies it asks for.
@@ -444,6 +450,113 @@ pkv_status pkv_reshape_and_cache_head_scaled(const void *k, const void *v, pkv_d
 pkv_status pkv_copy_blocks(void *k_cache, void *v_cache, pkv_dtype kv_dtype, int num_kv_heads,
                            int head_dim, int block_size, int num_blocks, const int32_t *pairs,
                            int num_pairs, int32_t *status, void *stream);
+
+/*
+ * Causal attention over whole prompts ("Inference optimization" lesson, Step 2
+ * scaled_dot_product_attention with its causal mask): the first pass of new
+ * requests, whose K and V are still in the rows that the projections wrote.
+ * Sequence s is rows q_start[s] .. q_start[s+1]-1 of q, k, v and out (packed,
+ * any lengths, empty ones included); its row i attends its rows 0 .. i:
+ *   out[i, h, :] = sum_{j <= i} softmax_j(scale * q[i, h] . k[j, h / G]) v[j, h / G]
+ * with G = num_q_heads / num_kv_heads <= 16.  K and V rows of other sequences
+ * and later rows never reach a result, whatever they hold (infinities and NaN
+ * included).  A NaN among the scores a row sees gives a NaN row.
+ *
+ *   q            [num_tokens, num_q_heads, head_dim] of dtype (F32 or BF16), row t
+ *                at q + t * q_stride elements; k, v [num_tokens, num_kv_heads,
+ *                head_dim] likewise.  A stride is at least the row it steps over
+ *                and a multiple of 16 bytes, so q, k and v may be views of one
+ *                fused projection.  The arithmetic is f32 throughout; with BF16
+ *                inputs on the tensor cores the softmax weights are rounded to
+ *                bf16 for a BF16 out and carried as two bf16 parts for an F32 out.
+ *   q_start      int32 [num_seqs + 1] (device), non-decreasing, within
+ *                [0, num_tokens].  Rows of out that belong to no sequence are
+ *                not written.
+ *   head_dim     64 or 128.
+ *   max_q_len    host bound on every sequence's rows.
+ *   scale        finite, any sign.
+ *   out          [num_tokens, num_q_heads, head_dim], F32 or BF16, dense.  It may
+ *                not overlap the inputs.
+ *   status       optional device int32, as for pkv_reshape_and_cache: a sequence
+ *                whose q_start range is invalid or longer than max_q_len is
+ *                reported as PKV_ERR_OUT_OF_RANGE and not written.
+ *   flags        0.
+ * Needs no workspace and no host copy of q_start; can be captured in a graph.
+ */
+pkv_status pkv_prompt_attn(const void *q, const void *k, const void *v, pkv_dtype dtype,
+                           int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                           const int32_t *q_start, int num_seqs, int num_tokens, int num_q_heads,
+                           int num_kv_heads, int head_dim, int max_q_len, float scale, void *out,
+                           pkv_dtype out_dtype, int32_t *status, int flags, void *stream);
+
+/*
+ * One scheduling step of a page pool that lives in device memory: the tables,
+ * slots and packed row starts the other calls read, built on the GPU from the
+ * tokens that every row gives back and asks for ("Inference optimization"
+ * lesson, section "PagedAttention"; "Continuous Batching e PagedAttention no
+ * vLLM", section 3).  The pool is three device arrays of the caller:
+ *   seq_lens     int32 [num_seqs], tokens held by each row (0: the row is free).
+ *   block_tables int32 [num_seqs, max_blocks_per_seq], as for attention.
+ *   ref_counts   int32 [num_blocks], 16-byte aligned: rows holding each page (0:
+ *                free).  A new pool is all zero; a caller may hold pages of its
+ *                own by counting them (a cached prefix).
+ * The step, in this order:
+ *   drop_lens    int32 [num_seqs] or NULL (nothing): row s drops its last
+ *                min(drop_lens[s], seq_lens[s]) tokens (rejected drafts, or all
+ *                of a finished request).  Pages it no longer needs lose a
+ *                reference, their table entries become -1.
+ *   new_lens     int32 [num_seqs] or NULL (nothing): row s reserves new_lens[s]
+ *                tokens after the ones it keeps.  Fresh pages are taken lowest id
+ *                first, in row order.  A row that would write into a part-filled
+ *                page other rows still hold gets a fresh page in its place (its
+ *                first one) and (old, new) in copy_pairs[s]: the last holder
+ *                writes in place.  With one new token per row this is
+ *                pkv_bm_append over the rows in order.
+ * and what it writes besides the pool:
+ *   q_start      int32 [num_seqs + 1] or NULL: first packed row of each row's new
+ *                tokens (the q_start of pkv_prompt_attn and
+ *                pkv_paged_attn_prefill).
+ *   slot_mapping int64 [max_tokens]: cache slots of the new tokens in that
+ *                order, then -1 (which pkv_reshape_and_cache skips).  NULL when
+ *                max_tokens is 0.
+ *   copy_pairs   int32 [num_seqs, 2] or NULL: (src, dst) page copies, (-1, -1) for
+ *                rows without one.  pkv_copy_blocks with status = NULL skips
+ *                those; run it before the new tokens are written.  When NULL, a
+ *                row that needs a copy makes the reservation fail.
+ * Reservations are made for all rows or for none: when the pool has too few
+ * free pages (PKV_ERR_NO_BLOCKS), or a row is invalid (a length outside its
+ * table before or after the step, a negative count, a last page that is not
+ * held) or more than max_tokens tokens are asked for (PKV_ERR_OUT_OF_RANGE), the
+ * drops stand, q_start is all zero, slot_mapping and copy_pairs all -1, and
+ * *status (optional, device) records why, as for pkv_reshape_and_cache.  A drop
+ * that meets a page id outside the pool or a page nobody holds skips it and is
+ * reported as PKV_ERR_OUT_OF_RANGE too, as is a row with a negative drop count,
+ * which drops nothing.  The arrays must not overlap.
+ * num_seqs up to 8192 (else PKV_ERR_UNSUPPORTED), max_blocks_per_seq below
+ * 2^26.  Calls on one pool must be ordered by the caller (one stream).
+ */
+pkv_status pkv_tables_step(int32_t *seq_lens, int32_t *block_tables, int32_t *ref_counts,
+                           int num_seqs, int max_blocks_per_seq, int block_size, int num_blocks,
+                           const int32_t *drop_lens, const int32_t *new_lens, int32_t *q_start,
+                           int64_t *slot_mapping, int max_tokens, int32_t *copy_pairs,
+                           int32_t *status, void *stream);
+
+/*
+ * Rows that start as copies of others and share their pages (several answers
+ * to one prompt, beams): for every i < num_pairs with (parent, child) =
+ * (pairs[2i], pairs[2i+1]) (int32, device), row child, which must be free
+ * (length 0), gets parent's length and table entries, and every page one more
+ * reference; as pkv_bm_fork.  A pair of two negative numbers is skipped.  A row
+ * outside the batch, a child that is not free, is listed by an earlier pair or
+ * is a parent in the same call, a parent of invalid length: the pair is skipped
+ * and reported as PKV_ERR_OUT_OF_RANGE in *status (optional device int32).  So is
+ * a page outside the pool or held by nobody: the child's entry becomes -1.
+ * Other arguments as for pkv_tables_step.
+ */
+pkv_status pkv_tables_fork(const int32_t *pairs, int num_pairs, int32_t *seq_lens,
+                           int32_t *block_tables, int32_t *ref_counts, int num_seqs,
+                           int max_blocks_per_seq, int block_size, int num_blocks,
+                           int32_t *status, void *stream);
 
 /*
  * Host-side block manager (no GPU calls; thread-safe).  It keeps the page

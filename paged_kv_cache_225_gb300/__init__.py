@@ -10,6 +10,9 @@ current stream and the workspace allocation.
     paged_attn_decode_append(q, new_k, new_v, k_cache, v_cache, ..., out)
     paged_attn_prefill(q, q_start, k_cache, v_cache, block_tables, seq_lens, scale, out)
     reshape_and_cache(k, v, slot_mapping, k_cache, v_cache)
+    prompt_attn(q, k, v, q_start, scale, out)          (whole prompts, no cache read)
+    tables_step(seq_lens, block_tables, ref_counts, drop_lens=, new_lens=, ...)
+    tables_fork(pairs, seq_lens, block_tables, ref_counts)   (page pool on the GPU)
     copy_blocks(k_cache, v_cache, pairs)
     BlockManager(num_blocks)   (host-side page pool: add / fork / append / free / tables)
 """
@@ -28,6 +31,7 @@ __all__ = ["paged_attn_decode", "paged_attn_decode_append", "paged_attn_prefill"
            "paged_attn_decode_head_scaled", "reshape_and_cache_head_scaled",
            "reshape_and_cache", "workspace_size", "partition_tokens",
            "prefill_workspace_size", "prefill_partition_tokens", "copy_blocks",
+           "prompt_attn", "tables_step", "tables_fork",
            "BlockManager",
            "read_status", "PkvError", "lib", "F32", "BF16", "FP8_E5M2", "FP8_E4M3",
            "INT4"]
@@ -121,6 +125,14 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
             L.pkv_reshape_and_cache.argtypes = [vp, vp, i, vp, i, i, i, i, i, vp, vp, i, f, f, vp,
                                                 vp]
             L.pkv_reshape_and_cache.restype = i
+            i64 = ctypes.c_int64
+            L.pkv_prompt_attn.argtypes = [vp, vp, vp, i, i64, i64, i64, vp, i, i, i, i, i, i, f,
+                                          vp, i, vp, i, vp]
+            L.pkv_prompt_attn.restype = i
+            L.pkv_tables_step.argtypes = [vp, vp, vp, i, i, i, i, vp, vp, vp, vp, i, vp, vp, vp]
+            L.pkv_tables_step.restype = i
+            L.pkv_tables_fork.argtypes = [vp, i, vp, vp, vp, i, i, i, i, vp, vp]
+            L.pkv_tables_fork.restype = i
             L.pkv_read_status.argtypes = [vp, i, ctypes.POINTER(ctypes.c_int32), vp]
             L.pkv_read_status.restype = i
             L.pkv_status_string.argtypes = [i]
@@ -625,6 +637,144 @@ def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, pairs: torch.Tenso
                                pairs.shape[0], st_ptr, _stream(dev, stream))
     if rc != 0:
         raise PkvError(rc, "pkv_copy_blocks")
+
+
+def _launch(dev: torch.device, stream: Optional[torch.cuda.Stream], call) -> int:
+    """``call(stream pointer)`` with ``dev`` as the current device."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to {dev}")
+    if torch.cuda.current_device() == dev.index:
+        return call(_stream(dev, stream))
+    with torch.cuda.device(dev):
+        return call(_stream(dev, stream))
+
+
+def _check_rows(t: torch.Tensor, what: str, device: torch.device) -> int:
+    """Row stride in elements of a [T, H, D] tensor whose rows are dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{what} must be a CUDA tensor (the library has no CPU path)")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, expected {device}")
+    if t.dim() != 3:
+        raise ValueError(f"{what} must have 3 dims, got {tuple(t.shape)}")
+    T, H, D = t.shape
+    if T > 0 and ((D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D)):
+        raise ValueError(f"{what}: every row must be dense")
+    return t.stride(0) if T > 1 else H * D
+
+
+def _int32(t: Optional[torch.Tensor], what: str, ndim: int, device: torch.device):
+    if t is None:
+        return None
+    _check(t, what, ndim, device)
+    if t.dtype != torch.int32:
+        raise TypeError(f"{what} must be int32")
+    return t.data_ptr()
+
+
+def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor,
+                scale: float, out: torch.Tensor, *, max_q_len: Optional[int] = None,
+                status: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None, flags: int = 0) -> torch.Tensor:
+    """Causal attention over whole prompts, packed one after another.
+
+    q [T, Hq, D], k, v [T, Hkv, D] (all f32 or all bf16), rows dense and any
+    multiple of 16 bytes apart, so views of a fused QKV projection are fine;
+    q_start int32 [S+1]: sequence s is rows q_start[s]..q_start[s+1]-1, row i of
+    it attends its rows 0..i; out [T, Hq, D] f32/bf16.  ``max_q_len`` bounds the
+    sequences (default T).  ``status`` (int32 [1], optional) records device-side
+    errors.  Returns ``out``.
+    """
+    dev = q.device
+    qs, ks, vs = (_check_rows(t, name, dev) for t, name in ((q, "q"), (k, "k"), (v, "v")))
+    _check(out, "out", 3, dev)
+    starts = _int32(q_start, "q_start", 1, dev)
+    st = _int32(status, "status", 1, dev)
+    T, Hq, D = q.shape
+    if k.shape[0] != T or k.shape[2] != D or v.shape != k.shape or out.shape != q.shape:
+        raise ValueError("inconsistent shapes")
+    if q_start.shape[0] < 1 or (status is not None and status.shape[0] < 1):
+        raise ValueError("q_start needs at least one entry, status exactly one")
+    code = _dtype_code(q, "q")
+    if _dtype_code(k, "k") != code or _dtype_code(v, "v") != code:
+        raise TypeError("q, k and v must have one dtype")
+    rc = _launch(dev, stream, lambda s: lib().pkv_prompt_attn(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), code, qs, ks, vs, starts,
+        q_start.shape[0] - 1, T, Hq, k.shape[1], D, T if max_q_len is None else int(max_q_len),
+        float(scale), out.data_ptr(), _dtype_code(out, "out"), st, int(flags), s))
+    if rc != 0:
+        raise PkvError(rc, "pkv_prompt_attn")
+    return out
+
+
+def _check_pool(seq_lens, block_tables, ref_counts):
+    dev = seq_lens.device
+    ptrs = (_int32(seq_lens, "seq_lens", 1, dev), _int32(block_tables, "block_tables", 2, dev),
+            _int32(ref_counts, "ref_counts", 1, dev))
+    if block_tables.shape[0] != seq_lens.shape[0]:
+        raise ValueError("block_tables needs one row per entry of seq_lens")
+    return dev, ptrs
+
+
+def tables_step(seq_lens: torch.Tensor, block_tables: torch.Tensor, ref_counts: torch.Tensor, *,
+                drop_lens: Optional[torch.Tensor] = None,
+                new_lens: Optional[torch.Tensor] = None,
+                q_start: Optional[torch.Tensor] = None,
+                slot_mapping: Optional[torch.Tensor] = None,
+                copy_pairs: Optional[torch.Tensor] = None, block_size: int = 16,
+                status: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> None:
+    """One scheduling step of a page pool kept on the GPU.
+
+    seq_lens int32 [S], block_tables int32 [S, max_blocks], ref_counts int32
+    [num_blocks] (rows holding each page) are updated in place.  Every row first
+    drops its last ``drop_lens[s]`` tokens, then reserves ``new_lens[s]``: fresh
+    pages lowest id first in row order, all rows or none.  Written: ``q_start``
+    int32 [S+1] (packed rows of the new tokens), ``slot_mapping`` int64 (their
+    slots, then -1) and ``copy_pairs`` int32 [S, 2] ((src, dst) copy-on-write
+    pages for ``copy_blocks`` without a status, else -1).  ``status`` int32 [1].
+    """
+    dev, (lens, tables, refs) = _check_pool(seq_lens, block_tables, ref_counts)
+    S = seq_lens.shape[0]
+    drop, new = _int32(drop_lens, "drop_lens", 1, dev), _int32(new_lens, "new_lens", 1, dev)
+    starts, pairs = _int32(q_start, "q_start", 1, dev), _int32(copy_pairs, "copy_pairs", 2, dev)
+    st = _int32(status, "status", 1, dev)
+    slots, max_tokens = None, 0
+    if slot_mapping is not None:
+        _check(slot_mapping, "slot_mapping", 1, dev)
+        if slot_mapping.dtype != torch.int64:
+            raise TypeError("slot_mapping must be int64")
+        slots, max_tokens = slot_mapping.data_ptr(), slot_mapping.shape[0]
+    for t, shape in ((drop_lens, (S,)), (new_lens, (S,)), (q_start, (S + 1,)),
+                     (copy_pairs, (S, 2)), (status, (1,))):
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError("inconsistent shapes")
+    rc = _launch(dev, stream, lambda s: lib().pkv_tables_step(
+        lens, tables, refs, S, block_tables.shape[1], block_size, ref_counts.shape[0], drop, new,
+        starts, slots, max_tokens, pairs, st, s))
+    if rc != 0:
+        raise PkvError(rc, "pkv_tables_step")
+
+
+def tables_fork(pairs: torch.Tensor, seq_lens: torch.Tensor, block_tables: torch.Tensor,
+                ref_counts: torch.Tensor, *, block_size: int = 16,
+                status: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Rows that start as copies of others: for every (parent, child) in ``pairs``
+    (int32 [n, 2]) the free row child gets parent's length and pages, each with
+    one more reference.  Other arguments as for ``tables_step``."""
+    dev, (lens, tables, refs) = _check_pool(seq_lens, block_tables, ref_counts)
+    ptr = _int32(pairs, "pairs", 2, dev)
+    st = _int32(status, "status", 1, dev)
+    if pairs.shape[1] != 2 or (status is not None and tuple(status.shape) != (1,)):
+        raise ValueError("pairs must be int32 [n, 2], status int32 [1]")
+    rc = _launch(dev, stream, lambda s: lib().pkv_tables_fork(
+        ptr, pairs.shape[0], lens, tables, refs, seq_lens.shape[0], block_tables.shape[1],
+        block_size, ref_counts.shape[0], st, s))
+    if rc != 0:
+        raise PkvError(rc, "pkv_tables_fork")
 
 
 class BlockManager:

@@ -1,0 +1,282 @@
+"""Whole-prompt attention (pkv_prompt_attn) against the same formula in 64
+bits: lengths, groups, types, strides, what masked places may hold, scales,
+device-side reports, streams and graphs."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_225_gb300 as pkv
+
+from prompt_util import reference, tolerance
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def starts(lens, first=0):
+    return torch.from_numpy(np.concatenate([[first], first + np.cumsum(lens)]).astype(np.int32)).to(DEV)
+
+
+def make(lens, Hq, Hkv, D, dtype, seed, fused=True, tail=0):
+    T = int(sum(lens)) + tail
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    qkv = torch.randn((T, Hq + 2 * Hkv, D), generator=g, device=DEV).to(dtype)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    return (q, k, v) if fused else (q.contiguous(), k.contiguous(), v.contiguous())
+
+
+def check(q, k, v, lens, scale, out_dtype=None, **kw):
+    out = torch.full(q.shape, float("nan"), dtype=out_dtype or q.dtype, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkv.prompt_attn(q, k, v, starts(lens), scale, out, status=status, **kw)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    ref, mass, most = reference(q, k, v, lens, scale)
+    tol = tolerance(ref, mass, most, lens, q.shape[2], scale, q.dtype, out.dtype)
+    n = sum(lens)
+    off = (out[:n].double() - ref[:n]).abs()
+    assert not torch.isnan(off).any()
+    assert bool((off <= tol[:n]).all()), f"worst {float((off / tol[:n]).max()):.3g} of the tolerance"
+    assert torch.isnan(out[n:].float()).all()      # rows of no sequence are not written
+    return out
+
+
+TYPES = [(F32, F32), (F32, BF16), (BF16, BF16), (BF16, F32)]
+
+
+@pytest.mark.parametrize("dtype,out_dtype", TYPES)
+@pytest.mark.parametrize("lens", [[1], [2], [17], [64], [127, 128, 129], [0, 1, 0, 33, 1, 0],
+                                  [300, 5, 0, 256, 1], [1] * 70, [65, 63, 511, 97]])
+def test_lengths(lens, dtype, out_dtype):
+    q, k, v = make(lens, 8, 2, 128, dtype, sum(lens), tail=3)
+    check(q, k, v, lens, 1 / math.sqrt(128), out_dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 4), (8, 4), (6, 2), (4, 1), (10, 2), (6, 1), (14, 2), (8, 1),
+                                    (9, 1), (10, 1), (11, 1), (24, 2), (13, 1), (14, 1), (15, 1), (16, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_groups(Hq, Hkv, D, dtype):
+    lens = [150, 3, 0, 71]
+    q, k, v = make(lens, Hq, Hkv, D, dtype, Hq * 100 + D)
+    check(q, k, v, lens, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n,Hq,Hkv,D", [(2500, 4, 4, 64), (3001, 8, 1, 128), (2047, 12, 4, 128)])
+def test_long(n, Hq, Hkv, D, dtype):
+    q, k, v = make([n], Hq, Hkv, D, dtype, n)
+    check(q, k, v, [n], 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.0])
+def test_scales(scale, dtype):
+    lens = [200, 90]
+    q, k, v = make(lens, 4, 2, 64, dtype, 7)
+    check(q, k, v, lens, scale)
+
+
+@pytest.mark.parametrize("dtype,out_dtype", TYPES)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_growing_and_falling_scores(sign, dtype, out_dtype):
+    # The running maximum rises by far more than 2^8 again and again (or never
+    # after the first key).
+    n, D = 700, 64
+    q, k, v = make([n], 4, 2, D, dtype, 3, fused=False)
+    ramp = torch.linspace(0, 6, n, device=DEV)
+    if sign < 0:
+        ramp = ramp.flip(0)
+    q.fill_(1.0)
+    k.copy_((ramp[:, None, None] + 0.01 * k.float()).to(dtype))
+    check(q, k, v, [n], 1.0, out_dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_strides(D, dtype):
+    # Rows 16-byte multiples apart, each tensor with its own distance, dense rows
+    # starting anywhere on a 16-byte boundary.
+    lens, Hq, Hkv = [100, 31], 6, 2
+    T = sum(lens)
+    g = torch.Generator(device=DEV).manual_seed(1)
+
+    def rows(H, pad, first):
+        buf = torch.randn(T * (H * D + pad) + first, generator=g, device=DEV).to(dtype)
+        return torch.as_strided(buf, (T, H, D), (H * D + pad, D, 1), first)
+
+    unit = 16 * 8 // torch.finfo(dtype).bits
+    q, k, v = rows(Hq, unit, 0), rows(Hkv, 3 * unit, unit), rows(Hkv, 0, 5 * unit)
+    check(q, k, v, lens, 0.1)
+
+
+@pytest.mark.parametrize("dtype,out_dtype", TYPES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_masked_places_may_hold_anything(bad, dtype, out_dtype):
+    # Rows before a bad token, and every other sequence, do not see it.
+    lens = [70, 200, 45]
+    q, k, v = make(lens, 8, 2, 64, dtype, 9, fused=False, tail=40)
+    k2, v2 = k.clone(), v.clone()
+    cut = 70 + 90
+    k2[cut:70 + 200], v2[cut:70 + 200] = bad, bad
+    k2[sum(lens):], v2[sum(lens):] = bad, bad
+    a = torch.zeros(q.shape, dtype=out_dtype, device=DEV)
+    b = torch.zeros_like(a)
+    pkv.prompt_attn(q, k, v, starts(lens), 0.125, a)
+    pkv.prompt_attn(q, k2, v2, starts(lens), 0.125, b)
+    ref, mass, most = reference(q, k, v, lens, 0.125)
+    tol = tolerance(ref, mass, most, lens, 64, 0.125, dtype, out_dtype)
+    for rows in (slice(0, cut), slice(270, 315)):
+        assert bool(((a[rows].double() - ref[rows]).abs() <= tol[rows]).all())
+        assert bool(((b[rows].double() - ref[rows]).abs() <= tol[rows]).all())
+
+
+@pytest.mark.parametrize("dtype,out_dtype", TYPES)
+def test_bad_values_reach_the_rows_that_see_them(dtype, out_dtype):
+    lens = [150, 60]
+    q, k, v = make(lens, 4, 1, 128, dtype, 10, fused=False)
+    v[40, 0, 5] = float("inf")
+    v[90, 0, 7] = float("nan")
+    k[120, 0, 0] = float("nan")
+    out = torch.zeros(q.shape, dtype=out_dtype, device=DEV)
+    pkv.prompt_attn(q, k, v, starts(lens), 0.1, out)
+    o = out.float()
+    dims = torch.arange(128, device=DEV)
+    assert torch.isfinite(o[:40]).all() and torch.isfinite(o[150:]).all()
+    assert bool((o[40:90, :, 5] == math.inf).all()) and torch.isfinite(o[40:90][..., dims != 5]).all()
+    assert torch.isnan(o[90:120, :, 7]).all() and bool((o[90:120, :, 5] == math.inf).all())
+    assert torch.isfinite(o[90:120][..., (dims != 5) & (dims != 7)]).all()
+    assert torch.isnan(o[120:150]).all()
+
+
+def test_scores_of_minus_infinity():
+    # A key whose score is -inf has no weight; a row that sees nothing else is NaN,
+    # as in the formula.
+    for dtype in (F32, BF16):
+        q, k, v = make([140], 2, 1, 64, dtype, 11, fused=False)
+        q.copy_(q.abs() + 0.1)
+        k[:130, 0, 0] = -float("inf")
+        out = torch.zeros(q.shape, dtype=dtype, device=DEV)
+        pkv.prompt_attn(q, k, v, starts([140]), 0.1, out)
+        assert torch.isnan(out[:130].float()).all()
+        ref, mass, _ = reference(q[130:], k[130:], v[130:], [10], 0.1)
+        most = float((q[130:].double().abs().amax() * k[130:].double().abs().amax()) * 64)
+        tol = tolerance(ref, mass, most, [140], 64, 0.1, dtype, dtype)
+        assert bool(((out[130:].double() - ref).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_invalid_ranges_are_reported_and_not_written(dtype):
+    q, k, v = make([40, 50, 30], 4, 2, 64, dtype, 12)
+    good = torch.zeros(q.shape, dtype=dtype, device=DEV)
+    pkv.prompt_attn(q, k, v, starts([40, 50, 30]), 0.1, good)
+
+    def run(qs, **kw):
+        out = torch.full(q.shape, 7.0, dtype=dtype, device=DEV)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        pkv.prompt_attn(q, k, v, torch.tensor(qs, dtype=torch.int32, device=DEV), 0.1, out,
+                        status=status, **kw)
+        return out, int(status)
+
+    out, st = run([0, 40, 90, 121])               # past the rows
+    assert st == 4 and torch.equal(out[:90], good[:90]) and bool((out[90:] == 7).all())
+    out, st = run([0, 40, 30, 30])                # decreasing
+    assert st == 4 and torch.equal(out[:40], good[:40]) and bool((out[40:] == 7).all())
+    out, st = run([-1, 40, 90, 120])              # before the rows
+    assert st == 4 and bool((out[:40] == 7).all()) and torch.equal(out[40:], good[40:])
+    out, st = run([0, 40, 90, 120], max_q_len=45)  # longer than promised
+    assert st == 4 and bool((out[40:90] == 7).all())
+    assert torch.equal(out[:40], good[:40]) and torch.equal(out[90:], good[90:])
+    out, st = run([0, 0, 0, 0])
+    assert st == 0 and bool((out == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_no_rows(dtype):
+    e = torch.empty((0, 4, 64), dtype=dtype, device=DEV)
+    out = pkv.prompt_attn(e, e, e, torch.zeros(3, dtype=torch.int32, device=DEV), 0.1, e.clone())
+    assert out.shape == (0, 4, 64)
+    q, k, v = make([5], 4, 2, 64, dtype, 1)
+    out = torch.full(q.shape, 7.0, dtype=dtype, device=DEV)
+    pkv.prompt_attn(q, k, v, torch.zeros(1, dtype=torch.int32, device=DEV), 0.1, out)
+    assert bool((out == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_bits_do_not_change(dtype):
+    # Twice, beside other sequences, and with more room in max_q_len: the same bits.
+    lens = [200, 333]
+    q, k, v = make(lens, 16, 2, 128, dtype, 13)
+    a, b, c = (torch.zeros(q.shape, dtype=dtype, device=DEV) for _ in range(3))
+    pkv.prompt_attn(q, k, v, starts(lens), 0.1, a)
+    pkv.prompt_attn(q, k, v, starts(lens), 0.1, b, max_q_len=333)
+    pkv.prompt_attn(q, k, v, starts([200]), 0.1, c, max_q_len=200)
+    assert torch.equal(a, b) and torch.equal(a[:200], c[:200])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_streams_and_graphs(dtype):
+    lens = [90, 200, 1]
+    q, k, v = make(lens, 8, 2, 128, dtype, 14, fused=False)
+    want = torch.zeros(q.shape, dtype=dtype, device=DEV)
+    pkv.prompt_attn(q, k, v, starts(lens), 0.1, want)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = torch.zeros_like(want)
+    qs = starts(lens)
+    torch.cuda.synchronize()
+    pkv.prompt_attn(q, k, v, qs, 0.1, got, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    # One graph, replayed over other lengths and other values in the same buffers; a
+    # second graph beside it.
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    o1, o2 = torch.zeros_like(want), torch.zeros_like(want)
+    with torch.cuda.graph(g1):
+        pkv.prompt_attn(q, k, v, qs, 0.1, o1)
+    with torch.cuda.graph(g2):
+        pkv.prompt_attn(q, k, v, qs, 0.1, o2)
+    side = torch.cuda.Stream()
+    for new in ([90, 200, 1], [1, 289, 1], [0, 0, 291]):
+        qs.copy_(starts(new))
+        k.mul_(0.5)
+        pkv.prompt_attn(q, k, v, qs, 0.1, want)
+        side.wait_stream(torch.cuda.current_stream())
+        g1.replay()
+        with torch.cuda.stream(side):
+            g2.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o1, want) and torch.equal(o2, want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_offsets_past_32_bits(dtype):
+    # Rows 2^18 elements apart: the last ones lie past 2^31 elements (2^32 bytes).
+    T, Hq, Hkv, D, stride = 8300, 4, 2, 64, 1 << 18
+    buf = torch.empty((T, stride), dtype=dtype, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    small = torch.randn((T, Hq + 2 * Hkv, D), generator=g, device=DEV).to(dtype)
+    n = (Hq + 2 * Hkv) * D
+    buf[:, :n] = small.view(T, n)
+    rows = buf[:, :n].view(T, Hq + 2 * Hkv, D)
+    lens = [8000, 250, 50]
+    out = torch.zeros((T, Hq, D), dtype=dtype, device=DEV)
+    pkv.prompt_attn(rows[:, :Hq], rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:], starts(lens), 0.125, out)
+    want = torch.zeros_like(out)
+    c = small.contiguous()
+    pkv.prompt_attn(c[:, :Hq], c[:, Hq:Hq + Hkv], c[:, Hq + Hkv:], starts(lens), 0.125, want)
+    assert torch.equal(out, want)
+    tail = c[8000:]
+    check(tail[:, :Hq], tail[:, Hq:Hq + Hkv], tail[:, Hq + Hkv:], [250, 50], 0.125)
+
+
+def test_many_short_sequences():
+    r = np.random.RandomState(5)
+    lens = [int(x) for x in r.randint(0, 40, 700)]
+    for dtype in (F32, BF16):
+        q, k, v = make(lens, 4, 2, 64, dtype, 15)
+        check(q, k, v, lens, 0.125)
