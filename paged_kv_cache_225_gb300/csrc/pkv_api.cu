@@ -807,7 +807,8 @@ pkv_status pkv_prompt_attn(const void *q, const void *k, const void *v, pkv_dtyp
         return PKV_ERR_UNSUPPORTED;
     if (num_q_heads / num_kv_heads > 16)
         return PKV_ERR_UNSUPPORTED;
-    if (!std::isfinite(scale) || flags != 0)
+    if (!std::isfinite(scale) || (flags & ~PKV_FLAG_TEST_DROP_FIRST_COPY) != 0 ||
+        (flags != 0 && dtype != PKV_BF16))
         return PKV_ERR_INVALID_ARG;
     if (num_seqs == 0 || num_tokens == 0 || max_q_len == 0)
         return PKV_OK;
@@ -846,8 +847,16 @@ pkv_status pkv_prompt_attn(const void *q, const void *k, const void *v, pkv_dtyp
     p.head_dim = head_dim;
     p.group = num_q_heads / num_kv_heads;
     p.max_q_len = max_q_len < num_tokens ? max_q_len : num_tokens;
-    p.score_scale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-    return launch_prompt_simt(p, static_cast<cudaStream_t>(stream));
+    // The kernels work with a positive factor: the sign is applied to Q (or the
+    // score), and a zero becomes a factor too small to tell weights apart, which
+    // keeps masked scores (-inf) out all the same.
+    const float factor = static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634);
+    const float least = std::ldexp(1.0f, -120);
+    p.score_scale = factor > least ? factor : least;
+    p.negate = scale < 0.f ? 1 : 0;
+    p.drop_first_copy = (flags & PKV_FLAG_TEST_DROP_FIRST_COPY) ? 1 : 0;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dtype == PKV_BF16 ? launch_prompt_tc(p, st) : launch_prompt_simt(p, st);
 }
 
 // Sizes that the table calls share.

@@ -116,7 +116,9 @@ struct PromptParams {
     int dtype, out_dtype;
     int num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, group;
     int max_q_len;           // bound on a sequence's rows
-    float score_scale;       // scale * log2(e)
+    float score_scale;       // |scale| * log2(e), at least 2^-120
+    int negate;              // scale < 0: the kernels negate the scores
+    int drop_first_copy;     // test hook: never issue the first copy of CTA 0
 };
 
 // One scheduling step of a page pool kept in device memory.
@@ -179,7 +181,8 @@ pkv_status launch_copy_blocks(void *k_cache, void *v_cache, size_t block_bytes,
                               const int32_t *pairs, int num_pairs, int num_blocks,
                               int32_t *status, cudaStream_t stream);
 
-pkv_status launch_prompt_simt(const PromptParams &p, cudaStream_t stream);
+pkv_status launch_prompt_simt(const PromptParams &p, cudaStream_t stream);  // fp32
+pkv_status launch_prompt_tc(const PromptParams &p, cudaStream_t stream);    // bf16
 pkv_status launch_tables_step(const TablesParams &p, cudaStream_t stream);
 pkv_status launch_tables_fork(const int32_t *pairs, int num_pairs, int32_t *seq_lens,
                               int32_t *block_tables, int32_t *ref_counts, int num_seqs,

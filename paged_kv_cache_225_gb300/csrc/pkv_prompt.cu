@@ -1,4 +1,4 @@
-// Causal attention over whole prompts on the CUDA cores.
+// Causal attention over whole fp32 prompts on the CUDA cores.
 //
 // softmax(scale * q K^T) V of the "Inference optimization" lesson (Step 2,
 // scaled_dot_product_attention with its causal mask) for every sequence of a
@@ -12,7 +12,6 @@
 // A CTA holds 64 rows (token, grouped head) and walks 64 keys at a time, all
 // operands in shared memory as f32; a thread owns 8 rows x 4 keys of the
 // scores and 8 rows x D / 16 columns of the output.
-#include "pkv_convert.cuh"
 #include "pkv_prompt.cuh"
 
 namespace pkv {
@@ -30,14 +29,9 @@ template <int D> struct SimtGeom {
     static constexpr int kSmem = kFloats * 4;
 };
 
-// Four consecutive elements of a row as f32.
-__device__ __forceinline__ float4 load4(const void *base, int dtype, size_t off)
+__device__ __forceinline__ float4 load4(const void *base, size_t off)
 {
-    if (dtype == PKV_F32)
-        return __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off));
-    const uint2 w =
-        __ldg(reinterpret_cast<const uint2 *>(static_cast<const unsigned short *>(base) + off));
-    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+    return __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off));
 }
 
 template <int D>
@@ -52,7 +46,6 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = p.group;
     const int tokens = kRows / G;  // tokens per item
-    const int rows = tokens * G;
     if (warp == 0) {
         PromptScan scan;
         scan.init(p, tokens, lane, blockIdx.x == 0);
@@ -72,7 +65,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
         const int r = e / (D / 4), c = 4 * (e % (D / 4));
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < nt * G)
-            v = load4(p.q, p.dtype,
+            v = load4(p.q,
                       (static_cast<size_t>(it.row0) + t0 + r / G) * p.q_stride +
                           static_cast<size_t>(it.hkv * G + r % G) * D + c);
         *reinterpret_cast<float4 *>(sq + r * kLd + c) = v;
@@ -99,8 +92,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
             if (k0 + r < end) {
                 const size_t tok = static_cast<size_t>(it.row0) + k0 + r;
                 const size_t col = static_cast<size_t>(it.hkv) * D + c;
-                kk = load4(p.k, p.dtype, tok * p.k_stride + col);
-                vv = load4(p.v, p.dtype, tok * p.v_stride + col);
+                kk = load4(p.k, tok * p.k_stride + col);
+                vv = load4(p.v, tok * p.v_stride + col);
             }
             *reinterpret_cast<float4 *>(sk + r * kLd + c) = kk;
             *reinterpret_cast<float4 *>(sv + r * D + c) = vv;
@@ -126,6 +119,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
                     x[i][j] = fmaf(qf.x, kf[j].x, fmaf(qf.y, kf[j].y, fmaf(qf.z, kf[j].z, fmaf(qf.w, kf[j].w, x[i][j]))));
             }
         }
+        const float c = p.negate ? -p.score_scale : p.score_scale;
         const bool masked = k0 + kKeys > t0 + 1;  // some row does not see some key
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -133,7 +127,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const bool seen = k0 + tx + 16 * j <= pos[i];
-                x[i][j] = seen ? x[i][j] * p.score_scale : -INFINITY;
+                x[i][j] = seen ? x[i][j] * c : -INFINITY;
                 mx = fmaxf(mx, x[i][j]);
             }
 #pragma unroll
@@ -233,7 +227,6 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
             }
         }
     }
-    (void)rows;
 }
 
 template <int D> pkv_status launch_simt_d(const PromptParams &p, cudaStream_t stream)
@@ -249,13 +242,7 @@ template <int D> pkv_status launch_simt_d(const PromptParams &p, cudaStream_t st
     });
     if (rc != PKV_OK)
         return rc;
-    // At most T / tokens + S items per KV head.
-    const long tokens = kRows / p.group;
-    const long per_seq = (static_cast<long>(p.max_q_len) + tokens - 1) / tokens;
-    long items = static_cast<long>(p.num_tokens) / tokens + p.num_seqs;
-    if (items > per_seq * p.num_seqs)
-        items = per_seq * p.num_seqs;
-    items *= p.num_kv_heads;
+    const long items = prompt_max_items(p, kRows / p.group);
     if (items <= 0)
         return PKV_OK;
     if (items > 0x7fffffffL)

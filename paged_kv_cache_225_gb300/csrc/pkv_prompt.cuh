@@ -31,6 +31,15 @@ __device__ __forceinline__ int prompt_len(const PromptParams &p, int s, int &sta
     return ok ? end - start : 0;
 }
 
+// Items there can be at most (host): every sequence's tokens / `tokens` and one
+// more, or the longest's for each of them.
+inline long prompt_max_items(const PromptParams &p, long tokens)
+{
+    const long per_seq = (static_cast<long>(p.max_q_len) + tokens - 1) / tokens;
+    const long a = static_cast<long>(p.num_tokens) / tokens + p.num_seqs, b = per_seq * p.num_seqs;
+    return (a < b ? a : b) * p.num_kv_heads;
+}
+
 // One warp looks items up by number.  With P_s items in sequence s, the items
 // of index >= i number C(i) = sum_s max(0, P_s - i) per KV head, so item
 // number u has the largest index i with C(i) > u / num_kv_heads: a binary search.

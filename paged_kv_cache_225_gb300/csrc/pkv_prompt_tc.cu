@@ -1,0 +1,802 @@
+// Causal attention over whole prompts on the tcgen05 tensor cores (bf16).
+//
+// softmax(scale * q K^T) V of the "Inference optimization" lesson (Step 2,
+// scaled_dot_product_attention with its causal mask), one pass over the keys
+// with the running maximum and sum of the softmax.  A row is one (token,
+// grouped query head) pair; the G heads of a group read the same K and V.
+//
+// Layout on the GPU:
+//  * A tile is 128 rows: R = 128 / G consecutive tokens (rounded down) with
+//    their G heads.  An item is two neighbouring tiles of one sequence and KV
+//    head: every K and V block of 128 keys that reaches shared memory serves
+//    256 rows.  One persistent CTA per SM walks the items, costliest first,
+//    in alternating direction, so that the CTAs' totals stay even.
+//  * Ten warps: 0-3 own the rows of tile 0 (a thread per row, which is its
+//    TMEM lane), 4-7 those of tile 1, warp 8 looks items up and issues the TMA
+//    loads, one thread of warp 9 issues the MMAs.
+//  * TMEM: scores of both tiles (2 x 128 columns, P written back over them as
+//    bf16) and both outputs (2 x head_dim columns).  Per block and tile:
+//    S = Q K^T from shared memory; the rows' threads read S, apply the limit
+//    and the softmax and write P; O += P V with P read from TMEM.  While one
+//    tile's threads work, the tensor cores run the other tile's products.
+//  * All shared-memory operands are in the 128-byte swizzle mode: [128 rows]
+//    [64 elements] per half of head_dim, K-major for Q and K, MN-major for V.
+//  * The last block of an item is cut to its keys in steps of 16 (N of S, K of
+//    P V).
+//  * The running maximum is raised only when a score exceeds it by 2^8; O is
+//    then rescaled in TMEM by the rows' threads.
+//  * P V multiplies a masked weight 0 with the V rows of later tokens in the
+//    diagonal block, which may hold infinities or NaN.  Rows past the item's
+//    keys are zeroed in shared memory; a row whose output is not finite is
+//    computed again from global memory over its own keys when a V row that it
+//    must not see is not finite (redo_rows).
+//  * Every wait is bounded; a timeout records PKV_ERR_TIMEOUT, stops every role,
+//    lets copies and MMAs in flight finish and frees TMEM.
+#include <climits>
+
+#include "pkv_prompt.cuh"
+#include "pkv_tc.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kM = 128;     // rows of a tile
+constexpr int kKeys = 128;  // keys of a block
+constexpr int kThreads = 320;
+constexpr int kTileWarps = 4;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kQueue = 4;
+constexpr int kHalf = 128 * 128;  // bytes of [128 rows][64 bf16]
+
+template <int D> struct PtGeom {
+    static constexpr int kTile = D / 64 * kHalf;
+    static constexpr int NS = D == 128 ? 5 : 8;   // K / V tiles in the ring
+    static constexpr int kSmem = (2 + NS) * kTile + 1024;
+    static constexpr int kOCol = 2 * kKeys;       // outputs follow the scores
+    static_assert(kOCol + 2 * D <= 512, "scores and outputs fill TMEM");
+};
+
+struct PromptMaps {
+    CUtensorMap q, k, v;
+};
+
+// One queue entry: an item, or s < 0 for the end of the work.
+struct PtItem {
+    int s, hkv, row0, n, tok0;
+    int nt[2];   // tokens of the two tiles
+    int end[2];  // keys a tile sees
+    int nb[2];   // its blocks
+    int blocks;  // blocks loaded
+
+    __device__ __forceinline__ void fill(const int *w, int R)
+    {
+        s = w[0];
+        hkv = w[1];
+        row0 = w[2];
+        n = w[3];
+        tok0 = w[4];
+        nt[0] = min(R, n - tok0);
+        nt[1] = max(0, min(R, n - tok0 - R));
+        end[0] = tok0 + nt[0];
+        end[1] = end[0] + nt[1];
+        nb[0] = (end[0] + kKeys - 1) / kKeys;
+        nb[1] = nt[1] > 0 ? (end[1] + kKeys - 1) / kKeys : 0;
+        blocks = max(nb[0], nb[1]);
+    }
+    // Keys of block j that tile t multiplies, in steps of 16.
+    __device__ __forceinline__ int cols(int t, int j) const
+    {
+        return j + 1 < nb[t] ? kKeys : (end[t] - j * kKeys + 15) & ~15;
+    }
+};
+
+// Shared-memory descriptor of a 128-byte-swizzled operand: atoms of 8 rows x
+// 128 bytes; lbo: distance of atoms along the contiguous axis (MN-major only),
+// sbo: distance of 8-row groups; descriptor version 1, layout code 2.
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo)
+{
+    uint64_t d = static_cast<uint64_t>((addr >> 4) & 0x3fffu);
+    d |= static_cast<uint64_t>((lbo >> 4) & 0x3fffu) << 16;
+    d |= static_cast<uint64_t>((sbo >> 4) & 0x3fffu) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                          bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u));
+}
+
+// 32 columns of the warp's 32 lanes; valid after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v)
+{
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        v[i] = __uint_as_float(r[i]);
+}
+
+// Waits for the loads above and ties the values to the wait: nothing that
+// uses them can be scheduled before it.
+template <int N> __device__ __forceinline__ void tmem_wait_ld(float (&v)[N])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("" : "+f"(v[i]));
+}
+
+// Two f32 fused multiply-adds / adds in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t x, y, z, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    float2 o;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+    return o;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    uint64_t x, y, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    float2 o;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+    return o;
+}
+
+__device__ __forceinline__ void store_out8(const PromptParams &p, size_t off, const float *v)
+{
+    if (p.out_dtype == PKV_F32) {
+        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + off);
+        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        uint4 w;
+        w.x = pack_bf16(v[0], v[1]);
+        w.y = pack_bf16(v[2], v[3]);
+        w.z = pack_bf16(v[4], v[5]);
+        w.w = pack_bf16(v[6], v[7]);
+        *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(p.out) + off) = w;
+    }
+}
+
+// The rows of a warp that came out infinite or NaN (lane mask `rows`, lane i
+// owning row r0 + i of the tile).  A row is computed again over the keys it
+// sees if a V row after them, before `key_end`, the end of the keys the MMAs
+// multiplied, is not finite; with P in two parts also if a V row that it sees
+// holds an infinity (a part that is zero or negative turns it into NaN).  Keys
+// on the lanes for the scores, dims on the lanes for the sums.  Rare, so kept
+// out of line.
+template <int D, bool kSplit>
+__device__ __noinline__ void redo_rows(const PromptParams &p, unsigned rows, int r0, int tok, int row0,
+                                       int hkv, int key_end, int lane)
+{
+    constexpr int kPer = D / 32;  // dims per lane
+    const int G = p.group;
+    const unsigned short *kb = static_cast<const unsigned short *>(p.k) +
+                               static_cast<size_t>(row0) * p.k_stride + hkv * D;
+    const unsigned short *vb = static_cast<const unsigned short *>(p.v) +
+                               static_cast<size_t>(row0) * p.v_stride + hkv * D;
+    const int first = tok + (r0 + __ffs(rows) - 1) / G;  // earliest token among the rows
+    int last_bad = -1, first_inf = INT_MAX;
+    for (int j = kSplit ? 0 : first + 1; j < key_end; ++j) {
+        bool bad = false, inf = false;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const unsigned w = vb[j * p.v_stride + lane * kPer + e] & 0x7fffu;
+            bad = bad || w >= 0x7f80u;
+            inf = inf || w == 0x7f80u;
+        }
+        if (__any_sync(kFullMask, bad))
+            last_bad = j;
+        if (kSplit && first_inf == INT_MAX && __any_sync(kFullMask, inf))
+            first_inf = j;
+    }
+    for (; rows; rows &= rows - 1) {
+        const int r = r0 + __ffs(rows) - 1;
+        const int pos = tok + r / G;
+        if (pos >= last_bad && pos < first_inf)
+            continue;  // no product went wrong: the row stands
+        const size_t head = hkv * G + r % G;
+        const unsigned short *q = static_cast<const unsigned short *>(p.q) +
+                                  static_cast<size_t>(row0 + pos) * p.q_stride + head * D;
+        float m = -INFINITY, l = 0.f, o[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+            o[e] = 0.f;
+        for (int j0 = 0; j0 <= pos; j0 += 32) {
+            const int j = j0 + lane;
+            float x = -INFINITY;
+            if (j <= pos) {
+                const uint4 *kr = reinterpret_cast<const uint4 *>(kb + j * p.k_stride);
+                const uint4 *qr = reinterpret_cast<const uint4 *>(q);
+                float a = 0.f;
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 kw = __ldg(kr + c), qw = __ldg(qr + c);
+                    const uint32_t kk[4] = {kw.x, kw.y, kw.z, kw.w}, qq[4] = {qw.x, qw.y, qw.z, qw.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        a = fmaf(bf16_lo(qq[e]), bf16_lo(kk[e]), fmaf(bf16_hi(qq[e]), bf16_hi(kk[e]), a));
+                }
+                x = a * (p.negate ? -p.score_scale : p.score_scale);
+            }
+            float mx = x;
+#pragma unroll
+            for (int w = 16; w >= 1; w >>= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, w));
+            const float mn = fmaxf(m, mx);
+            const float off = mn == -INFINITY ? 0.f : mn;
+            const float alpha = MmaSoftmax::ex2(m - off);
+            const float wgt = j <= pos ? MmaSoftmax::ex2(x - off) : 0.f;
+            m = mn;
+            l = l * alpha + wgt;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+                o[e] *= alpha;
+            const int cnt = min(32, pos + 1 - j0);
+            for (int i = 0; i < cnt; ++i) {
+                const float w = __shfl_sync(kFullMask, wgt, i);
+                const unsigned short *vr = vb + (j0 + i) * p.v_stride + lane * kPer;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    o[e] = fmaf(w, __uint_as_float(static_cast<uint32_t>(vr[e]) << 16), o[e]);
+            }
+        }
+#pragma unroll
+        for (int w = 16; w >= 1; w >>= 1)
+            l += __shfl_xor_sync(kFullMask, l, w);
+        const size_t off = (static_cast<size_t>(row0 + pos) * p.num_q_heads + head) * D + lane * kPer;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const float y = o[e] / l;
+            if (p.out_dtype == PKV_F32)
+                static_cast<float *>(p.out)[off + e] = y;
+            else
+                static_cast<__nv_bfloat16 *>(p.out)[off + e] = __float2bfloat16(y);
+        }
+    }
+}
+
+template <int D, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_tc_kernel(const PromptParams p, const __grid_constant__ PromptMaps maps)
+{
+    using Geo = PtGeom<D>;
+    constexpr int NS = Geo::NS;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) uint64_t full[NS], empty[NS];
+    __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_free[2];
+    __shared__ __align__(8) uint64_t item_full[kQueue], item_empty[kQueue], drain;
+    __shared__ int s_item[kQueue][5];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    volatile int *abort = &s_abort;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t smem0 = (raw + 1023u) & ~1023u;
+    unsigned char *smem = smem_raw + (smem0 - raw);
+    const int G = p.group;
+    const int R = kM / G;  // tokens of a tile
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&q_full[t], 1);
+            mbar_init(&q_empty[t], 1);
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], kTileWarps);
+            mbar_init(&pv_done[t], 1);
+            mbar_init(&o_free[t], kTileWarps);
+        }
+        for (int i = 0; i < kQueue; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], 2 * kTileWarps + 1);
+        }
+        mbar_init(&drain, 1);
+        s_abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&s_tmem)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // Q rows past G * R are never loaded: zero.
+    for (int e = threadIdx.x; e < 2 * (D / 64) * (kM - G * R) * 8; e += kThreads) {
+        const int per = (kM - G * R) * 8;  // 16-byte pieces of one half
+        *reinterpret_cast<uint4 *>(smem + (e / per) * kHalf + (G * R * 8 + e % per) * 16) =
+            make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const uint32_t ring0 = smem0 + 2 * Geo::kTile;
+
+    if (warp == kProducerWarp) {
+        // ------------------------------------------------------- producer
+        PromptScan scan;
+        scan.init(p, 2 * R, lane, blockIdx.x == 0);
+        uint32_t kv = 0;        // tiles issued
+        uint32_t qn[2] = {0, 0};  // Q tiles issued
+        bool ok = true;
+        for (unsigned k = 0; ok; ++k) {
+            const unsigned u = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            const PromptItem found = scan.find(p, 2 * R, u, lane);
+            if (lane == 0) {
+                const int slot = k % kQueue;
+                if (k >= kQueue)
+                    ok = tc_wait(&item_empty[slot], ((k / kQueue) - 1) & 1, abort);
+                if (ok) {
+                    int *w = s_item[slot];
+                    w[0] = found.s;
+                    w[1] = found.hkv;
+                    w[2] = found.row0;
+                    w[3] = found.n;
+                    w[4] = found.index * 2 * R;
+                    mbar_arrive(&item_full[slot]);
+                }
+                if (ok && found.s >= 0) {
+                    PtItem it;
+                    it.fill(s_item[slot], R);
+                    auto load = [&](const CUtensorMap *map, int j) {
+                        const uint32_t st = kv % NS;
+                        if (kv >= NS && !tc_wait(&empty[st], ((kv / NS) - 1) & 1, abort))
+                            return false;
+                        mbar_arrive_expect_tx(&full[st], Geo::kTile);
+                        for (int h = 0; h < D / 64; ++h) {
+                            if (p.drop_first_copy && blockIdx.x == 0 && kv == 0 && h == 0)
+                                continue;
+                            tma_load_3d(smem + (2 * Geo::kTile + st * Geo::kTile + h * kHalf), map,
+                                        64 * h, it.hkv, it.row0 + j * kKeys, &full[st]);
+                        }
+                        ++kv;
+                        return true;
+                    };
+                    for (int j = 0; j < it.blocks && ok; ++j) {
+                        ok = load(&maps.k, j);
+                        for (int t = 0; t < 2 && j == 0 && ok; ++t) {
+                            if (it.nt[t] == 0)
+                                continue;
+                            if (qn[t] > 0)
+                                ok = tc_wait(&q_empty[t], (qn[t] - 1) & 1, abort);
+                            if (!ok)
+                                break;
+                            mbar_arrive_expect_tx(&q_full[t], (D / 64) * G * R * 128);
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_load_3d(smem + t * Geo::kTile + h * kHalf, &maps.q, 64 * h,
+                                            it.hkv * G, it.row0 + it.tok0 + t * R, &q_full[t]);
+                            ++qn[t];
+                        }
+                        ok = ok && load(&maps.v, j);
+                    }
+                }
+                if (!ok) {
+                    set_status(p.status, PKV_ERR_TIMEOUT);
+                    *abort = 1;
+                }
+            }
+            ok = __shfl_sync(kFullMask, ok ? 1 : 0, 0) != 0;
+            if (found.s < 0)
+                break;
+        }
+        __syncwarp();
+        if (lane == 0 && *abort) {
+            // Let every copy still in flight land before the CTA exits.
+            for (uint32_t c = kv > NS ? kv - NS : 0; c < kv; ++c)
+                mbar_wait_bounded(&full[c % NS], (c / NS) & 1, kWaitLimitNs);
+            for (int t = 0; t < 2; ++t)
+                if (qn[t] > 0)
+                    mbar_wait_bounded(&q_full[t], (qn[t] - 1) & 1, kWaitLimitNs);
+        }
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------- MMA issue
+        if (lane == 0) {
+            // A negative scale negates Q (instruction descriptor bit 13).
+            const uint32_t id_s0 = tc_idesc(kM, 0, false) | (p.negate ? 1u << 13 : 0u);
+            constexpr uint32_t kIdPV = tc_idesc(kM, D, true);
+            uint32_t q_cnt[2] = {0, 0}, p_cnt[2] = {0, 0}, o_cnt[2] = {0, 0};
+            uint32_t base = 0;  // ring index of the current item's first K tile
+            unsigned k = 0;
+            auto next_item = [&](PtItem &it) -> int {  // 1 item, 0 end, -1 failure
+                const int slot = k % kQueue;
+                if (!tc_wait(&item_full[slot], (k / kQueue) & 1, abort))
+                    return -1;
+                it.fill(s_item[slot], R);
+                mbar_arrive(&item_empty[slot]);
+                ++k;
+                return it.s >= 0 ? 1 : 0;
+            };
+            auto qk = [&](int t, const PtItem &it, int j, uint32_t b) -> bool {
+                if (j == 0) {
+                    if (!tc_wait(&q_full[t], q_cnt[t] & 1, abort))
+                        return false;
+                    ++q_cnt[t];
+                }
+                const uint32_t c = b + 2 * j, st = c % NS;
+                if (!tc_wait(&full[st], (c / NS) & 1, abort))
+                    return false;
+                tc_fence_after();
+                const uint32_t id = id_s0 | (static_cast<uint32_t>(it.cols(t, j) >> 3) << 17);
+                const uint64_t qd = smem_desc_sw128(smem0 + t * Geo::kTile, 16, 1024);
+                const uint64_t kd = smem_desc_sw128(ring0 + st * Geo::kTile, 16, 1024);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t o = ((ks / 4) * kHalf + (ks % 4) * 32) >> 4;
+                    tc_mma_ss(tmem + t * kKeys, qd + o, kd + o, id, ks > 0);
+                }
+                tc_commit(&s_full[t]);
+                if (j + 1 == it.nb[t])
+                    tc_commit(&q_empty[t]);
+                return true;
+            };
+            auto pv = [&](int t, const PtItem &it, int j, uint32_t b) -> bool {
+                if (!tc_wait(&p_full[t], p_cnt[t] & 1, abort))
+                    return false;
+                ++p_cnt[t];
+                if (j == 0) {
+                    if (o_cnt[t] > 0 && !tc_wait(&o_free[t], (o_cnt[t] - 1) & 1, abort))
+                        return false;
+                    ++o_cnt[t];
+                }
+                const uint32_t c = b + 2 * j + 1, st = c % NS;
+                if (!tc_wait(&full[st], (c / NS) & 1, abort))
+                    return false;
+                tc_fence_after();
+                const uint64_t vd = smem_desc_sw128(ring0 + st * Geo::kTile, kHalf, 1024);
+                const int steps = it.cols(t, j) >> 4;
+                const uint32_t pcol = tmem + t * kKeys, ocol = tmem + Geo::kOCol + t * D;
+                for (int ks = 0; ks < steps; ++ks)
+                    tc_mma_ta(ocol, pcol + 8 * ks, vd + ks * (2048 >> 4), kIdPV, j > 0 || ks > 0);
+                if constexpr (kSplit)
+                    for (int ks = 0; ks < steps; ++ks)
+                        tc_mma_ta(ocol, pcol + 64 + 8 * ks, vd + ks * (2048 >> 4), kIdPV, true);
+                tc_commit(&pv_done[t]);
+                return true;
+            };
+            auto release = [&](uint32_t c) { tc_commit(&empty[c % NS]); };
+
+            PtItem cur, nxt;
+            int have = next_item(cur);
+            bool failed = have < 0;
+            if (have > 0) {
+                failed = !qk(0, cur, 0, base) || (cur.nb[1] > 0 && !qk(1, cur, 0, base));
+                if (!failed)
+                    release(base);
+            }
+            while (have > 0 && !failed) {
+                const uint32_t nbase = base + 2 * cur.blocks;
+                int have_next = 0;
+                for (int j = 0; j < cur.blocks; ++j) {
+                    if (j < cur.nb[0]) {
+                        failed = !pv(0, cur, j, base) ||
+                                 (j + 1 < cur.nb[0] && !qk(0, cur, j + 1, base));
+                        if (failed)
+                            break;
+                    }
+                    if (j + 1 == cur.blocks) {
+                        // The next item's first scores of tile 0, so that its
+                        // threads find them when their output is written.
+                        have_next = next_item(nxt);
+                        failed = have_next < 0 || (have_next > 0 && !qk(0, nxt, 0, nbase));
+                        if (failed)
+                            break;
+                    }
+                    if (j < cur.nb[1]) {
+                        failed = !pv(1, cur, j, base);
+                        if (failed)
+                            break;
+                    }
+                    release(base + 2 * j + 1);
+                    if (j + 1 < cur.blocks) {
+                        failed = j + 1 < cur.nb[1] && !qk(1, cur, j + 1, base);
+                        if (failed)
+                            break;
+                        release(base + 2 * (j + 1));
+                    }
+                }
+                if (failed)
+                    break;
+                if (have_next > 0) {
+                    failed = nxt.nb[1] > 0 && !qk(1, nxt, 0, nbase);
+                    if (failed)
+                        break;
+                    release(nbase);
+                }
+                cur = nxt;
+                base = nbase;
+                have = have_next;
+            }
+            if (failed) {
+                set_status(p.status, PKV_ERR_TIMEOUT);
+                *abort = 1;
+            }
+            // Every MMA issued has completed before TMEM is freed.
+            tc_commit(&drain);
+            mbar_wait_bounded(&drain, 0, kWaitLimitNs);
+        }
+        __syncwarp();
+    } else if (warp < 2 * kTileWarps) {
+        // ------------------------------------------- softmax and output
+        const int t = warp >> 2;                // tile
+        const int r = threadIdx.x & (kM - 1);   // row of the tile = TMEM lane
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t scol = tmem + lanes + t * kKeys;
+        const uint32_t ocol = tmem + lanes + Geo::kOCol + t * D;
+        const float c = p.score_scale;  // positive
+        constexpr float kLazy = MmaSoftmax::kLazy;
+        uint32_t cnt = 0;   // blocks of this tile
+        uint32_t base = 0;  // ring index of the item's first K tile
+        bool failed = false;
+        for (unsigned k = 0; !failed; ++k) {
+            const int slot = k % kQueue;
+            if (!warp_wait(&item_full[slot], (k / kQueue) & 1, abort)) {
+                failed = true;
+                break;
+            }
+            PtItem it;
+            it.fill(s_item[slot], R);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&item_empty[slot]);
+            if (it.s < 0)
+                break;
+            const int nt = it.nt[t], nb = it.nb[t];
+            const int first = it.tok0 + t * R;  // token of row 0
+            const int pos = first + min(r / G, nt - 1);
+            float m = -INFINITY;                // running maximum, log2 units
+            float2 l2 = make_float2(0.f, 0.f);  // its sum, in two halves
+            for (int j = 0; j < nb; ++j, ++cnt) {
+                const int cols = it.cols(t, j);
+                const int tb = j * kKeys;
+                if (!warp_wait(&s_full[t], cnt & 1, abort)) {
+                    failed = true;
+                    break;
+                }
+                tc_fence_after();
+                float x[kKeys];
+                const bool whole = tb + kKeys <= first + 1;  // every row sees every key
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4)
+                    if (32 * q4 < cols)
+                        tmem_ld32(scol + 32 * q4, x + 32 * q4);
+                tmem_wait_ld(x);
+                if (!whole) {
+                    const int lim = pos - tb + 1;
+#pragma unroll
+                    for (int e = 0; e < kKeys; ++e)
+                        x[e] = e < lim ? x[e] : -INFINITY;
+                }
+                float mx;
+                {
+                    float a[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        a[e] = x[e];
+#pragma unroll
+                    for (int e = 8; e < kKeys; e += 16)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            a[i] = e + 8 + i < kKeys ? fmaxf(a[i], fmaxf(x[e + i], x[(e + 8 + i) % kKeys]))
+                                                     : fmaxf(a[i], x[e + i]);
+                    mx = fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])),
+                               fmaxf(fmaxf(a[4], a[5]), fmaxf(a[6], a[7]))) * c;
+                }
+                const bool need = mx > m + kLazy;  // false when nothing is visible
+                float alpha = 1.f;
+                if (need) {
+                    alpha = m == -INFINITY ? 0.f : MmaSoftmax::ex2(m - mx);
+                    l2.x *= alpha;
+                    l2.y *= alpha;
+                    m = mx;
+                }
+                if (j > 0 && __any_sync(kFullMask, need)) {
+                    // O holds earlier blocks: rescale it once their P V is done.
+                    if (!warp_wait(&pv_done[t], (cnt - 1) & 1, abort)) {
+                        failed = true;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                        float ov[16];
+                        tmem_ld16(ocol + c0, ov);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            ov[e] *= alpha;
+                        tmem_st16(ocol + c0, ov);
+                    }
+                    tmem_wait_st();
+                }
+                // Weights 2^(c x - m); a row of nothing but -inf so far has
+                // weights 0.
+                const float off = m == -INFINITY ? 0.f : -m;
+                const float2 c2 = make_float2(c, c), off2 = make_float2(off, off);
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    if (32 * q4 >= cols)
+                        break;
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 y = fma2(make_float2(x[32 * q4 + e], x[32 * q4 + e + 1]), c2, off2);
+                        const float2 w = make_float2(MmaSoftmax::ex2(y.x), MmaSoftmax::ex2(y.y));
+                        l2 = add2(l2, w);
+                        hi[e / 2] = pack_bf16(w.x, w.y);
+                        if constexpr (kSplit)
+                            lo[e / 2] = pack_bf16(w.x - bf16_lo(hi[e / 2]), w.y - bf16_hi(hi[e / 2]));
+                    }
+                    tmem_st16u(scol + 16 * q4, hi);
+                    if constexpr (kSplit)
+                        tmem_st16u(scol + 64 + 16 * q4, lo);
+                }
+                tmem_wait_st();
+                // V rows past the item's keys may hold anything.
+                const int zero0 = max(it.end[0], it.end[1]) - tb;
+                if (zero0 < cols) {
+                    const uint32_t vc = base + 2 * j + 1;
+                    if (!warp_wait(&full[vc % NS], (vc / NS) & 1, abort)) {
+                        failed = true;
+                        break;
+                    }
+                    unsigned char *vt = smem + (2 + vc % NS) * Geo::kTile;
+                    for (int e = r; e < (cols - zero0) * (D / 8); e += kM) {
+                        const int row = zero0 + e / (D / 8), piece = e % (D / 8);
+                        *reinterpret_cast<uint4 *>(vt + (piece >> 3) * kHalf + row * 128 +
+                                                   (piece & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&p_full[t]);
+            }
+            base += 2 * it.blocks;
+            if (failed)
+                break;
+            if (nb == 0)
+                continue;
+
+            // ------------------------------------------------ output rows
+            if (!warp_wait(&pv_done[t], (cnt - 1) & 1, abort)) {
+                failed = true;
+                break;
+            }
+            tc_fence_after();
+            const bool live = r < nt * G;
+            const float inv = 1.f / (l2.x + l2.y);
+            const size_t orow = (static_cast<size_t>(it.row0 + pos) * p.num_q_heads + it.hkv * G + r % G) * D;
+            float bad = 0.f;  // NaN once an output is not finite
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                float ov[32];
+                tmem_ld32(ocol + c0, ov);
+                tmem_wait_ld(ov);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    ov[e] *= inv;
+                    bad = fmaf(ov[e], 0.f, bad);
+                }
+                if (live)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        store_out8(p, orow + c0 + e, ov + e);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&o_free[t]);
+            const unsigned redo = __ballot_sync(kFullMask, live && bad != 0.f);
+            if (redo)
+                redo_rows<D, kSplit>(p, redo, 32 * (warp & 3), first, it.row0, it.hkv,
+                             min((nb - 1) * kKeys + it.cols(t, nb - 1), max(it.end[0], it.end[1])), lane);
+        }
+        if (failed && lane == 0) {
+            set_status(p.status, PKV_ERR_TIMEOUT);
+            *abort = 1;
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                     : "memory");
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+// Rows of [num_tokens][heads][D] bf16, `stride` elements apart: boxes of 64
+// elements x `box_heads` heads x `box_tokens` tokens in the 128-byte swizzle mode.
+bool encode_rows(EncodeTiledFn enc, CUtensorMap *map, const void *base, int D, int heads, int64_t tokens,
+                 int64_t stride, int box_heads, int box_tokens)
+{
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads),
+                               static_cast<cuuint32_t>(box_tokens)};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+               es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kSplit> pkv_status launch_ptc(const PromptParams &p, cudaStream_t stream)
+{
+    static ContextCache cache;
+    int set = 0;
+    const pkv_status rc = cache.get(&set, [](int *out) -> pkv_status {
+        *out = 1;
+        return cudaFuncSetAttribute(prompt_tc_kernel<D, kSplit>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    PtGeom<D>::kSmem) == cudaSuccess
+                   ? PKV_OK
+                   : PKV_ERR_CUDA;
+    });
+    if (rc != PKV_OK)
+        return rc;
+    EncodeTiledFn enc = encoder();
+    if (!enc)
+        return PKV_ERR_CUDA;
+    const int R = kM / p.group;
+    PromptMaps maps;
+    if (!encode_rows(enc, &maps.q, p.q, D, p.num_q_heads, p.num_tokens, p.q_stride, p.group, R) ||
+        !encode_rows(enc, &maps.k, p.k, D, p.num_kv_heads, p.num_tokens, p.k_stride, 1, kKeys) ||
+        !encode_rows(enc, &maps.v, p.v, D, p.num_kv_heads, p.num_tokens, p.v_stride, 1, kKeys))
+        return PKV_ERR_CUDA;
+    const long items = prompt_max_items(p, 2 * R);
+    if (items <= 0)
+        return PKV_OK;
+    if (items > 0x40000000L)
+        return PKV_ERR_UNSUPPORTED;
+    const long sms = device_sm_count();
+    const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
+    prompt_tc_kernel<D, kSplit><<<grid, kThreads, PtGeom<D>::kSmem, stream>>>(p, maps);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace
+
+pkv_status launch_prompt_tc(const PromptParams &p, cudaStream_t stream)
+{
+    const bool split = p.out_dtype == PKV_F32;
+    if (p.head_dim == 128)
+        return split ? launch_ptc<128, true>(p, stream) : launch_ptc<128, false>(p, stream);
+    return split ? launch_ptc<64, true>(p, stream) : launch_ptc<64, false>(p, stream);
+}
+
+}  // namespace pkv

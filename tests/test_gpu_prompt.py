@@ -280,3 +280,15 @@ def test_many_short_sequences():
     for dtype in (F32, BF16):
         q, k, v = make(lens, 4, 2, 64, dtype, 15)
         check(q, k, v, lens, 0.125)
+
+
+def test_bounded_wait_reports_timeout_and_recovers():
+    lens = [300, 40]
+    q, k, v = make(lens, 8, 2, 128, BF16, 16)
+    out = torch.zeros(q.shape, dtype=BF16, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkv.prompt_attn(q, k, v, starts(lens), 0.1, out, status=status,
+                    flags=pkv.FLAG_TEST_DROP_FIRST_COPY)
+    torch.cuda.synchronize()
+    assert int(status) == 5  # PKV_ERR_TIMEOUT
+    check(q, k, v, lens, 0.1)

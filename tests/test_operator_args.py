@@ -24,7 +24,7 @@ def prompt(**kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(S=-1), INVALID), (dict(T=-1), INVALID), (dict(Hq=0), INVALID), (dict(Hkv=0), INVALID),
     (dict(Hq=30), INVALID), (dict(maxq=-1), INVALID), (dict(scale=math.nan), INVALID),
-    (dict(scale=math.inf), INVALID), (dict(flags=1), INVALID), (dict(flags=0x200), INVALID),
+    (dict(scale=math.inf), INVALID), (dict(flags=1), INVALID), (dict(flags=0x200), INVALID), (dict(flags=0x100, dtype=pkv.F32), INVALID),
     (dict(dtype=pkv.FP8_E5M2), UNSUPPORTED), (dict(dtype=pkv.INT4), UNSUPPORTED),
     (dict(out_dtype=pkv.FP8_E4M3), UNSUPPORTED), (dict(D=96), UNSUPPORTED), (dict(D=256), UNSUPPORTED),
     (dict(Hq=136, qs=136 * 128), UNSUPPORTED),
