@@ -639,39 +639,53 @@ def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, pairs: torch.Tenso
         raise PkvError(rc, "pkv_copy_blocks")
 
 
-def _launch(dev: torch.device, stream: Optional[torch.cuda.Stream], call) -> int:
-    """``call(stream pointer)`` with ``dev`` as the current device."""
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream belongs to {stream.device}, the tensors to {dev}")
+def _launch(fn, dev: torch.device, stream: Optional[torch.cuda.Stream], args) -> int:
+    """``fn(*args, stream pointer)`` with ``dev`` as the current device."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream belongs to {stream.device}, the tensors to {dev}")
+        s = stream.cuda_stream
+    else:
+        s = torch._C._cuda_getCurrentRawStream(dev.index)
     if torch.cuda.current_device() == dev.index:
-        return call(_stream(dev, stream))
+        return fn(*args, s)
     with torch.cuda.device(dev):
-        return call(_stream(dev, stream))
+        return fn(*args, s)
 
 
-def _check_rows(t: torch.Tensor, what: str, device: torch.device) -> int:
-    """Row stride in elements of a [T, H, D] tensor whose rows are dense."""
+def _ptr(t: Optional[torch.Tensor], what: str, ndim: int, dtype: torch.dtype, index: int):
+    """Address of a contiguous ``ndim``-dimensional CUDA tensor of ``dtype`` on device
+    ``index``, None for None; anything else raises."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == index
+            and t.dim() == ndim and t.is_contiguous()):
+        return t.data_ptr()
+    _check(t, what, ndim, torch.device("cuda", index))
+    raise TypeError(f"{what} must be {str(dtype).replace('torch.', '')}")
+
+
+def _cuda_index(t: torch.Tensor, what: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor (the library has no CPU path)")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, expected {device}")
+    return t.get_device()
+
+
+def _check_rows(t: torch.Tensor, what: str, dtype: torch.dtype, index: int):
+    """(rows, heads, head_dim, row stride in elements) of a tensor whose rows are dense."""
+    if _cuda_index(t, what) != index:
+        raise ValueError(f"{what} is on {t.device}, expected cuda:{index}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {str(dtype).replace('torch.', '')} like q")
     if t.dim() != 3:
         raise ValueError(f"{what} must have 3 dims, got {tuple(t.shape)}")
     T, H, D = t.shape
-    if T > 0 and ((D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D)):
+    row, head, elem = t.stride()
+    if T > 0 and ((D > 1 and elem != 1) or (H > 1 and head != D)):
         raise ValueError(f"{what}: every row must be dense")
-    return t.stride(0) if T > 1 else H * D
-
-
-def _int32(t: Optional[torch.Tensor], what: str, ndim: int, device: torch.device):
-    if t is None:
-        return None
-    _check(t, what, ndim, device)
-    if t.dtype != torch.int32:
-        raise TypeError(f"{what} must be int32")
-    return t.data_ptr()
+    return T, H, D, (row if T > 1 else H * D)
 
 
 def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor,
@@ -687,35 +701,37 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torc
     sequences (default T).  ``status`` (int32 [1], optional) records device-side
     errors.  Returns ``out``.
     """
-    dev = q.device
-    qs, ks, vs = (_check_rows(t, name, dev) for t, name in ((q, "q"), (k, "k"), (v, "v")))
-    _check(out, "out", 3, dev)
-    starts = _int32(q_start, "q_start", 1, dev)
-    st = _int32(status, "status", 1, dev)
-    T, Hq, D = q.shape
-    if k.shape[0] != T or k.shape[2] != D or v.shape != k.shape or out.shape != q.shape:
-        raise ValueError("inconsistent shapes")
-    if q_start.shape[0] < 1 or (status is not None and status.shape[0] < 1):
-        raise ValueError("q_start needs at least one entry, status exactly one")
+    index = _cuda_index(q, "q")
     code = _dtype_code(q, "q")
-    if _dtype_code(k, "k") != code or _dtype_code(v, "v") != code:
-        raise TypeError("q, k and v must have one dtype")
-    rc = _launch(dev, stream, lambda s: lib().pkv_prompt_attn(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), code, qs, ks, vs, starts,
-        q_start.shape[0] - 1, T, Hq, k.shape[1], D, T if max_q_len is None else int(max_q_len),
-        float(scale), out.data_ptr(), _dtype_code(out, "out"), st, int(flags), s))
+    T, Hq, D, qs = _check_rows(q, "q", q.dtype, index)
+    kT, Hkv, kD, ks = _check_rows(k, "k", q.dtype, index)
+    vT, vH, vD, vs = _check_rows(v, "v", q.dtype, index)
+    o = _ptr(out, "out", 3, out.dtype if isinstance(out, torch.Tensor) else q.dtype, index)
+    starts = _ptr(q_start, "q_start", 1, torch.int32, index)
+    st = _ptr(status, "status", 1, torch.int32, index)
+    S = q_start.shape[0] - 1
+    if kT != T or kD != D or (vT, vH, vD) != (kT, Hkv, kD) or out.shape != q.shape:
+        raise ValueError("inconsistent shapes")
+    if S < 0 or (status is not None and status.shape[0] != 1):
+        raise ValueError("q_start needs at least one entry, status exactly one")
+    rc = _launch(lib().pkv_prompt_attn, q.device, stream,
+                 (q.data_ptr(), k.data_ptr(), v.data_ptr(), code, qs, ks, vs, starts, S, T, Hq, Hkv,
+                  D, T if max_q_len is None else int(max_q_len), float(scale), o,
+                  _dtype_code(out, "out"), st, int(flags)))
     if rc != 0:
         raise PkvError(rc, "pkv_prompt_attn")
     return out
 
 
-def _check_pool(seq_lens, block_tables, ref_counts):
-    dev = seq_lens.device
-    ptrs = (_int32(seq_lens, "seq_lens", 1, dev), _int32(block_tables, "block_tables", 2, dev),
-            _int32(ref_counts, "ref_counts", 1, dev))
-    if block_tables.shape[0] != seq_lens.shape[0]:
+def _pool(seq_lens, block_tables, ref_counts):
+    index = _cuda_index(seq_lens, "seq_lens")
+    ptrs = (_ptr(seq_lens, "seq_lens", 1, torch.int32, index),
+            _ptr(block_tables, "block_tables", 2, torch.int32, index),
+            _ptr(ref_counts, "ref_counts", 1, torch.int32, index))
+    S, width = block_tables.shape
+    if S != seq_lens.shape[0]:
         raise ValueError("block_tables needs one row per entry of seq_lens")
-    return dev, ptrs
+    return index, ptrs, S, width
 
 
 def tables_step(seq_lens: torch.Tensor, block_tables: torch.Tensor, ref_counts: torch.Tensor, *,
@@ -736,24 +752,21 @@ def tables_step(seq_lens: torch.Tensor, block_tables: torch.Tensor, ref_counts: 
     slots, then -1) and ``copy_pairs`` int32 [S, 2] ((src, dst) copy-on-write
     pages for ``copy_blocks`` without a status, else -1).  ``status`` int32 [1].
     """
-    dev, (lens, tables, refs) = _check_pool(seq_lens, block_tables, ref_counts)
-    S = seq_lens.shape[0]
-    drop, new = _int32(drop_lens, "drop_lens", 1, dev), _int32(new_lens, "new_lens", 1, dev)
-    starts, pairs = _int32(q_start, "q_start", 1, dev), _int32(copy_pairs, "copy_pairs", 2, dev)
-    st = _int32(status, "status", 1, dev)
-    slots, max_tokens = None, 0
-    if slot_mapping is not None:
-        _check(slot_mapping, "slot_mapping", 1, dev)
-        if slot_mapping.dtype != torch.int64:
-            raise TypeError("slot_mapping must be int64")
-        slots, max_tokens = slot_mapping.data_ptr(), slot_mapping.shape[0]
-    for t, shape in ((drop_lens, (S,)), (new_lens, (S,)), (q_start, (S + 1,)),
-                     (copy_pairs, (S, 2)), (status, (1,))):
-        if t is not None and tuple(t.shape) != shape:
-            raise ValueError("inconsistent shapes")
-    rc = _launch(dev, stream, lambda s: lib().pkv_tables_step(
-        lens, tables, refs, S, block_tables.shape[1], block_size, ref_counts.shape[0], drop, new,
-        starts, slots, max_tokens, pairs, st, s))
+    index, (lens, tables, refs), S, width = _pool(seq_lens, block_tables, ref_counts)
+    i32 = torch.int32
+    drop, new = _ptr(drop_lens, "drop_lens", 1, i32, index), _ptr(new_lens, "new_lens", 1, i32, index)
+    starts, pairs = _ptr(q_start, "q_start", 1, i32, index), _ptr(copy_pairs, "copy_pairs", 2, i32, index)
+    slots = _ptr(slot_mapping, "slot_mapping", 1, torch.int64, index)
+    st = _ptr(status, "status", 1, i32, index)
+    if ((drop_lens is not None and drop_lens.shape[0] != S)
+            or (new_lens is not None and new_lens.shape[0] != S)
+            or (q_start is not None and q_start.shape[0] != S + 1)
+            or (copy_pairs is not None and copy_pairs.shape != (S, 2))
+            or (status is not None and status.shape[0] != 1)):
+        raise ValueError("inconsistent shapes")
+    rc = _launch(lib().pkv_tables_step, seq_lens.device, stream,
+                 (lens, tables, refs, S, width, block_size, ref_counts.shape[0], drop, new, starts,
+                  slots, 0 if slots is None else slot_mapping.shape[0], pairs, st))
     if rc != 0:
         raise PkvError(rc, "pkv_tables_step")
 
@@ -765,14 +778,14 @@ def tables_fork(pairs: torch.Tensor, seq_lens: torch.Tensor, block_tables: torch
     """Rows that start as copies of others: for every (parent, child) in ``pairs``
     (int32 [n, 2]) the free row child gets parent's length and pages, each with
     one more reference.  Other arguments as for ``tables_step``."""
-    dev, (lens, tables, refs) = _check_pool(seq_lens, block_tables, ref_counts)
-    ptr = _int32(pairs, "pairs", 2, dev)
-    st = _int32(status, "status", 1, dev)
-    if pairs.shape[1] != 2 or (status is not None and tuple(status.shape) != (1,)):
+    index, (lens, tables, refs), S, width = _pool(seq_lens, block_tables, ref_counts)
+    ptr = _ptr(pairs, "pairs", 2, torch.int32, index)
+    st = _ptr(status, "status", 1, torch.int32, index)
+    if pairs.shape[1] != 2 or (status is not None and status.shape[0] != 1):
         raise ValueError("pairs must be int32 [n, 2], status int32 [1]")
-    rc = _launch(dev, stream, lambda s: lib().pkv_tables_fork(
-        ptr, pairs.shape[0], lens, tables, refs, seq_lens.shape[0], block_tables.shape[1],
-        block_size, ref_counts.shape[0], st, s))
+    rc = _launch(lib().pkv_tables_fork, seq_lens.device, stream,
+                 (ptr, pairs.shape[0], lens, tables, refs, S, width, block_size,
+                  ref_counts.shape[0], st))
     if rc != 0:
         raise PkvError(rc, "pkv_tables_fork")
 

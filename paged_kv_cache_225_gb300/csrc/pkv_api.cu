@@ -893,7 +893,7 @@ pkv_status pkv_tables_step(int32_t *seq_lens, int32_t *block_tables, int32_t *re
         return PKV_OK;
     TablesParams p;
     std::memset(&p, 0, sizeof p);
-    p.drop_lens = drop_lens;
+    p.drop_lens = num_seqs > 0 ? drop_lens : nullptr;
     p.new_lens = new_lens;
     p.seq_lens = seq_lens;
     p.block_tables = block_tables;

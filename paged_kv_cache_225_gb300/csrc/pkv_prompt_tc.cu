@@ -9,16 +9,17 @@
 //  * A tile is 128 rows: R = 128 / G consecutive tokens (rounded down) with
 //    their G heads.  An item is two neighbouring tiles of one sequence and KV
 //    head: every K and V block of 128 keys that reaches shared memory serves
-//    256 rows.  One persistent CTA per SM walks the items, costliest first,
-//    in alternating direction, so that the CTAs' totals stay even.
-//  * Ten warps: 0-3 own the rows of tile 0 (a thread per row, which is its
-//    TMEM lane), 4-7 those of tile 1, warp 8 looks items up and issues the TMA
-//    loads, one thread of warp 9 issues the MMAs.
+//    256 rows.  One persistent CTA per SM walks the items.
+//  * Warps 0-3 own the rows of tile 0 (a thread per row, which is its TMEM
+//    lane), 4-7 those of tile 1, one thread of warp 8 issues the TMA loads, one
+//    of warp 9 the MMAs, and warp 10 looks the items up ahead of all of them.
 //  * TMEM: scores of both tiles (2 x 128 columns, P written back over them as
 //    bf16) and both outputs (2 x head_dim columns).  Per block and tile:
 //    S = Q K^T from shared memory; the rows' threads read S, apply the limit
 //    and the softmax and write P; O += P V with P read from TMEM.  While one
-//    tile's threads work, the tensor cores run the other tile's products.
+//    tile's threads work, the tensor cores run the other tile's products; P is
+//    handed over in parts of 32 keys, so that P V starts before the last
+//    weights are there.
 //  * All shared-memory operands are in the 128-byte swizzle mode: [128 rows]
 //    [64 elements] per half of head_dim, K-major for Q and K, MN-major for V.
 //  * The last block of an item is cut to its keys in steps of 16 (N of S, K of
@@ -33,6 +34,7 @@
 //  * Every wait is bounded; a timeout records PKV_ERR_TIMEOUT, stops every role,
 //    lets copies and MMAs in flight finish and frees TMEM.
 #include <climits>
+#include <type_traits>
 
 #include "pkv_prompt.cuh"
 #include "pkv_tc.cuh"
@@ -43,10 +45,13 @@ namespace {
 
 constexpr int kM = 128;     // rows of a tile
 constexpr int kKeys = 128;  // keys of a block
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kTileWarps = 4;
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kItemWarp = 10;
+constexpr int kParts = 2;         // a block's P is handed to the MMAs in parts
+constexpr int kPart = kKeys / kParts;
 constexpr int kQueue = 4;
 constexpr int kHalf = 128 * 128;  // bytes of [128 rows][64 bf16]
 
@@ -85,24 +90,22 @@ struct PtItem {
         nb[1] = nt[1] > 0 ? (end[1] + kKeys - 1) / kKeys : 0;
         blocks = max(nb[0], nb[1]);
     }
-    // Keys of block j that tile t multiplies, in steps of 16.
-    __device__ __forceinline__ int cols(int t, int j) const
-    {
-        return j + 1 < nb[t] ? kKeys : (end[t] - j * kKeys + 15) & ~15;
-    }
 };
 
-// Shared-memory descriptor of a 128-byte-swizzled operand: atoms of 8 rows x
-// 128 bytes; lbo: distance of atoms along the contiguous axis (MN-major only),
-// sbo: distance of 8-row groups; descriptor version 1, layout code 2.
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo)
+// Keys of block j that a tile of nb blocks ending at key `end` multiplies, in
+// steps of 16.
+__device__ __forceinline__ int block_cols(int nb, int end, int j)
 {
-    uint64_t d = static_cast<uint64_t>((addr >> 4) & 0x3fffu);
-    d |= static_cast<uint64_t>((lbo >> 4) & 0x3fffu) << 16;
-    d |= static_cast<uint64_t>((sbo >> 4) & 0x3fffu) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
+    return j + 1 < nb ? kKeys : (end - j * kKeys + 15) & ~15;
+}
+
+// Shared-memory descriptor of a 128-byte-swizzled operand (atoms of 8 rows x
+// 128 bytes).  Low word: address / 16, and from bit 16 the distance / 16 of
+// atoms along the contiguous axis (MN-major only).  High word: the distance /
+// 16 of 8-row groups, descriptor version 1 (bit 14), layout code 2 (bit 29).
+__device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi)
+{
+    return static_cast<uint64_t>(hi) << 32 | lo;
 }
 
 __device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
@@ -165,19 +168,79 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return o;
 }
 
-__device__ __forceinline__ void store_out8(const PromptParams &p, size_t off, const float *v)
+// Maximum of 64 scores.
+__device__ __forceinline__ float max64(const float *x)
 {
-    if (p.out_dtype == PKV_F32) {
-        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + off);
-        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        uint4 w;
-        w.x = pack_bf16(v[0], v[1]);
-        w.y = pack_bf16(v[2], v[3]);
-        w.z = pack_bf16(v[4], v[5]);
-        w.w = pack_bf16(v[6], v[7]);
-        *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(p.out) + off) = w;
+    float a[8];
+#pragma unroll
+    for (int f = 0; f < 8; ++f)
+        a[f] = fmaxf(x[f], x[8 + f]);
+#pragma unroll
+    for (int e = 16; e < 64; e += 16)
+#pragma unroll
+        for (int f = 0; f < 8; ++f)
+            a[f] = fmaxf(a[f], fmaxf(x[e + f], x[e + 8 + f]));
+    return fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), fmaxf(fmaxf(a[4], a[5]), fmaxf(a[6], a[7])));
+}
+
+// Weights 2^(c x + off) of 64 scores: added to the sums l, stored as bf16 pairs
+// at column `col` (and what the rounding leaves, 64 columns on).  Sixteen at
+// a time, stage by stage, so that neighbouring instructions are independent.
+template <bool kSplit>
+__device__ __forceinline__ void weights64(const float *x, float c, float off, float2 (&l)[4], uint32_t col)
+{
+    const float2 c2 = make_float2(c, c), off2 = make_float2(off, off);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            float2 w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                w[e] = fma2(make_float2(x[32 * h + 16 * g + 2 * e], x[32 * h + 16 * g + 2 * e + 1]), c2, off2);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                w[e] = make_float2(MmaSoftmax::ex2(w[e].x), MmaSoftmax::ex2(w[e].y));
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                hi[8 * g + e] = pack_bf16(w[e].x, w[e].y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                l[e % 4] = add2(l[e % 4], w[e]);
+            if constexpr (kSplit)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    lo[8 * g + e] = pack_bf16(w[e].x - bf16_lo(hi[8 * g + e]), w[e].y - bf16_hi(hi[8 * g + e]));
+        }
+        tmem_st16u(col + 16 * h, hi);
+        if constexpr (kSplit)
+            tmem_st16u(col + 64 + 16 * h, lo);
+    }
+}
+
+// 32 consecutive columns of an output row, f32 or bf16.  With 32-byte stores a
+// lane fills whole sectors (`wide`: the output is aligned for them).
+template <bool kF32>
+__device__ __forceinline__ void store_out32(const PromptParams &p, size_t off, const float *v, bool wide)
+{
+    unsigned char *dst = static_cast<unsigned char *>(p.out) + off * (kF32 ? 4 : 2);
+#pragma unroll
+    for (int i = 0; i < (kF32 ? 4 : 2); ++i) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            w[e] = kF32 ? __float_as_uint(v[8 * i + e]) : pack_bf16(v[16 * i + 2 * e], v[16 * i + 2 * e + 1]);
+        if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 32 * i),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                         "r"(w[7])
+                         : "memory");
+        } else {
+            uint4 *d = reinterpret_cast<uint4 *>(dst + 32 * i);
+            d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
     }
 }
 
@@ -270,7 +333,7 @@ __device__ __noinline__ void redo_rows(const PromptParams &p, unsigned rows, int
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
             const float y = o[e] / l;
-            if (p.out_dtype == PKV_F32)
+            if constexpr (kSplit)
                 static_cast<float *>(p.out)[off + e] = y;
             else
                 static_cast<__nv_bfloat16 *>(p.out)[off + e] = __float2bfloat16(y);
@@ -286,7 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int NS = Geo::NS;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t full[NS], empty[NS];
-    __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_free[2];
+    __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][kParts], pv_done[2],
+        o_free[2];
     __shared__ __align__(8) uint64_t item_full[kQueue], item_empty[kQueue], drain;
     __shared__ int s_item[kQueue][5];
     __shared__ uint32_t s_tmem;
@@ -310,13 +374,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&q_full[t], 1);
             mbar_init(&q_empty[t], 1);
             mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[t], kTileWarps);
+            for (int i = 0; i < kParts; ++i)
+                mbar_init(&p_full[t][i], kTileWarps);
             mbar_init(&pv_done[t], 1);
             mbar_init(&o_free[t], kTileWarps);
         }
         for (int i = 0; i < kQueue; ++i) {
             mbar_init(&item_full[i], 1);
-            mbar_init(&item_empty[i], 2 * kTileWarps + 1);
+            mbar_init(&item_empty[i], 2 * kTileWarps + 2);
         }
         mbar_init(&drain, 1);
         s_abort = 0;
@@ -343,13 +408,75 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ring0 = smem0 + 2 * Geo::kTile;
 
     if (warp == kProducerWarp) {
-        // ------------------------------------------------------- producer
+        // ------------------------------------------------------- copies
+        if (lane == 0) {
+            uint32_t kv = 0;          // tiles issued
+            uint32_t qn[2] = {0, 0};  // Q tiles issued
+            bool ok = true;
+            auto load = [&](const CUtensorMap *map, const PtItem &it, int j) {
+                const uint32_t st = kv % NS;
+                if (kv >= NS && !tc_wait(&empty[st], ((kv / NS) - 1) & 1, abort))
+                    return false;
+                mbar_arrive_expect_tx(&full[st], Geo::kTile);
+                for (int h = 0; h < D / 64; ++h) {
+                    if (p.drop_first_copy && blockIdx.x == 0 && kv == 0 && h == 0)
+                        continue;
+                    tma_load_3d(smem + (2 + st) * Geo::kTile + h * kHalf, map, 64 * h, it.hkv,
+                                it.row0 + j * kKeys, &full[st]);
+                }
+                ++kv;
+                return true;
+            };
+            for (unsigned k = 0; ok; ++k) {
+                const int slot = k % kQueue;
+                ok = tc_wait(&item_full[slot], (k / kQueue) & 1, abort);
+                if (!ok)
+                    break;
+                PtItem it;
+                it.fill(s_item[slot], R);
+                mbar_arrive(&item_empty[slot]);
+                if (it.s < 0)
+                    break;
+                for (int j = 0; j < it.blocks && ok; ++j) {
+                    ok = load(&maps.k, it, j);
+                    for (int t = 0; t < 2 && j == 0 && ok; ++t) {
+                        if (it.nt[t] == 0)
+                            continue;
+                        if (qn[t] > 0)
+                            ok = tc_wait(&q_empty[t], (qn[t] - 1) & 1, abort);
+                        if (!ok)
+                            break;
+                        mbar_arrive_expect_tx(&q_full[t], (D / 64) * G * R * 128);
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_load_3d(smem + t * Geo::kTile + h * kHalf, &maps.q, 64 * h,
+                                        it.hkv * G, it.row0 + it.tok0 + t * R, &q_full[t]);
+                        ++qn[t];
+                    }
+                    ok = ok && load(&maps.v, it, j);
+                }
+            }
+            if (!ok) {
+                set_status(p.status, PKV_ERR_TIMEOUT);
+                *abort = 1;
+            }
+            if (*abort) {
+                // Let every copy still in flight land before the CTA exits.
+                for (uint32_t c = kv > NS ? kv - NS : 0; c < kv; ++c)
+                    mbar_wait_bounded(&full[c % NS], (c / NS) & 1, kWaitLimitNs);
+                for (int t = 0; t < 2; ++t)
+                    if (qn[t] > 0)
+                        mbar_wait_bounded(&q_full[t], (qn[t] - 1) & 1, kWaitLimitNs);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kItemWarp) {
+        // -------------------------------------------------- item look-up
         PromptScan scan;
         scan.init(p, 2 * R, lane, blockIdx.x == 0);
-        uint32_t kv = 0;        // tiles issued
-        uint32_t qn[2] = {0, 0};  // Q tiles issued
         bool ok = true;
         for (unsigned k = 0; ok; ++k) {
+            // Alternating direction: a CTA late in one row of items is early
+            // in the next, so that the CTAs' totals stay even.
             const unsigned u = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             const PromptItem found = scan.find(p, 2 * R, u, lane);
             if (lane == 0) {
@@ -364,179 +491,183 @@ __global__ void __launch_bounds__(kThreads, 1)
                     w[3] = found.n;
                     w[4] = found.index * 2 * R;
                     mbar_arrive(&item_full[slot]);
-                }
-                if (ok && found.s >= 0) {
-                    PtItem it;
-                    it.fill(s_item[slot], R);
-                    auto load = [&](const CUtensorMap *map, int j) {
-                        const uint32_t st = kv % NS;
-                        if (kv >= NS && !tc_wait(&empty[st], ((kv / NS) - 1) & 1, abort))
-                            return false;
-                        mbar_arrive_expect_tx(&full[st], Geo::kTile);
-                        for (int h = 0; h < D / 64; ++h) {
-                            if (p.drop_first_copy && blockIdx.x == 0 && kv == 0 && h == 0)
-                                continue;
-                            tma_load_3d(smem + (2 * Geo::kTile + st * Geo::kTile + h * kHalf), map,
-                                        64 * h, it.hkv, it.row0 + j * kKeys, &full[st]);
-                        }
-                        ++kv;
-                        return true;
-                    };
-                    for (int j = 0; j < it.blocks && ok; ++j) {
-                        ok = load(&maps.k, j);
-                        for (int t = 0; t < 2 && j == 0 && ok; ++t) {
-                            if (it.nt[t] == 0)
-                                continue;
-                            if (qn[t] > 0)
-                                ok = tc_wait(&q_empty[t], (qn[t] - 1) & 1, abort);
-                            if (!ok)
-                                break;
-                            mbar_arrive_expect_tx(&q_full[t], (D / 64) * G * R * 128);
-                            for (int h = 0; h < D / 64; ++h)
-                                tma_load_3d(smem + t * Geo::kTile + h * kHalf, &maps.q, 64 * h,
-                                            it.hkv * G, it.row0 + it.tok0 + t * R, &q_full[t]);
-                            ++qn[t];
-                        }
-                        ok = ok && load(&maps.v, j);
-                    }
-                }
-                if (!ok) {
+                } else {
                     set_status(p.status, PKV_ERR_TIMEOUT);
                     *abort = 1;
                 }
             }
-            ok = __shfl_sync(kFullMask, ok ? 1 : 0, 0) != 0;
-            if (found.s < 0)
-                break;
-        }
-        __syncwarp();
-        if (lane == 0 && *abort) {
-            // Let every copy still in flight land before the CTA exits.
-            for (uint32_t c = kv > NS ? kv - NS : 0; c < kv; ++c)
-                mbar_wait_bounded(&full[c % NS], (c / NS) & 1, kWaitLimitNs);
-            for (int t = 0; t < 2; ++t)
-                if (qn[t] > 0)
-                    mbar_wait_bounded(&q_full[t], (qn[t] - 1) & 1, kWaitLimitNs);
+            ok = __shfl_sync(kFullMask, ok ? 1 : 0, 0) != 0 && found.s >= 0;
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------- MMA issue
+        // One thread for both tiles, which keeps them out of phase: while one
+        // tile's rows are in the softmax the other's products run.  A step is,
+        // tile after tile, P V of block j and the scores of the next block;
+        // after an item's last block these are the next item's first scores,
+        // which its threads find when their output is written.  The tensor
+        // cores queue about three MMAs (200 cycles), so little may stand
+        // between one group of eight and the next: the steps in which every
+        // block is whole have a loop of their own.
         if (lane == 0) {
             // A negative scale negates Q (instruction descriptor bit 13).
             const uint32_t id_s0 = tc_idesc(kM, 0, false) | (p.negate ? 1u << 13 : 0u);
             constexpr uint32_t kIdPV = tc_idesc(kM, D, true);
-            uint32_t q_cnt[2] = {0, 0}, p_cnt[2] = {0, 0}, o_cnt[2] = {0, 0};
-            uint32_t base = 0;  // ring index of the current item's first K tile
+            constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+            constexpr uint32_t kTileLo = Geo::kTile >> 4;
+            const uint32_t qlo = (smem0 >> 4) | 1u << 16;
+            const uint32_t klo0 = (ring0 >> 4) | 1u << 16, vlo0 = (ring0 >> 4) | (kHalf >> 4) << 16;
+            uint32_t vst = NS - 1, vpar = 1, kst = 0, kpar = 0;  // ring positions of V (j) and K (next)
+            uint32_t q_par = 0, o_par = 3, p_par = 0;            // bit t
             unsigned k = 0;
-            auto next_item = [&](PtItem &it) -> int {  // 1 item, 0 end, -1 failure
-                const int slot = k % kQueue;
-                if (!tc_wait(&item_full[slot], (k / kQueue) & 1, abort))
-                    return -1;
-                it.fill(s_item[slot], R);
-                mbar_arrive(&item_empty[slot]);
-                ++k;
-                return it.s >= 0 ? 1 : 0;
-            };
-            auto qk = [&](int t, const PtItem &it, int j, uint32_t b) -> bool {
-                if (j == 0) {
-                    if (!tc_wait(&q_full[t], q_cnt[t] & 1, abort))
-                        return false;
-                    ++q_cnt[t];
-                }
-                const uint32_t c = b + 2 * j, st = c % NS;
-                if (!tc_wait(&full[st], (c / NS) & 1, abort))
-                    return false;
-                tc_fence_after();
-                const uint32_t id = id_s0 | (static_cast<uint32_t>(it.cols(t, j) >> 3) << 17);
-                const uint64_t qd = smem_desc_sw128(smem0 + t * Geo::kTile, 16, 1024);
-                const uint64_t kd = smem_desc_sw128(ring0 + st * Geo::kTile, 16, 1024);
+            bool ok = true;
+            // Eight MMAs of S (head_dim 128) for tile t, and of P V per part.
+            auto mma_s = [&](uint32_t t, uint32_t id) {
+                const uint32_t klo = klo0 + kst * kTileLo, q = qlo + t * kTileLo;
+                const uint32_t d = tmem + t * kKeys;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint32_t o = ((ks / 4) * kHalf + (ks % 4) * 32) >> 4;
-                    tc_mma_ss(tmem + t * kKeys, qd + o, kd + o, id, ks > 0);
+                    tc_mma_ss(d, desc64(q + o, kDescHi), desc64(klo + o, kDescHi), id, ks > 0);
                 }
-                tc_commit(&s_full[t]);
-                if (j + 1 == it.nb[t])
-                    tc_commit(&q_empty[t]);
-                return true;
             };
-            auto pv = [&](int t, const PtItem &it, int j, uint32_t b) -> bool {
-                if (!tc_wait(&p_full[t], p_cnt[t] & 1, abort))
-                    return false;
-                ++p_cnt[t];
-                if (j == 0) {
-                    if (o_cnt[t] > 0 && !tc_wait(&o_free[t], (o_cnt[t] - 1) & 1, abort))
-                        return false;
-                    ++o_cnt[t];
-                }
-                const uint32_t c = b + 2 * j + 1, st = c % NS;
-                if (!tc_wait(&full[st], (c / NS) & 1, abort))
-                    return false;
-                tc_fence_after();
-                const uint64_t vd = smem_desc_sw128(ring0 + st * Geo::kTile, kHalf, 1024);
-                const int steps = it.cols(t, j) >> 4;
-                const uint32_t pcol = tmem + t * kKeys, ocol = tmem + Geo::kOCol + t * D;
-                for (int ks = 0; ks < steps; ++ks)
-                    tc_mma_ta(ocol, pcol + 8 * ks, vd + ks * (2048 >> 4), kIdPV, j > 0 || ks > 0);
-                if constexpr (kSplit)
-                    for (int ks = 0; ks < steps; ++ks)
-                        tc_mma_ta(ocol, pcol + 64 + 8 * ks, vd + ks * (2048 >> 4), kIdPV, true);
-                tc_commit(&pv_done[t]);
-                return true;
-            };
-            auto release = [&](uint32_t c) { tc_commit(&empty[c % NS]); };
-
-            PtItem cur, nxt;
-            int have = next_item(cur);
-            bool failed = have < 0;
-            if (have > 0) {
-                failed = !qk(0, cur, 0, base) || (cur.nb[1] > 0 && !qk(1, cur, 0, base));
-                if (!failed)
-                    release(base);
-            }
-            while (have > 0 && !failed) {
-                const uint32_t nbase = base + 2 * cur.blocks;
-                int have_next = 0;
-                for (int j = 0; j < cur.blocks; ++j) {
-                    if (j < cur.nb[0]) {
-                        failed = !pv(0, cur, j, base) ||
-                                 (j + 1 < cur.nb[0] && !qk(0, cur, j + 1, base));
-                        if (failed)
-                            break;
-                    }
-                    if (j + 1 == cur.blocks) {
-                        // The next item's first scores of tile 0, so that its
-                        // threads find them when their output is written.
-                        have_next = next_item(nxt);
-                        failed = have_next < 0 || (have_next > 0 && !qk(0, nxt, 0, nbase));
-                        if (failed)
-                            break;
-                    }
-                    if (j < cur.nb[1]) {
-                        failed = !pv(1, cur, j, base);
-                        if (failed)
-                            break;
-                    }
-                    release(base + 2 * j + 1);
-                    if (j + 1 < cur.blocks) {
-                        failed = j + 1 < cur.nb[1] && !qk(1, cur, j + 1, base);
-                        if (failed)
-                            break;
-                        release(base + 2 * (j + 1));
-                    }
-                }
-                if (failed)
-                    break;
-                if (have_next > 0) {
-                    failed = nxt.nb[1] > 0 && !qk(1, nxt, 0, nbase);
-                    if (failed)
+            auto mma_pv = [&](uint32_t t, int part, int steps, bool first) {
+                const uint32_t vlo = vlo0 + vst * kTileLo + part * (kPart / 16) * (2048 >> 4);
+                const uint32_t a = tmem + t * kKeys + part * (kPart / 2), d = tmem + Geo::kOCol + t * D;
+#pragma unroll
+                for (int ks = 0; ks < kPart / 16; ++ks) {
+                    if (ks >= steps)
                         break;
-                    release(nbase);
+                    const uint64_t vd = desc64(vlo + ks * (2048 >> 4), kDescHi);
+                    tc_mma_ta(d, a + 8 * ks, vd, kIdPV, !(first && ks == 0));
+                    if constexpr (kSplit)
+                        tc_mma_ta(d, a + kKeys / 2 + 8 * ks, vd, kIdPV, true);
                 }
-                cur = nxt;
-                base = nbase;
-                have = have_next;
+            };
+            auto next_kv = [&] {  // V of the block just scored follows its K, then the next K
+                vst = kst + 1 == NS ? 0 : kst + 1;
+                vpar = kst + 1 == NS ? kpar ^ 1 : kpar;
+                kst = vst + 1 == NS ? 0 : vst + 1;
+                kpar = vst + 1 == NS ? vpar ^ 1 : vpar;
+            };
+            int nb0 = 0, nb1 = 0, end0 = 0, end1 = 0, blocks = 0;        // the item; 0 blocks: none
+            int nnb0 = 0, nnb1 = 0, nend0 = 0, nend1 = 0, nblocks = 0;   // the next one
+            auto next_item = [&] {
+                const int slot = k % kQueue;
+                ok = ok && tc_wait(&item_full[slot], (k / kQueue) & 1, abort);
+                nblocks = 0;
+                if (!ok)
+                    return;
+                PtItem it;
+                it.fill(s_item[slot], R);
+                mbar_arrive(&item_empty[slot]);
+                ++k;
+                if (it.s < 0)
+                    return;
+                nnb0 = it.nb[0];
+                nnb1 = it.nb[1];
+                nend0 = it.end[0];
+                nend1 = it.end[1];
+                nblocks = it.blocks;
+            };
+            int j = -1;
+            next_item();
+            blocks = nblocks;
+            nb0 = nnb0;
+            nb1 = nnb1;
+            end0 = nend0;
+            end1 = nend1;
+            while (ok && blocks > 0) {
+                // Steps whose blocks, and the ones scored in them, are whole
+                // for both tiles.
+                const uint32_t id_whole = id_s0 | (kKeys >> 3) << 17;
+                const int whole = min(nb0, nb1) - 2;
+                for (; j >= 0 && j < whole && ok; ++j) {
+                    if (j == 0) {
+                        ok = tc_wait(&o_free[0], o_par & 1, abort) && tc_wait(&o_free[1], o_par >> 1, abort);
+                        o_par ^= 3;
+                    }
+                    ok = ok && tc_wait(&full[vst], vpar, abort);
+#pragma unroll 1
+                    for (uint32_t t = 0; t < 2; ++t) {
+                        for (int part = 0; part < kParts; ++part) {
+                            ok = ok && tc_wait(&p_full[t][part], p_par >> t & 1, abort);
+                            tc_fence_after();
+                            if (ok)
+                                mma_pv(t, part, kPart / 16, j == 0 && part == 0);
+                        }
+                        tc_commit(&pv_done[t]);
+                        if (t == 0)
+                            ok = ok && tc_wait(&full[kst], kpar, abort);
+                        if (!ok)
+                            break;
+                        mma_s(t, id_whole);
+                        tc_commit(&s_full[t]);
+                    }
+                    p_par ^= 3;
+                    tc_commit(&empty[vst]);
+                    tc_commit(&empty[kst]);
+                    next_kv();
+                }
+                if (!ok)
+                    break;
+                // The other steps.
+                const bool last = j + 1 == blocks;
+                const int nj = last ? 0 : j + 1;
+                bool more = !last;
+#pragma unroll 1
+                for (uint32_t t = 0; t < 2; ++t) {
+                    const int nb = t ? nb1 : nb0, end = t ? end1 : end0;
+                    if (j >= 0 && j < nb) {
+                        if (j == 0) {  // the output of the tile's item before this one is read
+                            ok = ok && tc_wait(&o_free[t], o_par >> t & 1, abort);
+                            o_par ^= 1u << t;
+                        }
+                        ok = ok && tc_wait(&full[vst], vpar, abort);
+                        const int steps = block_cols(nb, end, j) / 16;
+                        for (int part = 0; part < kParts && kPart / 16 * part < steps; ++part) {
+                            ok = ok && tc_wait(&p_full[t][part], p_par >> t & 1, abort);
+                            tc_fence_after();
+                            if (ok)
+                                mma_pv(t, part, steps - kPart / 16 * part, j == 0 && part == 0);
+                        }
+                        p_par ^= 1u << t;
+                        tc_commit(&pv_done[t]);
+                    }
+                    if (last && t == 0) {
+                        next_item();
+                        more = nblocks > 0;
+                    }
+                    const int qnb = last ? (t ? nnb1 : nnb0) : nb, qend = last ? (t ? nend1 : nend0) : end;
+                    if (ok && more && nj < qnb) {
+                        if (nj == 0) {
+                            ok = tc_wait(&q_full[t], q_par >> t & 1, abort);
+                            q_par ^= 1u << t;
+                        }
+                        ok = ok && tc_wait(&full[kst], kpar, abort);
+                        tc_fence_after();
+                        if (ok)
+                            mma_s(t, id_s0 | (static_cast<uint32_t>(block_cols(qnb, qend, nj)) >> 3) << 17);
+                        tc_commit(&s_full[t]);
+                        if (nj + 1 == qnb)
+                            tc_commit(&q_empty[t]);
+                    }
+                }
+                if (j >= 0)
+                    tc_commit(&empty[vst]);
+                if (!ok || !more)
+                    break;
+                tc_commit(&empty[kst]);
+                next_kv();
+                if (last) {
+                    blocks = nblocks;
+                    nb0 = nnb0;
+                    nb1 = nnb1;
+                    end0 = nend0;
+                    end1 = nend1;
+                }
+                j = nj;
             }
-            if (failed) {
+            if (!ok) {
                 set_status(p.status, PKV_ERR_TIMEOUT);
                 *abort = 1;
             }
@@ -554,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ocol = tmem + lanes + Geo::kOCol + t * D;
         const float c = p.score_scale;  // positive
         constexpr float kLazy = MmaSoftmax::kLazy;
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         uint32_t cnt = 0;   // blocks of this tile
         uint32_t base = 0;  // ring index of the item's first K tile
         bool failed = false;
@@ -570,98 +702,74 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&item_empty[slot]);
             if (it.s < 0)
                 break;
-            const int nt = it.nt[t], nb = it.nb[t];
+            // Selected, not indexed: the item stays in registers.
+            const int nt = t ? it.nt[1] : it.nt[0], nb = t ? it.nb[1] : it.nb[0];
+            const int end = t ? it.end[1] : it.end[0], item_end = max(it.end[0], it.end[1]);
             const int first = it.tok0 + t * R;  // token of row 0
             const int pos = first + min(r / G, nt - 1);
             float m = -INFINITY;                // running maximum, log2 units
-            float2 l2 = make_float2(0.f, 0.f);  // its sum, in two halves
+            float2 l2[4] = {};                  // its sum, in eight parts
+            const int whole = (first + 1) / kKeys;  // leading blocks that every row sees whole
             for (int j = 0; j < nb; ++j, ++cnt) {
-                const int cols = it.cols(t, j);
-                const int tb = j * kKeys;
                 if (!warp_wait(&s_full[t], cnt & 1, abort)) {
                     failed = true;
                     break;
                 }
                 tc_fence_after();
+                const bool tail = j >= whole;
+                const int cols = tail ? block_cols(nb, end, j) : kKeys;
+                const bool second = cols > kPart;  // the block has keys in its second part
                 float x[kKeys];
-                const bool whole = tb + kKeys <= first + 1;  // every row sees every key
-#pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4)
-                    if (32 * q4 < cols)
-                        tmem_ld32(scol + 32 * q4, x + 32 * q4);
+                tmem_ld32(scol, x);
+                tmem_ld32(scol + 32, x + 32);
+                if (second) {
+                    tmem_ld32(scol + 64, x + 64);
+                    tmem_ld32(scol + 96, x + 96);
+                }
                 tmem_wait_ld(x);
-                if (!whole) {
-                    const int lim = pos - tb + 1;
+                if (tail) {
+                    const int lim = pos - j * kKeys + 1;  // keys this row sees
 #pragma unroll
                     for (int e = 0; e < kKeys; ++e)
                         x[e] = e < lim ? x[e] : -INFINITY;
                 }
-                float mx;
-                {
-                    float a[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        a[e] = x[e];
-#pragma unroll
-                    for (int e = 8; e < kKeys; e += 16)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            a[i] = e + 8 + i < kKeys ? fmaxf(a[i], fmaxf(x[e + i], x[(e + 8 + i) % kKeys]))
-                                                     : fmaxf(a[i], x[e + i]);
-                    mx = fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])),
-                               fmaxf(fmaxf(a[4], a[5]), fmaxf(a[6], a[7]))) * c;
-                }
+                float mx = max64(x);
+                if (second)
+                    mx = fmaxf(mx, max64(x + kPart));
+                mx *= c;
                 const bool need = mx > m + kLazy;  // false when nothing is visible
-                float alpha = 1.f;
-                if (need) {
-                    alpha = m == -INFINITY ? 0.f : MmaSoftmax::ex2(m - mx);
-                    l2.x *= alpha;
-                    l2.y *= alpha;
-                    m = mx;
-                }
-                if (j > 0 && __any_sync(kFullMask, need)) {
-                    // O holds earlier blocks: rescale it once their P V is done.
-                    if (!warp_wait(&pv_done[t], (cnt - 1) & 1, abort)) {
-                        failed = true;
-                        break;
+                if (__any_sync(kFullMask, need)) {
+                    float alpha = 1.f;
+                    if (need) {
+                        alpha = m == -INFINITY ? 0.f : MmaSoftmax::ex2(m - mx);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            l2[i].x *= alpha;
+                            l2[i].y *= alpha;
+                        }
+                        m = mx;
                     }
-                    tc_fence_after();
+                    if (j > 0) {
+                        // O holds earlier blocks: rescale it once their P V is done.
+                        if (!warp_wait(&pv_done[t], (cnt - 1) & 1, abort)) {
+                            failed = true;
+                            break;
+                        }
+                        tc_fence_after();
 #pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 16) {
-                        float ov[16];
-                        tmem_ld16(ocol + c0, ov);
+                        for (int c0 = 0; c0 < D; c0 += 16) {
+                            float ov[16];
+                            tmem_ld16(ocol + c0, ov);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            ov[e] *= alpha;
-                        tmem_st16(ocol + c0, ov);
+                            for (int e = 0; e < 16; ++e)
+                                ov[e] *= alpha;
+                            tmem_st16(ocol + c0, ov);
+                        }
+                        tmem_wait_st();
                     }
-                    tmem_wait_st();
                 }
-                // Weights 2^(c x - m); a row of nothing but -inf so far has
-                // weights 0.
-                const float off = m == -INFINITY ? 0.f : -m;
-                const float2 c2 = make_float2(c, c), off2 = make_float2(off, off);
-#pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    if (32 * q4 >= cols)
-                        break;
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 y = fma2(make_float2(x[32 * q4 + e], x[32 * q4 + e + 1]), c2, off2);
-                        const float2 w = make_float2(MmaSoftmax::ex2(y.x), MmaSoftmax::ex2(y.y));
-                        l2 = add2(l2, w);
-                        hi[e / 2] = pack_bf16(w.x, w.y);
-                        if constexpr (kSplit)
-                            lo[e / 2] = pack_bf16(w.x - bf16_lo(hi[e / 2]), w.y - bf16_hi(hi[e / 2]));
-                    }
-                    tmem_st16u(scol + 16 * q4, hi);
-                    if constexpr (kSplit)
-                        tmem_st16u(scol + 64 + 16 * q4, lo);
-                }
-                tmem_wait_st();
                 // V rows past the item's keys may hold anything.
-                const int zero0 = max(it.end[0], it.end[1]) - tb;
+                const int zero0 = item_end - j * kKeys;
                 if (zero0 < cols) {
                     const uint32_t vc = base + 2 * j + 1;
                     if (!warp_wait(&full[vc % NS], (vc / NS) & 1, abort)) {
@@ -676,10 +784,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     fence_proxy_async();
                 }
+                // Weights 2^(c x - m), in bf16 pairs over the consumed scores; a
+                // row of nothing but -inf so far has weights 0.
+                const float off = m == -INFINITY ? 0.f : -m;
+                weights64<kSplit>(x, c, off, l2, scol);
+                tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&p_full[t]);
+                    mbar_arrive(&p_full[t][0]);
+                if (second) {
+                    weights64<kSplit>(x + kPart, c, off, l2, scol + kPart / 2);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                }
+                if (lane == 0)  // both parts' barriers count every block
+                    mbar_arrive(&p_full[t][1]);
             }
             base += 2 * it.blocks;
             if (failed)
@@ -694,7 +815,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const bool live = r < nt * G;
-            const float inv = 1.f / (l2.x + l2.y);
+            const float2 lsum = add2(add2(l2[0], l2[1]), add2(l2[2], l2[3]));
+            const float inv = 1.f / (lsum.x + lsum.y);
             const size_t orow = (static_cast<size_t>(it.row0 + pos) * p.num_q_heads + it.hkv * G + r % G) * D;
             float bad = 0.f;  // NaN once an output is not finite
 #pragma unroll 1
@@ -708,9 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bad = fmaf(ov[e], 0.f, bad);
                 }
                 if (live)
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        store_out8(p, orow + c0 + e, ov + e);
+                    store_out32<kSplit>(p, orow + c0, ov, wide);
             }
             tc_fence_before();
             __syncwarp();
@@ -719,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const unsigned redo = __ballot_sync(kFullMask, live && bad != 0.f);
             if (redo)
                 redo_rows<D, kSplit>(p, redo, 32 * (warp & 3), first, it.row0, it.hkv,
-                             min((nb - 1) * kKeys + it.cols(t, nb - 1), max(it.end[0], it.end[1])), lane);
+                                     min((nb - 1) * kKeys + block_cols(nb, end, nb - 1), item_end), lane);
         }
         if (failed && lane == 0) {
             set_status(p.status, PKV_ERR_TIMEOUT);

@@ -23,40 +23,64 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+// CTAs of the cluster: the largest there is, which was never slower than fewer
+// (us a step on 1 / 4 / 16: 128 rows of a 31K-page pool 17.2 / 11.9 / 10.7, 64
+// prompts admitted 120.7 / 37.8 / 18.3, 512 rows of a 288K-page pool 154.9 /
+// 53.1 / 22.1).
+constexpr int kStepCtas = 16;
 
 __device__ __forceinline__ int pages_of(int tokens) { return (tokens + kBlockSize - 1) / kBlockSize; }
 
-// Inclusive prefix sum over the block; *total is the block's sum.  `part`
-// holds kWarps entries and is free to be reused on return.
-__device__ unsigned long long block_scan(unsigned long long x, unsigned long long *part,
-                                         unsigned long long *total)
+// Orders every CTA's accesses (shared and global) before the barrier with
+// those after it.  A cluster of one needs only the block's barrier.
+__device__ __forceinline__ void sync_all(int ctas)
+{
+    if (ctas == 1) {
+        __syncthreads();
+        return;
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Inclusive prefix sums of a pair over the block; *ta, *tb are the block's
+// sums.  `part` holds 2 * kWarps entries and is free to be reused on return.
+__device__ void block_scan2(unsigned long long &a, unsigned long long &b, unsigned long long *part,
+                            unsigned long long *ta, unsigned long long *tb)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const unsigned long long y = __shfl_up_sync(kFullMask, x, d);
-        if (lane >= d)
-            x += y;
+        const unsigned long long y = __shfl_up_sync(kFullMask, a, d);
+        const unsigned long long z = __shfl_up_sync(kFullMask, b, d);
+        if (lane >= d) {
+            a += y;
+            b += z;
+        }
     }
-    if (lane == 31)
-        part[warp] = x;
+    if (lane == 31) {
+        part[warp] = a;
+        part[kWarps + warp] = b;
+    }
     __syncthreads();
-    if (warp == 0) {
-        unsigned long long p = part[lane];
+    if (warp < 2) {
+        unsigned long long p = part[kWarps * warp + lane];
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const unsigned long long y = __shfl_up_sync(kFullMask, p, d);
             if (lane >= d)
                 p += y;
         }
-        part[lane] = p;
+        part[kWarps * warp + lane] = p;
     }
     __syncthreads();
-    if (warp > 0)
-        x += part[warp - 1];
-    *total = part[kWarps - 1];
+    if (warp > 0) {
+        a += part[warp - 1];
+        b += part[kWarps + warp - 1];
+    }
+    *ta = part[kWarps - 1];
+    *tb = part[2 * kWarps - 1];
     __syncthreads();
-    return x;
 }
 
 // First row whose inclusive end lies above i (ends is non-decreasing).
@@ -73,18 +97,33 @@ __device__ __forceinline__ int row_of(const int *ends, int n, int i)
     return lo;
 }
 
-// Ids in [lo, lo + 32) whose count is zero, as a lane mask.
-__device__ __forceinline__ unsigned zero_mask(const int32_t *ref, int lo, int hi, int lane)
+// Which of the four counts from id on are zero (bits 0..3); ids from `end` on
+// are not.  id is a multiple of 4 and the counts are 16-byte aligned.
+__device__ __forceinline__ unsigned zeros4(const int32_t *ref, long id, long end)
 {
-    const int p = lo + lane;
-    return __ballot_sync(kFullMask, p < hi && __ldcg(ref + p) == 0);
+    if (id + 4 <= end) {
+        const int4 v = __ldcg(reinterpret_cast<const int4 *>(ref + id));
+        return (v.x == 0) | (v.y == 0) << 1 | (v.z == 0) << 2 | (v.w == 0) << 3;
+    }
+    unsigned m = 0;
+    for (int c = 0; c < 4; ++c)
+        m |= (id + c < end && __ldcg(ref + id + c) == 0 ? 1u : 0u) << c;
+    return m;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) tables_step_kernel(const TablesParams p)
+constexpr int kStep = 4;  // loads of 128 counts a warp has in flight
+
+// A cluster of CTAs runs the whole step: the pool's counts and the rows' pages
+// and slots are spread over the cluster's warps, the (small) row sums are
+// computed by every CTA for itself, and three cluster barriers separate drops,
+// counting, handing out and writing slots.  All of it is a few dependent trips
+// to L2: bound by latency, not by bytes.
+__global__ void __launch_bounds__(kThreads, 1) tables_step_kernel(const TablesParams p, int ctas)
 {
     extern __shared__ int rows_smem[];
-    __shared__ unsigned long long s_part[kWarps];
+    __shared__ unsigned long long s_part[2 * kWarps];
     __shared__ int s_warp_base[kWarps + 1];
+    __shared__ int s_zeros[kStepCtas];  // zero counts of every CTA's part of the pool
     __shared__ int s_bad;
     const int S = p.num_seqs;
     int *tok_end = rows_smem;                                        // tokens reserved, inclusive
@@ -92,47 +131,87 @@ __global__ void __launch_bounds__(kThreads, 1) tables_step_kernel(const TablesPa
     unsigned *kept2 = reinterpret_cast<unsigned *>(page_end + S);    // 2 * kept + copy
     int *shared_last = reinterpret_cast<int *>(kept2 + S);           // shared part-filled last page
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int cta = blockIdx.x;  // the grid is one cluster
     const int max_len = p.max_blocks * kBlockSize;
     const size_t width = p.max_blocks;
 
     if (threadIdx.x == 0)
         s_bad = 0;
 
-    // Drops, a warp per row.
+    // Drops: as many warps per row as there are for all rows.
     if (p.drop_lens) {
-        for (int s = warp; s < S; s += kWarps) {
-            const int L = p.seq_lens[s], d = __ldg(p.drop_lens + s);
+        const int per_row = max(1, ctas * kWarps / S);
+        const int gw = cta * kWarps + warp;
+        const int sub = gw % per_row;
+        for (int s = gw / per_row; s < S; s += ctas * kWarps / per_row) {
+            if (gw / per_row >= ctas * kWarps / per_row)
+                break;  // warps left over
+            const int L = __ldcg(p.seq_lens + s), d = __ldg(p.drop_lens + s);
             if (L < 0 || L > max_len || d < 0) {
-                if (lane == 0)
+                if (lane == 0 && sub == 0)
                     set_status(p.status, PKV_ERR_OUT_OF_RANGE);
                 continue;
             }
             int32_t *row = p.block_tables + s * width;
-            for (int j = pages_of(L - min(d, L)) + lane; j < pages_of(L); j += 32) {
-                const int32_t page = row[j];
-                bool ok = page >= 0 && page < p.num_blocks;
-                if (ok && atomicSub(p.ref_counts + page, 1) <= 0) {
-                    atomicAdd(p.ref_counts + page, 1);  // nobody held it: put it back
-                    ok = false;
+            const int last = pages_of(L);
+            for (int j0 = pages_of(L - min(d, L)) + sub * 32 + lane; j0 < last;
+                 j0 += kStep * 32 * per_row) {
+                int32_t page[kStep];
+#pragma unroll
+                for (int i = 0; i < kStep; ++i) {
+                    const int j = j0 + i * 32 * per_row;
+                    page[i] = j < last ? __ldcg(row + j) : -1;
                 }
-                if (!ok)
+                bool bad = false;
+#pragma unroll
+                for (int i = 0; i < kStep; ++i) {
+                    const int j = j0 + i * 32 * per_row;
+                    if (j >= last)
+                        continue;
+                    row[j] = -1;
+                    bool ok = page[i] >= 0 && page[i] < p.num_blocks;
+                    if (ok && atomicSub(p.ref_counts + page[i], 1) <= 0) {
+                        atomicAdd(p.ref_counts + page[i], 1);  // nobody held it: put it back
+                        ok = false;
+                    }
+                    bad = bad || !ok;
+                }
+                if (bad)
                     set_status(p.status, PKV_ERR_OUT_OF_RANGE);
-                row[j] = -1;
             }
         }
     }
-    __syncthreads();
+    sync_all(ctas);  // also: every CTA runs, before its shared memory is written
+
+    // Zero counts: the pool in ranges of `per_warp` ids, one per warp of the
+    // cluster, in order.
+    const long per_warp = (p.num_blocks / (ctas * kWarps) + 128) & ~127;
+    const long lo = min(static_cast<long>(cta * kWarps + warp) * per_warp, static_cast<long>(p.num_blocks));
+    const long hi = min(lo + per_warp, static_cast<long>(p.num_blocks));
+    int zeros = 0;
+    for (long b = lo; b < hi; b += 128 * kStep) {
+        unsigned m[kStep];
+#pragma unroll
+        for (int i = 0; i < kStep; ++i)
+            m[i] = zeros4(p.ref_counts, min(b + 128 * i + 4 * lane, hi), hi);
+#pragma unroll
+        for (int i = 0; i < kStep; ++i)
+            zeros += __popc(m[i]);
+    }
+    zeros = __reduce_add_sync(kFullMask, zeros);
+    if (lane == 0)
+        s_warp_base[warp + 1] = zeros;
 
     // Rows: what is kept, and which part-filled last pages are shared.
     for (int s = threadIdx.x; s < S; s += kThreads) {
-        const int L = p.seq_lens[s], d = p.drop_lens ? __ldg(p.drop_lens + s) : 0;
+        const int L = __ldcg(p.seq_lens + s), d = p.drop_lens ? __ldg(p.drop_lens + s) : 0;
         const int n = p.new_lens ? __ldg(p.new_lens + s) : 0;
         const bool len_ok = L >= 0 && L <= max_len;
         const int kept = len_ok ? L - (d > 0 ? min(d, L) : 0) : 0;
         bool bad = !len_ok || n < 0 || n > max_len - kept;
         int shared = -1;
         if (!bad && n > 0 && kept % kBlockSize != 0) {
-            const int32_t page = p.block_tables[s * width + pages_of(kept) - 1];
+            const int32_t page = __ldcg(p.block_tables + s * width + pages_of(kept) - 1);
             const int refs = page >= 0 && page < p.num_blocks ? __ldcg(p.ref_counts + page) : 0;
             bad = refs <= 0;
             if (refs > 1)
@@ -144,6 +223,26 @@ __global__ void __launch_bounds__(kThreads, 1) tables_step_kernel(const TablesPa
             s_bad = 1;
     }
     __syncthreads();
+    if (threadIdx.x < 32) {  // this CTA's zero counts: per-warp bases, total to every CTA
+        int z = s_warp_base[lane + 1];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(kFullMask, z, d);
+            if (lane >= d)
+                z += y;
+        }
+        s_warp_base[lane + 1] = z;
+        if (lane == 0)
+            s_warp_base[0] = 0;
+        const int all = __shfl_sync(kFullMask, z, 31);
+        if (lane < ctas) {
+            uint32_t remote;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                         : "=r"(remote)
+                         : "r"(smem_u32(&s_zeros[cta])), "r"(lane));
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(all) : "memory");
+        }
+    }
     // A sharing row copies unless every other holder of the page is an
     // earlier row that has copied already.
     bool want_pair = false;
@@ -175,71 +274,70 @@ __global__ void __launch_bounds__(kThreads, 1) tables_step_kernel(const TablesPa
                 need = pages_of(kept + nn) - pages_of(kept) + (kept2[s] & 1u);
             }
         }
-        unsigned long long sum;
-        const unsigned long long te = tokens + block_scan(n, s_part, &sum);
-        tokens += sum;
-        const unsigned long long pe = pages + block_scan(need, s_part, &sum);
-        pages += sum;
+        unsigned long long sum_n, sum_need;
+        block_scan2(n, need, s_part, &sum_n, &sum_need);
         if (s < S) {  // read only when both totals fit an int (checked below)
-            tok_end[s] = static_cast<int>(te);
-            page_end[s] = static_cast<int>(pe);
+            tok_end[s] = static_cast<int>(tokens + n);
+            page_end[s] = static_cast<int>(pages + need);
         }
+        tokens += sum_n;
+        pages += sum_need;
     }
+    sync_all(ctas);
 
-    // Zero counts per warp, each over a contiguous range of the pool.
-    const int per_warp = (p.num_blocks / kWarps + 32) & ~31;
-    const int lo = static_cast<int>(min(static_cast<long>(warp) * per_warp, static_cast<long>(p.num_blocks)));
-    const int hi = static_cast<int>(min(static_cast<long>(lo) + per_warp, static_cast<long>(p.num_blocks)));
-    int zeros = 0;
-    for (int b = lo; b < hi; b += 32)
-        zeros += __popc(zero_mask(p.ref_counts, b, hi, lane));
-    if (lane == 0)
-        s_warp_base[warp + 1] = zeros;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        s_warp_base[0] = 0;
-        for (int w = 0; w < kWarps; ++w)
-            s_warp_base[w + 1] += s_warp_base[w];
+    int rank = s_warp_base[warp];
+    int total_zeros = 0;
+    for (int c = 0; c < ctas; ++c) {
+        const int z = s_zeros[c];
+        rank += c < cta ? z : 0;
+        total_zeros += z;
     }
-    __syncthreads();
-    const bool enough = pages <= static_cast<unsigned long long>(s_warp_base[kWarps]);
+    const bool enough = pages <= static_cast<unsigned long long>(total_zeros);
     const bool bad = s_bad || tokens > static_cast<unsigned long long>(p.max_tokens);
     const bool ok = !bad && enough;
-    if (!ok && threadIdx.x == 0)
+    if (!ok && cta == 0 && threadIdx.x == 0)
         set_status(p.status, bad ? PKV_ERR_OUT_OF_RANGE : PKV_ERR_NO_BLOCKS);
     const int total = ok ? static_cast<int>(tokens) : 0;
     const int taken = ok ? static_cast<int>(pages) : 0;
 
+    const int thread = cta * kThreads + threadIdx.x, threads = ctas * kThreads;
     if (p.copy_pairs)
-        for (int s = threadIdx.x; s < S; s += kThreads)
+        for (int s = thread; s < S; s += threads)
             if (!ok || !(kept2[s] & 1u))
                 p.copy_pairs[2 * s] = p.copy_pairs[2 * s + 1] = -1;
     // Hand out the pages: the r-th zero count goes to the row that owns r.
-    int rank = s_warp_base[warp];
-    for (int b = lo; b < hi && rank < taken; b += 32) {
-        const unsigned m = zero_mask(p.ref_counts, b, hi, lane);
-        const int r = rank + __popc(m & ((1u << lane) - 1u));
-        if ((m >> lane & 1u) && r < taken) {
+    for (long b = lo; b < hi && rank < taken; b += 128) {
+        unsigned m = zeros4(p.ref_counts, min(b + 4 * lane, hi), hi);
+        const int c = __popc(m);
+        int upto = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(kFullMask, upto, d);
+            if (lane >= d)
+                upto += y;
+        }
+        for (int r = rank + upto - c; m && r < taken; ++r, m &= m - 1) {
+            const int32_t page = static_cast<int32_t>(b) + 4 * lane + __ffs(m) - 1;
             const int s = row_of(page_end, S, r);
             const int j = r - (s ? page_end[s - 1] : 0);
             const unsigned k2 = kept2[s];
             const int copy = k2 & 1u;
             int32_t *entry = p.block_tables + s * width + pages_of(static_cast<int>(k2 >> 1)) - copy + j;
             if (copy && j == 0) {
-                const int32_t src = *entry;
+                const int32_t src = __ldcg(entry);
                 p.copy_pairs[2 * s] = src;
-                p.copy_pairs[2 * s + 1] = b + lane;
+                p.copy_pairs[2 * s + 1] = page;
                 atomicSub(p.ref_counts + src, 1);  // at least one holder is left
             }
-            *entry = b + lane;
-            p.ref_counts[b + lane] = 1;
+            *entry = page;
+            p.ref_counts[page] = 1;
         }
-        rank += __popc(m);
+        rank += __shfl_sync(kFullMask, upto, 31);
     }
-    __syncthreads();
+    sync_all(ctas);
 
     // Slots of the reserved tokens (-1 past them), row starts, lengths.
-    for (int i = threadIdx.x; i < p.max_tokens; i += kThreads) {
+    for (int i = thread; i < p.max_tokens; i += threads) {
         int64_t slot = -1;
         if (i < total) {
             const int s = row_of(tok_end, S, i);
@@ -249,16 +347,16 @@ __global__ void __launch_bounds__(kThreads, 1) tables_step_kernel(const TablesPa
         }
         p.slot_mapping[i] = slot;
     }
-    for (int s = threadIdx.x; s < S; s += kThreads) {
+    for (int s = thread; s < S; s += threads) {
         const int end = ok ? tok_end[s] : 0;
         const int n = ok ? end - (s ? tok_end[s - 1] : 0) : 0;
         if (p.q_start)
             p.q_start[s + 1] = end;
-        const int L = p.seq_lens[s];
+        const int L = __ldcg(p.seq_lens + s);
         if (L >= 0 && L <= max_len)
             p.seq_lens[s] = static_cast<int>(kept2[s] >> 1) + n;
     }
-    if (p.q_start && threadIdx.x == 0)
+    if (p.q_start && thread == 0)
         p.q_start[0] = 0;
 }
 
@@ -318,15 +416,28 @@ pkv_status launch_tables_step(const TablesParams &p, cudaStream_t stream)
     int set = 0;
     const pkv_status rc = cache.get(&set, [](int *out) -> pkv_status {
         *out = 1;
-        return cudaFuncSetAttribute(tables_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kTablesMaxRows * kTablesRowBytes) == cudaSuccess
-                   ? PKV_OK
-                   : PKV_ERR_CUDA;
+        if (cudaFuncSetAttribute(tables_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kTablesMaxRows * kTablesRowBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(tables_step_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                 1) != cudaSuccess)
+            return PKV_ERR_CUDA;
+        return PKV_OK;
     });
     if (rc != PKV_OK)
         return rc;
-    tables_step_kernel<<<1, kThreads, static_cast<size_t>(p.num_seqs) * kTablesRowBytes, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    const int ctas = kStepCtas;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.num_seqs) * kTablesRowBytes;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tables_step_kernel, p, ctas) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 pkv_status launch_tables_fork(const int32_t *pairs, int num_pairs, int32_t *seq_lens,
