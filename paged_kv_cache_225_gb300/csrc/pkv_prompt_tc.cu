@@ -9,16 +9,18 @@
 //  * A tile is 128 rows: R = 128 / G consecutive tokens (rounded down) with
 //    their G heads.  An item is two neighbouring tiles of one sequence and KV
 //    head: every K and V block of 128 keys that reaches shared memory serves
-//    256 rows.  One persistent CTA per SM walks the items.
+//    256 rows (a tile alone would ask L2 for 64 bytes a cycle and SM).  One
+//    persistent CTA per SM walks the items.
 //  * Warps 0-3 own the rows of tile 0 (a thread per row, which is its TMEM
-//    lane), 4-7 those of tile 1, one thread of warp 8 issues the TMA loads, one
-//    of warp 9 the MMAs, and warp 10 looks the items up ahead of all of them.
+//    lane), 4-7 those of tile 1.  One thread of warp 8 issues the TMA loads, one
+//    of warp 9 the MMAs; warp 10 looks the items up ahead of all of them, warp
+//    11 watches the loads for the MMA thread, warps 12-15 write the outputs.
 //  * TMEM: scores of both tiles (2 x 128 columns, P written back over them as
 //    bf16) and both outputs (2 x head_dim columns).  Per block and tile:
 //    S = Q K^T from shared memory; the rows' threads read S, apply the limit
 //    and the softmax and write P; O += P V with P read from TMEM.  While one
 //    tile's threads work, the tensor cores run the other tile's products; P is
-//    handed over in parts of 32 keys, so that P V starts before the last
+//    handed over in two parts of 64 keys, so that P V starts before the last
 //    weights are there.
 //  * All shared-memory operands are in the 128-byte swizzle mode: [128 rows]
 //    [64 elements] per half of head_dim, K-major for Q and K, MN-major for V.
@@ -33,8 +35,25 @@
 //    must not see is not finite (redo_rows).
 //  * Every wait is bounded; a timeout records PKV_ERR_TIMEOUT, stops every role,
 //    lets copies and MMAs in flight finish and frees TMEM.
+//
+// What bounds it.  Long prompts: the tensor cores (a 32K prompt of 32 heads of
+// 128 over 8 KV heads: 5.7 ms, 1.54 PFLOP/s, 91% of what a cuBLAS product
+// sustains on the same part).  A block takes them 2 x 1024 cycles; a tile's
+// softmax of about 1200 cycles hides behind the other tile's products.  The
+// queue of the tensor cores holds about three MMAs, so the issuing thread may
+// spend only some 200 cycles between two groups: hence one barrier per group
+// (the gate), one commit per step for the ring, and a loop of its own for
+// whole blocks.  Short prompts (128 of 256 to 512 tokens, 64 heads: 521 us,
+// 3.4 TB/s): the chain load - S - softmax - P V - store of items two blocks long,
+// and the issuing thread's general steps.
+//
+// Measured and not taken (same box; 32K prompt / chat batch): an issuing thread
+// per tile 8.1 ms / 501 us (both tiles' products run interleaved, then both
+// softmaxes; taking turns costs more), scores kept in registers between the
+// maximum and the weights 5.9 ms / 530 us (spills, and code that leaves the
+// instruction caches), two threads per row 8.3 ms / 945 us, the outputs written by
+// the softmax warps 5.8 ms / 525 us, Q prefetched into L2 5.7 ms / 558 us.
 #include <climits>
-#include <type_traits>
 
 #include "pkv_prompt.cuh"
 #include "pkv_tc.cuh"
@@ -45,14 +64,16 @@ namespace {
 
 constexpr int kM = 128;     // rows of a tile
 constexpr int kKeys = 128;  // keys of a block
-constexpr int kThreads = 352;
-constexpr int kTileWarps = 4;
+constexpr int kThreads = 512;
+constexpr int kTileWarps = 4;     // warps 0 .. 7: the rows of two tiles
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kItemWarp = 10;
+constexpr int kGateWarp = 11;     // 12 .. 15: the outputs
+constexpr int kSteps = 4;         // barriers of the MMA thread's steps
 constexpr int kParts = 2;         // a block's P is handed to the MMAs in parts
 constexpr int kPart = kKeys / kParts;
-constexpr int kQueue = 4;
+constexpr int kQueue = 4;         // items looked up ahead
 constexpr int kHalf = 128 * 128;  // bytes of [128 rows][64 bf16]
 
 template <int D> struct PtGeom {
@@ -137,6 +158,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v)
 
 // Waits for the loads above and ties the values to the wait: nothing that
 // uses them can be scheduled before it.
+template <int N> __device__ __forceinline__ void tie(float (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("" : "+f"(v[i]));
+}
 template <int N> __device__ __forceinline__ void tmem_wait_ld(float (&v)[N])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
@@ -168,55 +195,59 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return o;
 }
 
-// Maximum of 64 scores.
-__device__ __forceinline__ float max64(const float *x)
+// Scores at and past `lim` become -inf.
+__device__ __forceinline__ void mask32(float (&x)[32], int lim)
 {
-    float a[8];
 #pragma unroll
-    for (int f = 0; f < 8; ++f)
-        a[f] = fmaxf(x[f], x[8 + f]);
-#pragma unroll
-    for (int e = 16; e < 64; e += 16)
-#pragma unroll
-        for (int f = 0; f < 8; ++f)
-            a[f] = fmaxf(a[f], fmaxf(x[e + f], x[e + 8 + f]));
-    return fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), fmaxf(fmaxf(a[4], a[5]), fmaxf(a[6], a[7])));
+    for (int e = 0; e < 32; ++e)
+        x[e] = e < lim ? x[e] : -INFINITY;
 }
 
-// Weights 2^(c x + off) of 64 scores: added to the sums l, stored as bf16 pairs
-// at column `col` (and what the rounding leaves, 64 columns on).  Sixteen at
+__device__ __forceinline__ float max32(const float (&x)[32])
+{
+    float a[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+        a[f] = fmaxf(x[f], x[4 + f]);
+#pragma unroll
+    for (int e = 8; e < 32; e += 8)
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+            a[f] = fmaxf(a[f], fmaxf(x[e + f], x[e + 4 + f]));
+    return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+}
+
+// Weights 2^(c x + off) of 32 scores: added to the sums l, stored as bf16 pairs
+// at column `col` (and what the rounding leaves, 16 columns on).  Sixteen at
 // a time, stage by stage, so that neighbouring instructions are independent.
 template <bool kSplit>
-__device__ __forceinline__ void weights64(const float *x, float c, float off, float2 (&l)[4], uint32_t col)
+__device__ __forceinline__ void weights32(const float (&x)[32], float c, float off, float2 (&l)[2], uint32_t col)
 {
     const float2 c2 = make_float2(c, c), off2 = make_float2(off, off);
+    uint32_t hi[16], lo[16];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t hi[16], lo[16];
+    for (int g = 0; g < 2; ++g) {
+        float2 w[8];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            float2 w[8];
+        for (int e = 0; e < 8; ++e)
+            w[e] = fma2(make_float2(x[16 * g + 2 * e], x[16 * g + 2 * e + 1]), c2, off2);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                w[e] = fma2(make_float2(x[32 * h + 16 * g + 2 * e], x[32 * h + 16 * g + 2 * e + 1]), c2, off2);
+        for (int e = 0; e < 8; ++e)
+            w[e] = make_float2(MmaSoftmax::ex2(w[e].x), MmaSoftmax::ex2(w[e].y));
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                w[e] = make_float2(MmaSoftmax::ex2(w[e].x), MmaSoftmax::ex2(w[e].y));
+        for (int e = 0; e < 8; ++e)
+            hi[8 * g + e] = pack_bf16(w[e].x, w[e].y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                hi[8 * g + e] = pack_bf16(w[e].x, w[e].y);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                l[e % 4] = add2(l[e % 4], w[e]);
-            if constexpr (kSplit)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    lo[8 * g + e] = pack_bf16(w[e].x - bf16_lo(hi[8 * g + e]), w[e].y - bf16_hi(hi[8 * g + e]));
-        }
-        tmem_st16u(col + 16 * h, hi);
+        for (int e = 0; e < 8; ++e)
+            l[e % 2] = add2(l[e % 2], w[e]);
         if constexpr (kSplit)
-            tmem_st16u(col + 64 + 16 * h, lo);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                lo[8 * g + e] = pack_bf16(w[e].x - bf16_lo(hi[8 * g + e]), w[e].y - bf16_hi(hi[8 * g + e]));
     }
+    tmem_st16u(col, hi);
+    if constexpr (kSplit)
+        tmem_st16u(col + 16, lo);
 }
 
 // 32 consecutive columns of an output row, f32 or bf16.  With 32-byte stores a
@@ -348,11 +379,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     using Geo = PtGeom<D>;
     constexpr int NS = Geo::NS;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t full[NS], empty[NS];
-    __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][kParts], pv_done[2],
-        o_free[2];
+    __shared__ __align__(8) uint64_t full[NS], step_done[kSteps];
+    __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][kParts], o_full[2],
+        o_free[2], l_full[2];
     __shared__ __align__(8) uint64_t item_full[kQueue], item_empty[kQueue], drain;
     __shared__ int s_item[kQueue][5];
+    __shared__ float s_sum[2][kM];  // the rows' sums of weights, for the output warps
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     volatile int *abort = &s_abort;
@@ -368,20 +400,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
         }
+        for (int i = 0; i < kSteps; ++i)
+            mbar_init(&step_done[i], 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&q_full[t], 1);
             mbar_init(&q_empty[t], 1);
             mbar_init(&s_full[t], 1);
             for (int i = 0; i < kParts; ++i)
-                mbar_init(&p_full[t][i], kTileWarps);
-            mbar_init(&pv_done[t], 1);
+                mbar_init(&p_full[t][i], kTileWarps + (t == 0 && i == 0));  // and the gate
+            mbar_init(&o_full[t], 1);
+            mbar_init(&l_full[t], kTileWarps);
             mbar_init(&o_free[t], kTileWarps);
         }
         for (int i = 0; i < kQueue; ++i) {
             mbar_init(&item_full[i], 1);
-            mbar_init(&item_empty[i], 2 * kTileWarps + 2);
+            mbar_init(&item_empty[i], 3 * kTileWarps + 3);
         }
         mbar_init(&drain, 1);
         s_abort = 0;
@@ -411,12 +445,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------- copies
         if (lane == 0) {
             uint32_t kv = 0;          // tiles issued
+            uint32_t steps = 0;       // steps of the MMA thread seen done
             uint32_t qn[2] = {0, 0};  // Q tiles issued
             bool ok = true;
             auto load = [&](const CUtensorMap *map, const PtItem &it, int j) {
                 const uint32_t st = kv % NS;
-                if (kv >= NS && !tc_wait(&empty[st], ((kv / NS) - 1) & 1, abort))
-                    return false;
+                // Step i (from 0) gives back tiles 2 i - 1 and 2 i of the ring's
+                // sequence K, V, K, V, ...: V of a block and the next K.
+                for (; kv >= NS && 2 * steps < kv - NS + 2; ++steps)
+                    if (!tc_wait(&step_done[steps % kSteps], (steps / kSteps) & 1, abort))
+                        return false;
                 mbar_arrive_expect_tx(&full[st], Geo::kTile);
                 for (int h = 0; h < D / 64; ++h) {
                     if (p.drop_first_copy && blockIdx.x == 0 && kv == 0 && h == 0)
@@ -469,6 +507,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
+    } else if (warp == kGateWarp) {
+        // ------------------------------------------------------- K / V gate
+        // Waits for V of block j and K of the next one and counts as the fifth
+        // arrival on tile 0's first part of P, so that the MMA thread has one
+        // barrier to look at where it would have three.
+        if (lane == 0) {
+            uint32_t st = 0, par = 0;
+            uint32_t blocks = 0;  // of tile 0
+            bool ok = true;
+            auto arrived = [&] {
+                ok = ok && tc_wait(&full[st], par, abort);
+                if (++st == NS) {
+                    st = 0;
+                    par ^= 1;
+                }
+            };
+            for (unsigned k = 0; ok; ++k) {
+                const int slot = k % kQueue;
+                ok = tc_wait(&item_full[slot], (k / kQueue) & 1, abort);
+                if (!ok)
+                    break;
+                PtItem it;
+                it.fill(s_item[slot], R);
+                mbar_arrive(&item_empty[slot]);
+                if (it.s < 0)
+                    break;
+                arrived();  // K of block 0: the MMA thread waits for it itself
+                for (int j = 0; j < it.blocks && ok; ++j) {
+                    arrived();
+                    if (j + 1 < it.blocks)
+                        arrived();
+                    if (j >= it.nb[0])
+                        continue;
+                    // Not before the block before has all its arrivals.
+                    if (blocks > 0)
+                        ok = ok && tc_wait(&p_full[0][0], (blocks - 1) & 1, abort);
+                    ++blocks;
+                    if (ok)
+                        mbar_arrive(&p_full[0][0]);
+                }
+            }
+            if (!ok) {
+                set_status(p.status, PKV_ERR_TIMEOUT);
+                *abort = 1;
+            }
+        }
+        __syncwarp();
     } else if (warp == kItemWarp) {
         // -------------------------------------------------- item look-up
         PromptScan scan;
@@ -518,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t klo0 = (ring0 >> 4) | 1u << 16, vlo0 = (ring0 >> 4) | (kHalf >> 4) << 16;
             uint32_t vst = NS - 1, vpar = 1, kst = 0, kpar = 0;  // ring positions of V (j) and K (next)
             uint32_t q_par = 0, o_par = 3, p_par = 0;            // bit t
+            uint32_t step = 0;
             unsigned k = 0;
             bool ok = true;
             // Eight MMAs of S (head_dim 128) for tile t, and of P V per part.
@@ -532,15 +618,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto mma_pv = [&](uint32_t t, int part, int steps, bool first) {
                 const uint32_t vlo = vlo0 + vst * kTileLo + part * (kPart / 16) * (2048 >> 4);
-                const uint32_t a = tmem + t * kKeys + part * (kPart / 2), d = tmem + Geo::kOCol + t * D;
+                const uint32_t a = tmem + t * kKeys + part * kPart, d = tmem + Geo::kOCol + t * D;
 #pragma unroll
                 for (int ks = 0; ks < kPart / 16; ++ks) {
                     if (ks >= steps)
                         break;
                     const uint64_t vd = desc64(vlo + ks * (2048 >> 4), kDescHi);
-                    tc_mma_ta(d, a + 8 * ks, vd, kIdPV, !(first && ks == 0));
+                    tc_mma_ta(d, a + 32 * (ks / 2) + 8 * (ks % 2), vd, kIdPV, !(first && ks == 0));
                     if constexpr (kSplit)
-                        tc_mma_ta(d, a + kKeys / 2 + 8 * ks, vd, kIdPV, true);
+                        tc_mma_ta(d, a + 32 * (ks / 2) + 16 + 8 * (ks % 2), vd, kIdPV, true);
                 }
             };
             auto next_kv = [&] {  // V of the block just scored follows its K, then the next K
@@ -586,26 +672,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = tc_wait(&o_free[0], o_par & 1, abort) && tc_wait(&o_free[1], o_par >> 1, abort);
                         o_par ^= 3;
                     }
-                    ok = ok && tc_wait(&full[vst], vpar, abort);
-#pragma unroll 1
+#pragma unroll
                     for (uint32_t t = 0; t < 2; ++t) {
+#pragma unroll
                         for (int part = 0; part < kParts; ++part) {
                             ok = ok && tc_wait(&p_full[t][part], p_par >> t & 1, abort);
                             tc_fence_after();
                             if (ok)
                                 mma_pv(t, part, kPart / 16, j == 0 && part == 0);
                         }
-                        tc_commit(&pv_done[t]);
-                        if (t == 0)
-                            ok = ok && tc_wait(&full[kst], kpar, abort);
                         if (!ok)
                             break;
                         mma_s(t, id_whole);
                         tc_commit(&s_full[t]);
                     }
                     p_par ^= 3;
-                    tc_commit(&empty[vst]);
-                    tc_commit(&empty[kst]);
+                    tc_commit(&step_done[step++ % kSteps]);
                     next_kv();
                 }
                 if (!ok)
@@ -622,7 +704,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ok = ok && tc_wait(&o_free[t], o_par >> t & 1, abort);
                             o_par ^= 1u << t;
                         }
-                        ok = ok && tc_wait(&full[vst], vpar, abort);
+                        // V is there: the gate's arrival stands for it, and tile
+                        // 0 comes first in the step.
+                        if (j >= nb0)
+                            ok = ok && tc_wait(&full[vst], vpar, abort);
                         const int steps = block_cols(nb, end, j) / 16;
                         for (int part = 0; part < kParts && kPart / 16 * part < steps; ++part) {
                             ok = ok && tc_wait(&p_full[t][part], p_par >> t & 1, abort);
@@ -631,7 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mma_pv(t, part, steps - kPart / 16 * part, j == 0 && part == 0);
                         }
                         p_par ^= 1u << t;
-                        tc_commit(&pv_done[t]);
+                        if (j + 1 == nb)
+                            tc_commit(&o_full[t]);
                     }
                     if (last && t == 0) {
                         next_item();
@@ -643,7 +729,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ok = tc_wait(&q_full[t], q_par >> t & 1, abort);
                             q_par ^= 1u << t;
                         }
-                        ok = ok && tc_wait(&full[kst], kpar, abort);
+                        // So is K, but for an item's first block and those that
+                        // tile 0 does not see.
+                        if (t == 0 ? nj == 0 : nj >= (last ? nnb0 : nb0))
+                            ok = ok && tc_wait(&full[kst], kpar, abort);
                         tc_fence_after();
                         if (ok)
                             mma_s(t, id_s0 | (static_cast<uint32_t>(block_cols(qnb, qend, nj)) >> 3) << 17);
@@ -652,11 +741,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc_commit(&q_empty[t]);
                     }
                 }
-                if (j >= 0)
-                    tc_commit(&empty[vst]);
                 if (!ok || !more)
                     break;
-                tc_commit(&empty[kst]);
+                tc_commit(&step_done[step++ % kSteps]);
                 next_kv();
                 if (last) {
                     blocks = nblocks;
@@ -677,16 +764,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp < 2 * kTileWarps) {
-        // ------------------------------------------- softmax and output
+        // ------------------------------------------------------- softmax
         const int t = warp >> 2;                // tile
         const int r = threadIdx.x & (kM - 1);   // row of the tile = TMEM lane
+        const int r_tok = r / G;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t scol = tmem + lanes + t * kKeys;
         const uint32_t ocol = tmem + lanes + Geo::kOCol + t * D;
         const float c = p.score_scale;  // positive
         constexpr float kLazy = MmaSoftmax::kLazy;
-        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         uint32_t cnt = 0;   // blocks of this tile
+        uint32_t items = 0; // its items
         uint32_t base = 0;  // ring index of the item's first K tile
         bool failed = false;
         for (unsigned k = 0; !failed; ++k) {
@@ -706,9 +794,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nt = t ? it.nt[1] : it.nt[0], nb = t ? it.nb[1] : it.nb[0];
             const int end = t ? it.end[1] : it.end[0], item_end = max(it.end[0], it.end[1]);
             const int first = it.tok0 + t * R;  // token of row 0
-            const int pos = first + min(r / G, nt - 1);
+            const int pos = first + min(r_tok, nt - 1);
             float m = -INFINITY;                // running maximum, log2 units
-            float2 l2[4] = {};                  // its sum, in eight parts
+            float2 l2[2] = {};                  // its sum, in four parts
             const int whole = (first + 1) / kKeys;  // leading blocks that every row sees whole
             for (int j = 0; j < nb; ++j, ++cnt) {
                 if (!warp_wait(&s_full[t], cnt & 1, abort)) {
@@ -719,23 +807,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool tail = j >= whole;
                 const int cols = tail ? block_cols(nb, end, j) : kKeys;
                 const bool second = cols > kPart;  // the block has keys in its second part
-                float x[kKeys];
-                tmem_ld32(scol, x);
-                tmem_ld32(scol + 32, x + 32);
-                if (second) {
-                    tmem_ld32(scol + 64, x + 64);
-                    tmem_ld32(scol + 96, x + 96);
+                // Twice through the scores, for the maximum and for the weights:
+                // keeping them would not fit the registers without spilling,
+                // and loops this short stay in the instruction caches.
+                const int lim = pos - j * kKeys + 1;  // keys this row sees
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int c0 = 0; c0 < (second ? kKeys : kPart); c0 += 64) {
+                    float x[32], y[32];
+                    tmem_ld32(scol + c0, x);
+                    tmem_ld32(scol + c0 + 32, y);
+                    tmem_wait_ld(x);
+                    tie(y);
+                    if (tail) {
+                        mask32(x, lim - c0);
+                        mask32(y, lim - c0 - 32);
+                    }
+                    mx = fmaxf(mx, fmaxf(max32(x), max32(y)));
                 }
-                tmem_wait_ld(x);
-                if (tail) {
-                    const int lim = pos - j * kKeys + 1;  // keys this row sees
-#pragma unroll
-                    for (int e = 0; e < kKeys; ++e)
-                        x[e] = e < lim ? x[e] : -INFINITY;
-                }
-                float mx = max64(x);
-                if (second)
-                    mx = fmaxf(mx, max64(x + kPart));
                 mx *= c;
                 const bool need = mx > m + kLazy;  // false when nothing is visible
                 if (__any_sync(kFullMask, need)) {
@@ -743,19 +832,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (need) {
                         alpha = m == -INFINITY ? 0.f : MmaSoftmax::ex2(m - mx);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < 2; ++i) {
                             l2[i].x *= alpha;
                             l2[i].y *= alpha;
                         }
                         m = mx;
                     }
                     if (j > 0) {
-                        // O holds earlier blocks: rescale it once their P V is done.
-                        if (!warp_wait(&pv_done[t], (cnt - 1) & 1, abort)) {
-                            failed = true;
-                            break;
-                        }
-                        tc_fence_after();
+                        // O holds earlier blocks, whose P V is done: these
+                        // scores were issued, and so completed, after it.
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 16) {
                             float ov[16];
@@ -770,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // V rows past the item's keys may hold anything.
                 const int zero0 = item_end - j * kKeys;
-                if (zero0 < cols) {
+                if (tail && zero0 < cols) {
                     const uint32_t vc = base + 2 * j + 1;
                     if (!warp_wait(&full[vc % NS], (vc / NS) & 1, abort)) {
                         failed = true;
@@ -787,20 +872,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Weights 2^(c x - m), in bf16 pairs over the consumed scores; a
                 // row of nothing but -inf so far has weights 0.
                 const float off = m == -INFINITY ? 0.f : -m;
-                weights64<kSplit>(x, c, off, l2, scol);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&p_full[t][0]);
-                if (second) {
-                    weights64<kSplit>(x + kPart, c, off, l2, scol + kPart / 2);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
+#pragma unroll 1
+                for (int part = 0; part < kParts; ++part) {
+                    if (kPart * part < cols) {
+                        const uint32_t pc = scol + kPart * part;
+                        float x[32], y[32];
+                        tmem_ld32(pc, x);
+                        tmem_ld32(pc + 32, y);
+                        tmem_wait_ld(x);
+                        tie(y);
+                        if (tail) {
+                            mask32(x, lim - kPart * part);
+                            mask32(y, lim - kPart * part - 32);
+                        }
+                        weights32<kSplit>(x, c, off, l2, pc);
+                        weights32<kSplit>(y, c, off, l2, pc + 32);
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                    }
+                    if (lane == 0)  // both parts' barriers count every block
+                        mbar_arrive(&p_full[t][part]);
                 }
-                if (lane == 0)  // both parts' barriers count every block
-                    mbar_arrive(&p_full[t][1]);
             }
             base += 2 * it.blocks;
             if (failed)
@@ -808,38 +901,92 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (nb == 0)
                 continue;
 
-            // ------------------------------------------------ output rows
-            if (!warp_wait(&pv_done[t], (cnt - 1) & 1, abort)) {
+            // The sums go to the output warps, once they have read the last ones.
+            if (items > 0 && !warp_wait(&o_free[t], (items - 1) & 1, abort)) {
                 failed = true;
                 break;
             }
-            tc_fence_after();
-            const bool live = r < nt * G;
-            const float2 lsum = add2(add2(l2[0], l2[1]), add2(l2[2], l2[3]));
-            const float inv = 1.f / (lsum.x + lsum.y);
-            const size_t orow = (static_cast<size_t>(it.row0 + pos) * p.num_q_heads + it.hkv * G + r % G) * D;
-            float bad = 0.f;  // NaN once an output is not finite
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-                float ov[32];
-                tmem_ld32(ocol + c0, ov);
-                tmem_wait_ld(ov);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    ov[e] *= inv;
-                    bad = fmaf(ov[e], 0.f, bad);
-                }
-                if (live)
-                    store_out32<kSplit>(p, orow + c0, ov, wide);
-            }
-            tc_fence_before();
+            ++items;
+            const float2 lsum = add2(l2[0], l2[1]);
+            s_sum[t][r] = lsum.x + lsum.y;
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&o_free[t]);
-            const unsigned redo = __ballot_sync(kFullMask, live && bad != 0.f);
-            if (redo)
-                redo_rows<D, kSplit>(p, redo, 32 * (warp & 3), first, it.row0, it.hkv,
-                                     min((nb - 1) * kKeys + block_cols(nb, end, nb - 1), item_end), lane);
+                mbar_arrive(&l_full[t]);
+        }
+        if (failed && lane == 0) {
+            set_status(p.status, PKV_ERR_TIMEOUT);
+            *abort = 1;
+        }
+        __syncwarp();
+    } else {
+        // --------------------------------------------------- output rows
+        // Four warps of their own, for both tiles in turn: the rows' threads go
+        // on with the next item while its predecessor's output is read, scaled
+        // and stored.
+        const int r = 32 * (warp & 3) + lane;
+        const int r_tok = r / G, r_head = r % G;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+        uint32_t par = 0;  // bit t: parity of the tile's barriers
+        bool failed = false;
+        for (unsigned k = 0; !failed; ++k) {
+            const int slot = k % kQueue;
+            if (!warp_wait(&item_full[slot], (k / kQueue) & 1, abort)) {
+                failed = true;
+                break;
+            }
+            PtItem it;
+            it.fill(s_item[slot], R);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&item_empty[slot]);
+            if (it.s < 0)
+                break;
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {
+                const int nt = t ? it.nt[1] : it.nt[0], nb = t ? it.nb[1] : it.nb[0];
+                const int end = t ? it.end[1] : it.end[0];
+                if (nb == 0)
+                    continue;
+                const int first = it.tok0 + t * R;
+                const uint32_t ocol = tmem + lanes + Geo::kOCol + t * D;
+                if (!warp_wait(&l_full[t], par >> t & 1, abort) ||
+                    !warp_wait(&o_full[t], par >> t & 1, abort)) {
+                    failed = true;
+                    break;
+                }
+                par ^= 1u << t;
+                tc_fence_after();
+                const float inv = 1.f / s_sum[t][r];
+                const bool live = r < nt * G;
+                const size_t orow = (static_cast<size_t>(it.row0 + first + min(r_tok, nt - 1)) * p.num_q_heads +
+                                     it.hkv * G + r_head) * D;
+                float bad = 0.f;  // NaN once an output is not finite
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    float ov[32];
+                    tmem_ld32(ocol + c0, ov);
+                    tmem_wait_ld(ov);
+                    if (c0 + 32 == D) {  // read whole: the next item's P V may start
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&o_free[t]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        ov[e] *= inv;
+                        bad = fmaf(ov[e], 0.f, bad);
+                    }
+                    if (live)
+                        store_out32<kSplit>(p, orow + c0, ov, wide);
+                }
+                const unsigned redo = __ballot_sync(kFullMask, live && bad != 0.f);
+                if (redo)
+                    redo_rows<D, kSplit>(p, redo, 32 * (warp & 3), first, it.row0, it.hkv,
+                                         min((nb - 1) * kKeys + block_cols(nb, end, nb - 1),
+                                             max(it.end[0], it.end[1])), lane);
+            }
         }
         if (failed && lane == 0) {
             set_status(p.status, PKV_ERR_TIMEOUT);
