@@ -639,18 +639,26 @@ def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, pairs: torch.Tenso
         raise PkvError(rc, "pkv_copy_blocks")
 
 
-def _launch(fn, dev: torch.device, stream: Optional[torch.cuda.Stream], args) -> int:
-    """``fn(*args, stream pointer)`` with ``dev`` as the current device."""
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's pointer, without an object
+_I32, _I64 = torch.int32, torch.int64
+
+
+def _launch(name: str, index: int, stream: Optional[torch.cuda.Stream], args) -> None:
+    """Library call ``name(*args, stream pointer)`` with device ``index`` as the current one."""
+    fn = getattr(_lib if _lib is not None else lib(), name)
     if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream belongs to {stream.device}, the tensors to {dev}")
+        if stream.device.index != index:
+            raise ValueError(f"stream belongs to {stream.device}, the tensors to cuda:{index}")
         s = stream.cuda_stream
     else:
-        s = torch._C._cuda_getCurrentRawStream(dev.index)
-    if torch.cuda.current_device() == dev.index:
-        return fn(*args, s)
-    with torch.cuda.device(dev):
-        return fn(*args, s)
+        s = _raw_stream(index)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, s)
+    if rc != 0:
+        raise PkvError(rc, name)
 
 
 def _ptr(t: Optional[torch.Tensor], what: str, ndim: int, dtype: torch.dtype, index: int):
@@ -658,7 +666,7 @@ def _ptr(t: Optional[torch.Tensor], what: str, ndim: int, dtype: torch.dtype, in
     ``index``, None for None; anything else raises."""
     if t is None:
         return None
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == index
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
             and t.dim() == ndim and t.is_contiguous()):
         return t.data_ptr()
     _check(t, what, ndim, torch.device("cuda", index))
@@ -668,24 +676,29 @@ def _ptr(t: Optional[torch.Tensor], what: str, ndim: int, dtype: torch.dtype, in
 def _cuda_index(t: torch.Tensor, what: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch.Tensor")
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0 or not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor (the library has no CPU path)")
-    return t.get_device()
+    return index
 
 
-def _check_rows(t: torch.Tensor, what: str, dtype: torch.dtype, index: int):
-    """(rows, heads, head_dim, row stride in elements) of a tensor whose rows are dense."""
+def _rows(t: torch.Tensor, what: str, dtype: torch.dtype, index: int):
+    """(shape, row stride in elements) of a [T, H, D] tensor whose rows are dense."""
     if _cuda_index(t, what) != index:
         raise ValueError(f"{what} is on {t.device}, expected cuda:{index}")
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {str(dtype).replace('torch.', '')} like q")
-    if t.dim() != 3:
-        raise ValueError(f"{what} must have 3 dims, got {tuple(t.shape)}")
-    T, H, D = t.shape
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{what} must have 3 dims, got {tuple(shape)}")
+    T, H, D = shape
     row, head, elem = t.stride()
     if T > 0 and ((D > 1 and elem != 1) or (H > 1 and head != D)):
         raise ValueError(f"{what}: every row must be dense")
-    return T, H, D, (row if T > 1 else H * D)
+    return shape, (row if T > 1 else H * D)
+
+
+_FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor,
@@ -702,34 +715,40 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torc
     errors.  Returns ``out``.
     """
     index = _cuda_index(q, "q")
-    code = _dtype_code(q, "q")
-    T, Hq, D, qs = _check_rows(q, "q", q.dtype, index)
-    kT, Hkv, kD, ks = _check_rows(k, "k", q.dtype, index)
-    vT, vH, vD, vs = _check_rows(v, "v", q.dtype, index)
-    o = _ptr(out, "out", 3, out.dtype if isinstance(out, torch.Tensor) else q.dtype, index)
-    starts = _ptr(q_start, "q_start", 1, torch.int32, index)
-    st = _ptr(status, "status", 1, torch.int32, index)
-    S = q_start.shape[0] - 1
-    if kT != T or kD != D or (vT, vH, vD) != (kT, Hkv, kD) or out.shape != q.shape:
+    dtype = q.dtype
+    code = _FLOATS.get(dtype)
+    if code is None:
+        raise TypeError(f"q: unsupported dtype {dtype}")
+    qshape, qs = _rows(q, "q", dtype, index)
+    kshape, ks = _rows(k, "k", dtype, index)
+    vshape, vs = _rows(v, "v", dtype, index)
+    odtype = out.dtype if isinstance(out, torch.Tensor) else dtype
+    ocode = _FLOATS.get(odtype)
+    if ocode is None:
+        raise TypeError(f"out: unsupported dtype {odtype}")
+    o = _ptr(out, "out", 3, odtype, index)
+    starts = _ptr(q_start, "q_start", 1, _I32, index)
+    st = _ptr(status, "status", 1, _I32, index)
+    T, Hq, D = qshape
+    S = q_start.numel() - 1
+    if kshape[0] != T or kshape[2] != D or vshape != kshape or out.shape != qshape:
         raise ValueError("inconsistent shapes")
-    if S < 0 or (status is not None and status.shape[0] != 1):
+    if S < 0 or (status is not None and status.numel() != 1):
         raise ValueError("q_start needs at least one entry, status exactly one")
-    rc = _launch(lib().pkv_prompt_attn, q.device, stream,
-                 (q.data_ptr(), k.data_ptr(), v.data_ptr(), code, qs, ks, vs, starts, S, T, Hq, Hkv,
-                  D, T if max_q_len is None else int(max_q_len), float(scale), o,
-                  _dtype_code(out, "out"), st, int(flags)))
-    if rc != 0:
-        raise PkvError(rc, "pkv_prompt_attn")
+    _launch("pkv_prompt_attn", index, stream,
+            (q.data_ptr(), k.data_ptr(), v.data_ptr(), code, qs, ks, vs, starts, S, T, Hq,
+             kshape[1], D, T if max_q_len is None else int(max_q_len), float(scale), o, ocode, st,
+             int(flags)))
     return out
 
 
 def _pool(seq_lens, block_tables, ref_counts):
     index = _cuda_index(seq_lens, "seq_lens")
-    ptrs = (_ptr(seq_lens, "seq_lens", 1, torch.int32, index),
-            _ptr(block_tables, "block_tables", 2, torch.int32, index),
-            _ptr(ref_counts, "ref_counts", 1, torch.int32, index))
+    ptrs = (_ptr(seq_lens, "seq_lens", 1, _I32, index),
+            _ptr(block_tables, "block_tables", 2, _I32, index),
+            _ptr(ref_counts, "ref_counts", 1, _I32, index))
     S, width = block_tables.shape
-    if S != seq_lens.shape[0]:
+    if S != seq_lens.numel():
         raise ValueError("block_tables needs one row per entry of seq_lens")
     return index, ptrs, S, width
 
@@ -753,22 +772,18 @@ def tables_step(seq_lens: torch.Tensor, block_tables: torch.Tensor, ref_counts: 
     pages for ``copy_blocks`` without a status, else -1).  ``status`` int32 [1].
     """
     index, (lens, tables, refs), S, width = _pool(seq_lens, block_tables, ref_counts)
-    i32 = torch.int32
-    drop, new = _ptr(drop_lens, "drop_lens", 1, i32, index), _ptr(new_lens, "new_lens", 1, i32, index)
-    starts, pairs = _ptr(q_start, "q_start", 1, i32, index), _ptr(copy_pairs, "copy_pairs", 2, i32, index)
-    slots = _ptr(slot_mapping, "slot_mapping", 1, torch.int64, index)
-    st = _ptr(status, "status", 1, i32, index)
-    if ((drop_lens is not None and drop_lens.shape[0] != S)
-            or (new_lens is not None and new_lens.shape[0] != S)
-            or (q_start is not None and q_start.shape[0] != S + 1)
-            or (copy_pairs is not None and copy_pairs.shape != (S, 2))
-            or (status is not None and status.shape[0] != 1)):
+    drop, new = _ptr(drop_lens, "drop_lens", 1, _I32, index), _ptr(new_lens, "new_lens", 1, _I32, index)
+    starts, pairs = _ptr(q_start, "q_start", 1, _I32, index), _ptr(copy_pairs, "copy_pairs", 2, _I32, index)
+    slots = _ptr(slot_mapping, "slot_mapping", 1, _I64, index)
+    st = _ptr(status, "status", 1, _I32, index)
+    if ((drop is not None and drop_lens.numel() != S) or (new is not None and new_lens.numel() != S)
+            or (starts is not None and q_start.numel() != S + 1)
+            or (pairs is not None and copy_pairs.shape != (S, 2))
+            or (st is not None and status.numel() != 1)):
         raise ValueError("inconsistent shapes")
-    rc = _launch(lib().pkv_tables_step, seq_lens.device, stream,
-                 (lens, tables, refs, S, width, block_size, ref_counts.shape[0], drop, new, starts,
-                  slots, 0 if slots is None else slot_mapping.shape[0], pairs, st))
-    if rc != 0:
-        raise PkvError(rc, "pkv_tables_step")
+    _launch("pkv_tables_step", index, stream,
+            (lens, tables, refs, S, width, block_size, ref_counts.numel(), drop, new, starts, slots,
+             0 if slots is None else slot_mapping.numel(), pairs, st))
 
 
 def tables_fork(pairs: torch.Tensor, seq_lens: torch.Tensor, block_tables: torch.Tensor,
@@ -779,15 +794,13 @@ def tables_fork(pairs: torch.Tensor, seq_lens: torch.Tensor, block_tables: torch
     (int32 [n, 2]) the free row child gets parent's length and pages, each with
     one more reference.  Other arguments as for ``tables_step``."""
     index, (lens, tables, refs), S, width = _pool(seq_lens, block_tables, ref_counts)
-    ptr = _ptr(pairs, "pairs", 2, torch.int32, index)
-    st = _ptr(status, "status", 1, torch.int32, index)
-    if pairs.shape[1] != 2 or (status is not None and status.shape[0] != 1):
+    ptr = _ptr(pairs, "pairs", 2, _I32, index)
+    st = _ptr(status, "status", 1, _I32, index)
+    n, two = pairs.shape
+    if two != 2 or (st is not None and status.numel() != 1):
         raise ValueError("pairs must be int32 [n, 2], status int32 [1]")
-    rc = _launch(lib().pkv_tables_fork, seq_lens.device, stream,
-                 (ptr, pairs.shape[0], lens, tables, refs, S, width, block_size,
-                  ref_counts.shape[0], st))
-    if rc != 0:
-        raise PkvError(rc, "pkv_tables_fork")
+    _launch("pkv_tables_fork", index, stream,
+            (ptr, n, lens, tables, refs, S, width, block_size, ref_counts.numel(), st))
 
 
 class BlockManager:

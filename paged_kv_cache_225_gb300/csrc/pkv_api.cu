@@ -904,6 +904,7 @@ pkv_status pkv_tables_step(int32_t *seq_lens, int32_t *block_tables, int32_t *re
     p.max_tokens = max_tokens;
     p.q_start = q_start;
     p.slot_mapping = slot_mapping;
+    p.wide_slots = aligned(slot_mapping, 16) ? 1 : 0;
     p.copy_pairs = copy_pairs;
     p.status = status;
     return launch_tables_step(p, static_cast<cudaStream_t>(stream));

@@ -131,6 +131,7 @@ struct TablesParams {
     int num_seqs, max_blocks, num_blocks, max_tokens;
     int32_t *q_start;          // [S + 1] or null
     int64_t *slot_mapping;     // [max_tokens]
+    int wide_slots;            // slot_mapping is 16-byte aligned
     int32_t *copy_pairs;       // [S, 2] or null
     int32_t *status;           // optional
 };

@@ -9,9 +9,17 @@
 // (scores in log2 units): for a block of keys with scores x,
 //   m' = max(m, max x),  l' = l 2^(m - m') + sum 2^(x - m'),
 //   o' = o 2^(m - m') + sum 2^(x - m') v,   out = o / l.
+// Everything stays in f32: tensor-core products of split operands would lose
+// the last bits in their accumulation.
+//
 // A CTA holds 64 rows (token, grouped head) and walks 64 keys at a time, all
-// operands in shared memory as f32; a thread owns 8 rows x 4 keys of the
-// scores and 8 rows x D / 16 columns of the output.
+// operands in shared memory; a thread owns 8 rows x 4 keys of the scores and 8
+// rows x D / 16 columns of the output.  Products are packed two to an
+// instruction (fma.rn.f32x2): the scores sum even and odd dims in the halves,
+// the output holds pairs of columns.  Shared-memory loads bound it: a 16-byte
+// load of a warp takes four cycles, and a thread needs 12 of them for 64 packed
+// multiply-adds of the scores (32 cycles), 16 for 128 of the output (8 prompts of
+// 256 to 1024 tokens, 32 heads of 128 over 8 KV heads: PKV_F32).
 #include "pkv_prompt.cuh"
 
 namespace pkv {
@@ -23,15 +31,33 @@ constexpr int kKeys = 64;
 constexpr int kSimtThreads = 128;
 
 template <int D> struct SimtGeom {
-    static constexpr int kLd = D + 4;  // row stride of Q and K: rows 4 banks apart
-    static constexpr int kPLd = kKeys + 4;
-    static constexpr int kFloats = kRows * kLd + kKeys * kLd + kKeys * D + kRows * kPLd;
+    static constexpr int kLd = D + 4;          // row stride of Q and K: rows 4 banks apart
+    static constexpr int kPLd = kKeys + 4;     // and of the weights
+    // The weights take K's place once the scores are done.
+    static constexpr int kKP = kKeys * kLd > kRows * kPLd ? kKeys * kLd : kRows * kPLd;
+    static constexpr int kFloats = kRows * kLd + kKP + kKeys * D;
     static constexpr int kSmem = kFloats * 4;
 };
 
-__device__ __forceinline__ float4 load4(const void *base, size_t off)
+__device__ __forceinline__ void fma2(uint64_t &c, uint64_t a, uint64_t b)
 {
-    return __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ void mul2(uint64_t &c, uint64_t a)
+{
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(c) : "l"(a));
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
 }
 
 template <int D>
@@ -41,191 +67,220 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
     constexpr int kLd = Geo::kLd, kPLd = Geo::kPLd;
     constexpr int kCols = D / 64;  // float4 columns of the output per thread
     extern __shared__ __align__(16) float smem_f[];
-    float *sq = smem_f, *sk = sq + kRows * kLd, *sv = sk + kKeys * kLd, *sp = sv + kKeys * D;
+    float *sq = smem_f, *sk = sq + kRows * kLd, *sv = sk + Geo::kKP, *sp = sk;
     __shared__ PromptItem s_item;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = p.group;
     const int tokens = kRows / G;  // tokens per item
-    if (warp == 0) {
-        PromptScan scan;
-        scan.init(p, tokens, lane, blockIdx.x == 0);
-        const PromptItem it = scan.find(p, tokens, blockIdx.x, lane);
-        if (lane == 0)
-            s_item = it;
-    }
-    __syncthreads();
-    const PromptItem it = s_item;
-    if (it.s < 0)
-        return;
-    const int t0 = it.index * tokens;               // first token of the item
-    const int nt = min(tokens, it.n - t0);          // its tokens
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const float *q = static_cast<const float *>(p.q);
+    const float *k = static_cast<const float *>(p.k), *v = static_cast<const float *>(p.v);
+    const float c = p.negate ? -p.score_scale : p.score_scale;
 
-    for (int e = threadIdx.x; e < kRows * (D / 4); e += kSimtThreads) {
-        const int r = e / (D / 4), c = 4 * (e % (D / 4));
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < nt * G)
-            v = load4(p.q,
-                      (static_cast<size_t>(it.row0) + t0 + r / G) * p.q_stride +
-                          static_cast<size_t>(it.hkv * G + r % G) * D + c);
-        *reinterpret_cast<float4 *>(sq + r * kLd + c) = v;
-    }
-
-    float o[8][4 * kCols], m[8], l[8];
-    int pos[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-        pos[i] = t0 + min((ty + 8 * i) / G, nt - 1);  // rows past the item repeat its last token
-#pragma unroll
-        for (int c = 0; c < 4 * kCols; ++c)
-            o[i][c] = 0.f;
-    }
-
-    const int end = t0 + nt;  // keys any row of the item sees
-    for (int k0 = 0; k0 < end; k0 += kKeys) {
-        __syncthreads();  // the last block's reads are done
-        for (int e = threadIdx.x; e < kKeys * (D / 4); e += kSimtThreads) {
-            const int r = e / (D / 4), c = 4 * (e % (D / 4));
-            float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
-            if (k0 + r < end) {
-                const size_t tok = static_cast<size_t>(it.row0) + k0 + r;
-                const size_t col = static_cast<size_t>(it.hkv) * D + c;
-                kk = load4(p.k, tok * p.k_stride + col);
-                vv = load4(p.v, tok * p.v_stride + col);
-            }
-            *reinterpret_cast<float4 *>(sk + r * kLd + c) = kk;
-            *reinterpret_cast<float4 *>(sv + r * D + c) = vv;
+    PromptScan scan;
+    if (warp == 0)
+        scan.init(p, tokens, lane, blockIdx.x == 0);
+    for (unsigned u = blockIdx.x;; u += gridDim.x) {
+        if (warp == 0) {
+            const PromptItem found = scan.find(p, tokens, u, lane);
+            if (lane == 0)
+                s_item = found;
         }
         __syncthreads();
-        float x[8][4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                x[i][j] = 0.f;
-#pragma unroll 2
-        for (int d = 0; d < D; d += 4) {
-            float4 kf[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                kf[j] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * j) * kLd + d);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float4 qf = *reinterpret_cast<const float4 *>(sq + (ty + 8 * i) * kLd + d);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    x[i][j] = fmaf(qf.x, kf[j].x, fmaf(qf.y, kf[j].y, fmaf(qf.z, kf[j].z, fmaf(qf.w, kf[j].w, x[i][j]))));
-            }
+        const PromptItem it = s_item;
+        if (it.s < 0)
+            return;
+        const int t0 = it.index * tokens;       // first token of the item
+        const int nt = min(tokens, it.n - t0);  // its tokens
+        const int end = t0 + nt;                // keys any of its rows sees
+
+        for (int e = threadIdx.x; e < kRows * (D / 4); e += kSimtThreads) {
+            const int r = e / (D / 4), d = 4 * (e % (D / 4));
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < nt * G)
+                x = __ldg(reinterpret_cast<const float4 *>(
+                    q + (static_cast<size_t>(it.row0) + t0 + r / G) * p.q_stride +
+                    static_cast<size_t>(it.hkv * G + r % G) * D + d));
+            *reinterpret_cast<float4 *>(sq + r * kLd + d) = x;
         }
-        const float c = p.negate ? -p.score_scale : p.score_scale;
-        const bool masked = k0 + kKeys > t0 + 1;  // some row does not see some key
+
+        uint64_t o[8][2 * kCols];
+        float m[8], l[8];
+        int pos[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float mx = -INFINITY;
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+            pos[i] = t0 + min((ty + 8 * i) / G, nt - 1);  // rows past the item repeat its last token
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool seen = k0 + tx + 16 * j <= pos[i];
-                x[i][j] = seen ? x[i][j] * c : -INFINITY;
-                mx = fmaxf(mx, x[i][j]);
-            }
-#pragma unroll
-            for (int w = 8; w >= 1; w >>= 1)
-                mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, w));
-            const float m_new = fmaxf(m[i], mx);
-            // Nothing but -inf so far: any finite offset gives weights 0.
-            const float off = m_new == -INFINITY ? 0.f : m_new;
-            const float alpha = exp2f(m[i] - off);
-            m[i] = m_new;
-            l[i] *= alpha;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float w = exp2f(x[i][j] - off);
-                l[i] += w;
-                sp[(ty + 8 * i) * kPLd + tx + 16 * j] = w;
-            }
-#pragma unroll
-            for (int c = 0; c < 4 * kCols; ++c)
-                o[i][c] *= alpha;
+            for (int x = 0; x < 2 * kCols; ++x)
+                o[i][x] = 0;
         }
-        __syncwarp();  // a row's weights are written and read by one half warp
-        const int keys = min(kKeys, end - k0);
-        if (!masked) {
-#pragma unroll 1
-            for (int k = 0; k < kKeys; k += 4) {
-                float4 vf[4][kCols];
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-                    for (int c = 0; c < kCols; ++c)
-                        vf[kk][c] = *reinterpret_cast<const float4 *>(sv + (k + kk) * D + 4 * tx + 64 * c);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 w = *reinterpret_cast<const float4 *>(sp + (ty + 8 * i) * kPLd + k);
-                    const float ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-                        for (int c = 0; c < kCols; ++c) {
-                            o[i][4 * c] = fmaf(ww[kk], vf[kk][c].x, o[i][4 * c]);
-                            o[i][4 * c + 1] = fmaf(ww[kk], vf[kk][c].y, o[i][4 * c + 1]);
-                            o[i][4 * c + 2] = fmaf(ww[kk], vf[kk][c].z, o[i][4 * c + 2]);
-                            o[i][4 * c + 3] = fmaf(ww[kk], vf[kk][c].w, o[i][4 * c + 3]);
-                        }
-                }
+
+        for (int k0 = 0; k0 < end; k0 += kKeys) {
+            __syncthreads();  // the last block's reads are done
+            for (int e = threadIdx.x; e < kKeys * (D / 4); e += kSimtThreads) {
+                const int r = e / (D / 4), d = 4 * (e % (D / 4));
+                float *dk = sk + r * kLd + d;
+                if (k0 + r < end)
+                    cp_async_16(dk, k + (static_cast<size_t>(it.row0) + k0 + r) * p.k_stride +
+                                        static_cast<size_t>(it.hkv) * D + d);
+                else
+                    *reinterpret_cast<float4 *>(dk) = make_float4(0.f, 0.f, 0.f, 0.f);
             }
-        } else {
-            // Masked block: a key a row does not see adds nothing to it, not
-            // even 0 * inf.
-#pragma unroll 1
-            for (int k = 0; k < keys; ++k) {
-                float4 vf[kCols];
+            cp_async_commit();
+            for (int e = threadIdx.x; e < kKeys * (D / 4); e += kSimtThreads) {
+                const int r = e / (D / 4), d = 4 * (e % (D / 4));
+                float *dv = sv + r * D + d;
+                if (k0 + r < end)
+                    cp_async_16(dv, v + (static_cast<size_t>(it.row0) + k0 + r) * p.v_stride +
+                                        static_cast<size_t>(it.hkv) * D + d);
+                else
+                    *reinterpret_cast<float4 *>(dv) = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            cp_async_commit();
+            asm volatile("cp.async.wait_group 1;" ::: "memory");  // K; V may still be on its way
+            __syncthreads();
+            uint64_t acc[8][4];
 #pragma unroll
-                for (int c = 0; c < kCols; ++c)
-                    vf[c] = *reinterpret_cast<const float4 *>(sv + k * D + 4 * tx + 64 * c);
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[i][j] = 0;
+#pragma unroll 2
+            for (int d = 0; d < D; d += 4) {
+                ulonglong2 kf[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    kf[j] = *reinterpret_cast<const ulonglong2 *>(sk + (tx + 16 * j) * kLd + d);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    if (k0 + k > pos[i])
-                        continue;
-                    const float w = sp[(ty + 8 * i) * kPLd + k];
+                    const ulonglong2 qf = *reinterpret_cast<const ulonglong2 *>(sq + (ty + 8 * i) * kLd + d);
 #pragma unroll
-                    for (int c = 0; c < kCols; ++c) {
-                        o[i][4 * c] = fmaf(w, vf[c].x, o[i][4 * c]);
-                        o[i][4 * c + 1] = fmaf(w, vf[c].y, o[i][4 * c + 1]);
-                        o[i][4 * c + 2] = fmaf(w, vf[c].z, o[i][4 * c + 2]);
-                        o[i][4 * c + 3] = fmaf(w, vf[c].w, o[i][4 * c + 3]);
+                    for (int j = 0; j < 4; ++j) {
+                        fma2(acc[i][j], qf.x, kf[j].x);
+                        fma2(acc[i][j], qf.y, kf[j].y);
                     }
                 }
             }
-        }
-    }
+            cp_async_wait_all();
+            __syncthreads();  // K is read, V is there
 
+            const bool masked = k0 + kKeys > t0 + 1;  // some row does not see some key
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float sum = l[i];
+            for (int i = 0; i < 8; ++i) {
+                float x[4];
+                float mx = -INFINITY;
 #pragma unroll
-        for (int w = 8; w >= 1; w >>= 1)
-            sum += __shfl_xor_sync(kFullMask, sum, w);
-        const int r = ty + 8 * i;
-        if (r >= nt * G)
-            continue;
-        const size_t orow = ((static_cast<size_t>(it.row0) + t0 + r / G) * p.num_q_heads +
-                             it.hkv * G + r % G) * D;
+                for (int j = 0; j < 4; ++j) {
+                    const float2 s = unpair(acc[i][j]);
+                    x[j] = k0 + tx + 16 * j <= pos[i] ? (s.x + s.y) * c : -INFINITY;
+                    mx = fmaxf(mx, x[j]);
+                }
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-            const size_t off = orow + 4 * tx + 64 * c;
-            const float4 v = make_float4(o[i][4 * c] / sum, o[i][4 * c + 1] / sum,
-                                         o[i][4 * c + 2] / sum, o[i][4 * c + 3] / sum);
-            if (p.out_dtype == PKV_F32) {
-                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + off) = v;
+                for (int w = 8; w >= 1; w >>= 1)
+                    mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, w));
+                const float m_new = fmaxf(m[i], mx);
+                // Nothing but -inf so far: any finite offset gives weights 0.
+                const float off = m_new == -INFINITY ? 0.f : m_new;
+                const float alpha = exp2f(m[i] - off);
+                m[i] = m_new;
+                l[i] *= alpha;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float w = exp2f(x[j] - off);
+                    l[i] += w;
+                    sp[(ty + 8 * i) * kPLd + tx + 16 * j] = w;
+                }
+                const uint64_t a2 = pair(alpha, alpha);
+#pragma unroll
+                for (int x2 = 0; x2 < 2 * kCols; ++x2)
+                    mul2(o[i][x2], a2);
+            }
+            // A key a row does not see adds nothing to it, not even 0 * inf:
+            // with infinities or NaN among V, a masked block goes key by key.
+            bool careful = false;
+            if (masked) {
+                for (int e = threadIdx.x; e < kKeys * (D / 4); e += kSimtThreads) {
+                    const float4 x = *reinterpret_cast<const float4 *>(sv + 4 * e);
+                    careful = careful || !(x.x * 0.f == 0.f && x.y * 0.f == 0.f && x.z * 0.f == 0.f &&
+                                           x.w * 0.f == 0.f);
+                }
+                careful = __syncthreads_or(careful);
+            }
+            __syncwarp();  // a row's weights are written and read by one half warp
+            if (!careful) {
+#pragma unroll 1
+                for (int key = 0; key < kKeys; key += 4) {
+                    ulonglong2 vf[4][kCols];
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                        for (int x = 0; x < kCols; ++x)
+                            vf[kk][x] = *reinterpret_cast<const ulonglong2 *>(sv + (key + kk) * D + 4 * tx + 64 * x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 w = *reinterpret_cast<const float4 *>(sp + (ty + 8 * i) * kPLd + key);
+                        const float ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint64_t w2 = pair(ww[kk], ww[kk]);
+#pragma unroll
+                            for (int x = 0; x < kCols; ++x) {
+                                fma2(o[i][2 * x], w2, vf[kk][x].x);
+                                fma2(o[i][2 * x + 1], w2, vf[kk][x].y);
+                            }
+                        }
+                    }
+                }
             } else {
-                uint2 w;
-                w.x = pack_bf16(v.x, v.y);
-                w.y = pack_bf16(v.z, v.w);
-                *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(p.out) + off) = w;
+                const int keys = min(kKeys, end - k0);
+#pragma unroll 1
+                for (int key = 0; key < keys; ++key)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (k0 + key > pos[i])
+                            continue;
+                        const float w1 = sp[(ty + 8 * i) * kPLd + key];
+                        const uint64_t w = pair(w1, w1);
+#pragma unroll
+                        for (int x = 0; x < kCols; ++x) {
+                            const ulonglong2 vf =
+                                *reinterpret_cast<const ulonglong2 *>(sv + key * D + 4 * tx + 64 * x);
+                            fma2(o[i][2 * x], w, vf.x);
+                            fma2(o[i][2 * x + 1], w, vf.y);
+                        }
+                    }
             }
         }
+
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float sum = l[i];
+#pragma unroll
+            for (int w = 8; w >= 1; w >>= 1)
+                sum += __shfl_xor_sync(kFullMask, sum, w);
+            const int r = ty + 8 * i;
+            if (r >= nt * G)
+                continue;
+            const size_t orow = ((static_cast<size_t>(it.row0) + t0 + r / G) * p.num_q_heads +
+                                 it.hkv * G + r % G) * D;
+#pragma unroll
+            for (int x = 0; x < kCols; ++x) {
+                const size_t off = orow + 4 * tx + 64 * x;
+                const float2 a = unpair(o[i][2 * x]), b = unpair(o[i][2 * x + 1]);
+                const float4 y = make_float4(a.x / sum, a.y / sum, b.x / sum, b.y / sum);
+                if (p.out_dtype == PKV_F32) {
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + off) = y;
+                } else {
+                    uint2 w;
+                    w.x = pack_bf16(y.x, y.y);
+                    w.y = pack_bf16(y.z, y.w);
+                    *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(p.out) + off) = w;
+                }
+            }
+        }
+        __syncthreads();  // the item is read before the next one is written
     }
 }
 
@@ -245,9 +300,12 @@ template <int D> pkv_status launch_simt_d(const PromptParams &p, cudaStream_t st
     const long items = prompt_max_items(p, kRows / p.group);
     if (items <= 0)
         return PKV_OK;
-    if (items > 0x7fffffffL)
+    if (items > 0x40000000L)
         return PKV_ERR_UNSUPPORTED;
-    prompt_simt_kernel<D><<<static_cast<unsigned>(items), kSimtThreads, SimtGeom<D>::kSmem, stream>>>(p);
+    // Two CTAs to an SM; the costliest items go first, one at a time.
+    const long slots = 2L * device_sm_count();
+    prompt_simt_kernel<D><<<static_cast<unsigned>(items < slots ? items : slots), kSimtThreads,
+                            SimtGeom<D>::kSmem, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

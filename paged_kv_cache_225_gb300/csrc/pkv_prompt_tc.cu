@@ -374,7 +374,7 @@ __device__ __noinline__ void redo_rows(const PromptParams &p, unsigned rows, int
 
 template <int D, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
-    prompt_tc_kernel(const PromptParams p, const __grid_constant__ PromptMaps maps)
+    prompt_tc_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ PromptMaps maps)
 {
     using Geo = PtGeom<D>;
     constexpr int NS = Geo::NS;
@@ -420,6 +420,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&drain, 1);
         s_abort = 0;
         fence_mbar_init();
+    }
+    if (warp == kProducerWarp && lane < 3) {
+        const CUtensorMap *map = lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
     }
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(

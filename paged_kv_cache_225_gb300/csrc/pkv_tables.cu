@@ -31,15 +31,14 @@ constexpr int kStepCtas = 16;
 
 __device__ __forceinline__ int pages_of(int tokens) { return (tokens + kBlockSize - 1) / kBlockSize; }
 
-// Orders every CTA's accesses (shared and global) before the barrier with
-// those after it.  A cluster of one needs only the block's barrier.
-__device__ __forceinline__ void sync_all(int ctas)
+// A cluster barrier in two halves: what a CTA did before the first (shared and
+// global memory) is visible to every CTA after the second.
+__device__ __forceinline__ void cluster_arrive()
 {
-    if (ctas == 1) {
-        __syncthreads();
-        return;
-    }
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait()
+{
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -97,64 +96,82 @@ __device__ __forceinline__ int row_of(const int *ends, int n, int i)
     return lo;
 }
 
-// Which of the four counts from id on are zero (bits 0..3); ids from `end` on
-// are not.  id is a multiple of 4 and the counts are 16-byte aligned.
-__device__ __forceinline__ unsigned zeros4(const int32_t *ref, long id, long end)
+// Lanes whose count is zero among the 32 from id on (ids from `end` on are not).
+__device__ __forceinline__ unsigned zero_mask(const int32_t *ref, long id, long end, int lane)
 {
-    if (id + 4 <= end) {
-        const int4 v = __ldcg(reinterpret_cast<const int4 *>(ref + id));
-        return (v.x == 0) | (v.y == 0) << 1 | (v.z == 0) << 2 | (v.w == 0) << 3;
-    }
-    unsigned m = 0;
-    for (int c = 0; c < 4; ++c)
-        m |= (id + c < end && __ldcg(ref + id + c) == 0 ? 1u : 0u) << c;
-    return m;
+    return __ballot_sync(kFullMask, id + lane < end && __ldcg(ref + id + lane) == 0);
 }
 
-constexpr int kStep = 4;  // loads of 128 counts a warp has in flight
+constexpr int kStep = 4;     // loads of table entries in flight
+constexpr int kRounds = 8;   // turns that the warps take through the pool (a multiple of kStep)
+constexpr unsigned kInvalid = ~0u;
 
 // A cluster of CTAs runs the whole step: the pool's counts and the rows' pages
 // and slots are spread over the cluster's warps, the (small) row sums are
 // computed by every CTA for itself, and three cluster barriers separate drops,
-// counting, handing out and writing slots.  All of it is a few dependent trips
-// to L2: bound by latency, not by bytes.
-__global__ void __launch_bounds__(kThreads, 1) tables_step_kernel(const TablesParams p, int ctas)
+// counting, handing out and writing slots.  All of it is a few dependent trips to L2, each of
+// which the code starts as early as it can: bound by latency, not by bytes.
+__global__ void __launch_bounds__(kThreads, 1) tables_step_kernel(const TablesParams p)
 {
     extern __shared__ int rows_smem[];
     __shared__ unsigned long long s_part[2 * kWarps];
-    __shared__ int s_warp_base[kWarps + 1];
-    __shared__ int s_zeros[kStepCtas];  // zero counts of every CTA's part of the pool
+    __shared__ int s_warp_base[kRounds][kWarps];  // zero counts, then those of the warps before
+    __shared__ int s_zeros[kRounds][kStepCtas];   // zero counts of every CTA
     __shared__ int s_bad;
     const int S = p.num_seqs;
-    int *tok_end = rows_smem;                                        // tokens reserved, inclusive
-    int *page_end = tok_end + S;                                     // pages taken, inclusive
-    unsigned *kept2 = reinterpret_cast<unsigned *>(page_end + S);    // 2 * kept + copy
-    int *shared_last = reinterpret_cast<int *>(kept2 + S);           // shared part-filled last page
+    int *tok_end = rows_smem;     // tokens asked for; then reserved, inclusive sums
+    int *page_end = tok_end + S;  // length before the step; then pages taken, inclusive sums
+    // 2 * kept + copy, or kInvalid for a row of invalid length.
+    unsigned *kept2 = reinterpret_cast<unsigned *>(page_end + S);
+    // 2 * page + shared of the part-filled page that the row grows into, else kInvalid.
+    unsigned *last2 = kept2 + S;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int cta = blockIdx.x;  // the grid is one cluster
+    const int gw = cta * kWarps + warp, warps = kStepCtas * kWarps;
+    const int thread = cta * kThreads + threadIdx.x, threads = kStepCtas * kThreads;
     const int max_len = p.max_blocks * kBlockSize;
     const size_t width = p.max_blocks;
 
+    if (!p.drop_lens)
+        cluster_arrive();  // only says that this CTA runs
     if (threadIdx.x == 0)
         s_bad = 0;
+    __syncthreads();
+
+    // Rows: what is kept, and the part-filled last pages (which no drop touches).
+    int32_t page0 = -1;  // that of row threadIdx.x, on its way during the drops
+    for (int s = threadIdx.x; s < S; s += kThreads) {
+        const int L = __ldcg(p.seq_lens + s), d = p.drop_lens ? __ldg(p.drop_lens + s) : 0;
+        const int n = p.new_lens ? __ldg(p.new_lens + s) : 0;
+        const bool len_ok = L >= 0 && L <= max_len;
+        const int kept = len_ok ? L - (d > 0 ? min(d, L) : 0) : 0;
+        if (!len_ok || n < 0 || n > max_len - kept)
+            s_bad = 1;
+        else if (n > 0 && kept % kBlockSize != 0) {
+            const int32_t page = __ldcg(p.block_tables + s * width + pages_of(kept) - 1);
+            if (s == threadIdx.x)
+                page0 = page;
+            else
+                last2[s] = page >= 0 && page < p.num_blocks ? 2u * static_cast<unsigned>(page) : kInvalid;
+        }
+        if (p.drop_lens && (!len_ok || d < 0) && cta == 0)
+            set_status(p.status, PKV_ERR_OUT_OF_RANGE);
+        tok_end[s] = n;
+        page_end[s] = L;
+        kept2[s] = len_ok ? 2u * static_cast<unsigned>(kept) : kInvalid;
+    }
 
     // Drops: as many warps per row as there are for all rows.
     if (p.drop_lens) {
-        const int per_row = max(1, ctas * kWarps / S);
-        const int gw = cta * kWarps + warp;
+        __syncthreads();
+        const int per_row = max(1, warps / S);
         const int sub = gw % per_row;
-        for (int s = gw / per_row; s < S; s += ctas * kWarps / per_row) {
-            if (gw / per_row >= ctas * kWarps / per_row)
-                break;  // warps left over
-            const int L = __ldcg(p.seq_lens + s), d = __ldg(p.drop_lens + s);
-            if (L < 0 || L > max_len || d < 0) {
-                if (lane == 0 && sub == 0)
-                    set_status(p.status, PKV_ERR_OUT_OF_RANGE);
+        for (int s = gw / per_row; s < S && gw / per_row < warps / per_row; s += warps / per_row) {
+            if (kept2[s] == kInvalid)
                 continue;
-            }
             int32_t *row = p.block_tables + s * width;
-            const int last = pages_of(L);
-            for (int j0 = pages_of(L - min(d, L)) + sub * 32 + lane; j0 < last;
+            const int last = pages_of(page_end[s]);
+            for (int j0 = pages_of(static_cast<int>(kept2[s] >> 1)) + sub * 32 + lane; j0 < last;
                  j0 += kStep * 32 * per_row) {
                 int32_t page[kStep];
 #pragma unroll
@@ -180,95 +197,94 @@ __global__ void __launch_bounds__(kThreads, 1) tables_step_kernel(const TablesPa
                     set_status(p.status, PKV_ERR_OUT_OF_RANGE);
             }
         }
+        cluster_arrive();
+        cluster_wait();
     }
-    sync_all(ctas);  // also: every CTA runs, before its shared memory is written
 
-    // Zero counts: the pool in ranges of `per_warp` ids, one per warp of the
-    // cluster, in order.
-    const long per_warp = (p.num_blocks / (ctas * kWarps) + 128) & ~127;
-    const long lo = min(static_cast<long>(cta * kWarps + warp) * per_warp, static_cast<long>(p.num_blocks));
-    const long hi = min(lo + per_warp, static_cast<long>(p.num_blocks));
-    int zeros = 0;
-    for (long b = lo; b < hi; b += 128 * kStep) {
-        unsigned m[kStep];
+    // Zero counts.  The warps go through the pool in turns of `chunk` ids each,
+    // so that the low ids, where the free pages are taken, are spread over all.
+    const int chunk = static_cast<int>((p.num_blocks / (static_cast<long>(warps) * kRounds) + 32) & ~31L);
+    const long end = p.num_blocks;
+#pragma unroll 1
+    for (int r0 = 0; r0 < kRounds; r0 += kStep) {
+        int zeros[kStep] = {};
+#pragma unroll 1
+        for (int i = 0; i < chunk; i += 32)
 #pragma unroll
-        for (int i = 0; i < kStep; ++i)
-            m[i] = zeros4(p.ref_counts, min(b + 128 * i + 4 * lane, hi), hi);
+            for (int x = 0; x < kStep; ++x)
+                zeros[x] += __popc(zero_mask(p.ref_counts, (static_cast<long>(r0 + x) * warps + gw) * chunk + i,
+                                             end, lane));
+        if (lane == 0)
 #pragma unroll
-        for (int i = 0; i < kStep; ++i)
-            zeros += __popc(m[i]);
+            for (int x = 0; x < kStep; ++x)
+                s_warp_base[r0 + x][warp] = zeros[x];
     }
-    zeros = __reduce_add_sync(kFullMask, zeros);
-    if (lane == 0)
-        s_warp_base[warp + 1] = zeros;
-
-    // Rows: what is kept, and which part-filled last pages are shared.
+    // Counts of the rows' last pages, as the drops left them.
     for (int s = threadIdx.x; s < S; s += kThreads) {
-        const int L = __ldcg(p.seq_lens + s), d = p.drop_lens ? __ldg(p.drop_lens + s) : 0;
-        const int n = p.new_lens ? __ldg(p.new_lens + s) : 0;
-        const bool len_ok = L >= 0 && L <= max_len;
-        const int kept = len_ok ? L - (d > 0 ? min(d, L) : 0) : 0;
-        bool bad = !len_ok || n < 0 || n > max_len - kept;
-        int shared = -1;
-        if (!bad && n > 0 && kept % kBlockSize != 0) {
-            const int32_t page = __ldcg(p.block_tables + s * width + pages_of(kept) - 1);
-            const int refs = page >= 0 && page < p.num_blocks ? __ldcg(p.ref_counts + page) : 0;
-            bad = refs <= 0;
+        const int n = tok_end[s];
+        const unsigned k2 = kept2[s];
+        unsigned l2 = kInvalid;
+        if (k2 != kInvalid && n > 0 && n <= max_len - static_cast<int>(k2 >> 1) && (k2 >> 1) % kBlockSize != 0) {
+            if (s == threadIdx.x)
+                l2 = page0 >= 0 && page0 < p.num_blocks ? 2u * static_cast<unsigned>(page0) : kInvalid;
+            else
+                l2 = last2[s];
+            const int refs = l2 == kInvalid ? 0 : __ldcg(p.ref_counts + (l2 >> 1));
+            if (refs <= 0)
+                s_bad = 1;
             if (refs > 1)
-                shared = page;
+                l2 |= 1u;
         }
-        kept2[s] = 2u * static_cast<unsigned>(kept);
-        shared_last[s] = shared;
-        if (bad)
-            s_bad = 1;
+        last2[s] = l2;
     }
+    if (!p.drop_lens)
+        cluster_wait();  // every CTA runs: their shared memory may be written
     __syncthreads();
-    if (threadIdx.x < 32) {  // this CTA's zero counts: per-warp bases, total to every CTA
-        int z = s_warp_base[lane + 1];
+    if (warp < kRounds) {  // a turn's zero counts: per-warp bases, this CTA's total to every CTA
+        const int own = s_warp_base[warp][lane];
+        int z = own;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int y = __shfl_up_sync(kFullMask, z, d);
             if (lane >= d)
                 z += y;
         }
-        s_warp_base[lane + 1] = z;
-        if (lane == 0)
-            s_warp_base[0] = 0;
+        s_warp_base[warp][lane] = z - own;
         const int all = __shfl_sync(kFullMask, z, 31);
-        if (lane < ctas) {
+        if (lane < kStepCtas) {
             uint32_t remote;
             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                          : "=r"(remote)
-                         : "r"(smem_u32(&s_zeros[cta])), "r"(lane));
+                         : "r"(smem_u32(&s_zeros[warp][cta])), "r"(lane));
             asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(all) : "memory");
         }
     }
     // A sharing row copies unless every other holder of the page is an
-    // earlier row that has copied already.
-    bool want_pair = false;
-    for (int s = threadIdx.x; s < S; s += kThreads) {
-        const int page = shared_last[s];
-        if (page < 0)
+    // earlier row that has copied already.  A warp per row.
+    for (int s = warp; s < S; s += kWarps) {
+        const unsigned l2 = last2[s];
+        if (l2 == kInvalid || !(l2 & 1u))
             continue;
-        const int others = __ldcg(p.ref_counts + page) - 1;
+        const int others = __ldcg(p.ref_counts + (l2 >> 1)) - 1;
         int before = 0;
-        for (int t = 0; t < s && before < others; ++t)
-            before += shared_last[t] == page;
-        if (before < others) {
+        for (int t = lane; t < s; t += 32)
+            before += last2[t] == l2;
+        before = __reduce_add_sync(kFullMask, before);
+        if (before < others && lane == 0) {
             kept2[s] |= 1u;
-            want_pair = true;
+            if (!p.copy_pairs)
+                s_bad = 1;
         }
     }
-    if (want_pair && !p.copy_pairs)
-        s_bad = 1;
+    __syncthreads();
     // Prefix sums of the tokens and pages, 1024 rows at a time.
     unsigned long long tokens = 0, pages = 0;
     for (int s0 = 0; s0 < S; s0 += kThreads) {
         const int s = s0 + threadIdx.x;
         unsigned long long n = 0, need = 0;
-        if (s < S) {
+        if (s < S && kept2[s] != kInvalid) {
             const int kept = static_cast<int>(kept2[s] >> 1);
-            const int nn = p.new_lens ? __ldg(p.new_lens + s) : 0;
+            const int nn = tok_end[s];
             if (nn > 0 && nn <= max_len - kept) {
                 n = nn;
                 need = pages_of(kept + nn) - pages_of(kept) + (kept2[s] & 1u);
@@ -283,81 +299,114 @@ __global__ void __launch_bounds__(kThreads, 1) tables_step_kernel(const TablesPa
         tokens += sum_n;
         pages += sum_need;
     }
-    sync_all(ctas);
+    cluster_arrive();
+    cluster_wait();
 
-    int rank = s_warp_base[warp];
-    int total_zeros = 0;
-    for (int c = 0; c < ctas; ++c) {
-        const int z = s_zeros[c];
-        rank += c < cta ? z : 0;
-        total_zeros += z;
-    }
-    const bool enough = pages <= static_cast<unsigned long long>(total_zeros);
-    const bool bad = s_bad || tokens > static_cast<unsigned long long>(p.max_tokens);
-    const bool ok = !bad && enough;
-    if (!ok && cta == 0 && threadIdx.x == 0)
-        set_status(p.status, bad ? PKV_ERR_OUT_OF_RANGE : PKV_ERR_NO_BLOCKS);
-    const int total = ok ? static_cast<int>(tokens) : 0;
-    const int taken = ok ? static_cast<int>(pages) : 0;
-
-    const int thread = cta * kThreads + threadIdx.x, threads = ctas * kThreads;
-    if (p.copy_pairs)
-        for (int s = thread; s < S; s += threads)
-            if (!ok || !(kept2[s] & 1u))
-                p.copy_pairs[2 * s] = p.copy_pairs[2 * s + 1] = -1;
-    // Hand out the pages: the r-th zero count goes to the row that owns r.
-    for (long b = lo; b < hi && rank < taken; b += 128) {
-        unsigned m = zeros4(p.ref_counts, min(b + 4 * lane, hi), hi);
-        const int c = __popc(m);
-        int upto = c;
+    // Lane r: the zero counts ahead of this CTA's in turn r, and of the turn.
+    int ahead = 0, total_zeros = 0;
+    if (lane < kRounds)
+        for (int c = 0; c < kStepCtas; ++c) {
+            const int z = s_zeros[lane][c];
+            ahead += c < cta ? z : 0;
+            total_zeros += z;
+        }
+    {
+        int upto = total_zeros;  // turns up to this lane's
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
+        for (int d = 1; d < kRounds; d <<= 1) {
             const int y = __shfl_up_sync(kFullMask, upto, d);
             if (lane >= d)
                 upto += y;
         }
-        for (int r = rank + upto - c; m && r < taken; ++r, m &= m - 1) {
-            const int32_t page = static_cast<int32_t>(b) + 4 * lane + __ffs(m) - 1;
-            const int s = row_of(page_end, S, r);
-            const int j = r - (s ? page_end[s - 1] : 0);
+        ahead += upto - total_zeros;
+        total_zeros = __shfl_sync(kFullMask, upto, kRounds - 1);
+    }
+    const bool enough = pages <= static_cast<unsigned long long>(total_zeros);
+    const bool bad = s_bad || tokens > static_cast<unsigned long long>(p.max_tokens);
+    const bool ok = !bad && enough;
+    if (!ok && thread == 0)
+        set_status(p.status, bad ? PKV_ERR_OUT_OF_RANGE : PKV_ERR_NO_BLOCKS);
+    const int total = ok ? static_cast<int>(tokens) : 0;
+    const int taken = ok ? static_cast<int>(pages) : 0;
+
+    // Hand out the pages: the r-th zero count goes to the row that owns r.
+#pragma unroll 1
+    for (int r = 0; r < kRounds; ++r) {
+        const long b = (static_cast<long>(r) * warps + gw) * chunk;
+        int rank = __shfl_sync(kFullMask, ahead, r) + s_warp_base[r][warp];
+        if (b >= end || rank >= taken)
+            break;
+#pragma unroll 1
+        for (int i = 0; i < chunk && rank < taken; i += 32) {
+            const unsigned m = zero_mask(p.ref_counts, b + i, end, lane);
+            const int at = rank + __popc(m & ((1u << lane) - 1u));
+            rank += __popc(m);
+            if (!(m >> lane & 1u) || at >= taken)
+                continue;
+            const int32_t page = static_cast<int32_t>(b + i + lane);
+            const int s = row_of(page_end, S, at);
+            const int j = at - (s ? page_end[s - 1] : 0);
             const unsigned k2 = kept2[s];
             const int copy = k2 & 1u;
-            int32_t *entry = p.block_tables + s * width + pages_of(static_cast<int>(k2 >> 1)) - copy + j;
             if (copy && j == 0) {
-                const int32_t src = __ldcg(entry);
-                p.copy_pairs[2 * s] = src;
+                const unsigned src = last2[s] >> 1;
+                p.copy_pairs[2 * s] = static_cast<int32_t>(src);
                 p.copy_pairs[2 * s + 1] = page;
                 atomicSub(p.ref_counts + src, 1);  // at least one holder is left
             }
-            *entry = page;
+            p.block_tables[s * width + pages_of(static_cast<int>(k2 >> 1)) - copy + j] = page;
             p.ref_counts[page] = 1;
         }
-        rank += __shfl_sync(kFullMask, upto, 31);
     }
-    sync_all(ctas);
-
-    // Slots of the reserved tokens (-1 past them), row starts, lengths.
-    for (int i = thread; i < p.max_tokens; i += threads) {
-        int64_t slot = -1;
-        if (i < total) {
-            const int s = row_of(tok_end, S, i);
-            const int pos = static_cast<int>(kept2[s] >> 1) + i - (s ? tok_end[s - 1] : 0);
-            const int32_t page = __ldcg(p.block_tables + s * width + pos / kBlockSize);
-            slot = static_cast<int64_t>(page) * kBlockSize + pos % kBlockSize;
-        }
-        p.slot_mapping[i] = slot;
-    }
+    cluster_arrive();
     for (int s = thread; s < S; s += threads) {
         const int end = ok ? tok_end[s] : 0;
         const int n = ok ? end - (s ? tok_end[s - 1] : 0) : 0;
         if (p.q_start)
             p.q_start[s + 1] = end;
-        const int L = __ldcg(p.seq_lens + s);
-        if (L >= 0 && L <= max_len)
+        if (p.copy_pairs && (!ok || !(kept2[s] & 1u)))
+            p.copy_pairs[2 * s] = p.copy_pairs[2 * s + 1] = -1;
+        if (kept2[s] != kInvalid)
             p.seq_lens[s] = static_cast<int>(kept2[s] >> 1) + n;
     }
     if (p.q_start && thread == 0)
         p.q_start[0] = 0;
+    cluster_wait();  // the tables are written
+
+    // Slots of the reserved tokens, -1 past them: four tokens in a row per
+    // thread, which mostly share their row and page.
+    for (long i0 = 4L * thread; i0 < p.max_tokens; i0 += 4L * threads) {
+        const int *last = tok_end + S;
+        const int *e = i0 < total ? tok_end + row_of(tok_end, S, static_cast<int>(i0)) : last;
+        int64_t slot[4];
+        int at = -1;  // table entry in `page`
+        int32_t page = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            slot[x] = -1;
+            if (i0 + x >= total)
+                continue;
+            const int i = static_cast<int>(i0) + x;
+            for (; *e <= i; ++e)
+                at = -1;
+            const int s = static_cast<int>(e - tok_end);
+            const int pos = static_cast<int>(kept2[s] >> 1) + i - (s ? e[-1] : 0);
+            if (at != pos / kBlockSize) {
+                at = pos / kBlockSize;
+                page = __ldcg(p.block_tables + s * width + at);
+            }
+            slot[x] = static_cast<int64_t>(page) * kBlockSize + pos % kBlockSize;
+        }
+        if (i0 + 4 <= p.max_tokens && p.wide_slots) {
+            longlong2 *dst = reinterpret_cast<longlong2 *>(p.slot_mapping + i0);
+            dst[0] = make_longlong2(slot[0], slot[1]);
+            dst[1] = make_longlong2(slot[2], slot[3]);
+        } else {
+            for (int x = 0; x < 4; ++x)
+                if (i0 + x < p.max_tokens)
+                    p.slot_mapping[i0 + x] = slot[x];
+        }
+    }
 }
 
 // One CTA per (parent, child) pair.
@@ -425,19 +474,18 @@ pkv_status launch_tables_step(const TablesParams &p, cudaStream_t stream)
     });
     if (rc != PKV_OK)
         return rc;
-    const int ctas = kStepCtas;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = ctas;
+    attr.val.clusterDim.x = kStepCtas;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
+    cfg.gridDim = dim3(kStepCtas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(p.num_seqs) * kTablesRowBytes;
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tables_step_kernel, p, ctas) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, tables_step_kernel, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 pkv_status launch_tables_fork(const int32_t *pairs, int num_pairs, int32_t *seq_lens,

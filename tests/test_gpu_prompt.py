@@ -292,3 +292,37 @@ def test_bounded_wait_reports_timeout_and_recovers():
     torch.cuda.synchronize()
     assert int(status) == 5  # PKV_ERR_TIMEOUT
     check(q, k, v, lens, 0.1)
+
+
+@pytest.mark.parametrize("dtype,out_dtype", TYPES)
+@pytest.mark.parametrize("D", [64, 128])
+def test_output_on_a_16_byte_boundary(D, dtype, out_dtype):
+    # Outputs need 16-byte alignment only.
+    lens = [70, 1, 130]
+    q, k, v = make(lens, 6, 2, D, dtype, 17)
+    unit = 16 * 8 // torch.finfo(out_dtype).bits
+    buf = torch.full((q.numel() + 2 * unit,), 7.0, dtype=out_dtype, device=DEV)
+    out = buf[unit:unit + q.numel()].view(q.shape)
+    assert out.data_ptr() % 32 == 16
+    pkv.prompt_attn(q, k, v, starts(lens), 0.1, out)
+    want = torch.zeros(q.shape, dtype=out_dtype, device=DEV)
+    pkv.prompt_attn(q, k, v, starts(lens), 0.1, want)
+    assert torch.equal(out, want) and bool((buf[:unit] == 7).all()) and bool((buf[-unit:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_two_calls_at_once(dtype):
+    # Two streams, two batches, nothing shared: each as alone.
+    runs = []
+    for seed, lens in ((20, [500, 40, 300]), (21, [33] * 20)):
+        q, k, v = make(lens, 16, 4, 128, dtype, seed)
+        want = torch.zeros(q.shape, dtype=dtype, device=DEV)
+        pkv.prompt_attn(q, k, v, starts(lens), 0.1, want)
+        runs.append((q, k, v, starts(lens), want, torch.zeros_like(want), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for q, k, v, qs, _, got, s in runs:
+            pkv.prompt_attn(q, k, v, qs, 0.1, got, stream=s)
+    torch.cuda.synchronize()
+    for _, _, _, _, want, got, _ in runs:
+        assert torch.equal(want, got)

@@ -420,3 +420,45 @@ def test_serving_loop(dtype):
     # Retiring every row empties the pool.
     assert pool.step([1 << 30] * S, None) == 0
     assert int(pool.ref.abs().sum()) == 0 and (pool.tables == -1).all()
+
+
+@pytest.mark.gpu
+def test_slots_on_an_8_byte_boundary():
+    g = Pool(5, 20, 120, 600)
+    buf = torch.full((603,), 77, dtype=torch.int64, device=DEV)
+    m = Model(5, 20, 120)
+    for new in ([33, 0, 7, 128, 1], [1, 1, 1, 1, 1], [0, 250, 0, 3, 16]):
+        st, q_start, slots, pairs = m.reserve(new, 601)
+        assert g.step(None, new, slot_mapping=buf[1:602]) == st == 0
+        assert np.array_equal(buf[1:602].cpu().numpy(), slots)
+        assert int(buf[0]) == 77 and int(buf[602]) == 77
+        g.same(m)
+
+
+@pytest.mark.gpu
+def test_two_pools_at_once():
+    # Two pools on two streams, the steps captured in two graphs and replayed side by side.
+    pools, graphs = [Pool(64, 40, 2000, 4096) for _ in range(2)], []
+    new = [torch.full((64,), n, dtype=torch.int32, device=DEV) for n in (3, 7)]
+    drop = [torch.full((64,), n, dtype=torch.int32, device=DEV) for n in (1, 2)]
+    torch.cuda.synchronize()
+    for p, n, d in zip(pools, new, drop):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pkv.tables_step(p.lens, p.tables, p.ref, drop_lens=d, new_lens=n, q_start=p.q_start,
+                            slot_mapping=p.slots, copy_pairs=p.pairs, status=p.status)
+        graphs.append((graph, torch.cuda.Stream()))
+    for _ in range(30):
+        for graph, s in graphs:
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for p, n, d in zip(pools, (3, 7), (1, 2)):
+        m = Model(64, 40, 2000)
+        for _ in range(30):
+            m.drop([d] * 64)
+            st, q_start, slots, _ = m.reserve([n] * 64, 4096)
+            assert st == 0
+        assert int(p.status) == 0 and p.q_start.tolist() == q_start
+        assert np.array_equal(p.slots.cpu().numpy(), slots)
+        p.same(m)
