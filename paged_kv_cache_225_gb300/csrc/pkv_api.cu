@@ -851,8 +851,8 @@ pkv_status pkv_prompt_attn(const void *q, const void *k, const void *v, pkv_dtyp
     // score), and a zero becomes a factor too small to tell weights apart, which
     // keeps masked scores (-inf) out all the same.
     const float factor = static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634);
-    const float least = std::ldexp(1.0f, -120);
-    p.score_scale = factor > least ? factor : least;
+    const float least = std::ldexp(1.0f, -120), most = std::ldexp(1.0f, 127);
+    p.score_scale = factor < least ? least : factor > most ? most : factor;
     p.negate = scale < 0.f ? 1 : 0;
     p.drop_first_copy = (flags & PKV_FLAG_TEST_DROP_FIRST_COPY) ? 1 : 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -23,10 +23,9 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-// CTAs of the cluster: the largest there is, which was never slower than fewer
-// (us a step on 1 / 4 / 16: 128 rows of a 31K-page pool 17.2 / 11.9 / 10.7, 64
-// prompts admitted 120.7 / 37.8 / 18.3, 512 rows of a 288K-page pool 154.9 /
-// 53.1 / 22.1).
+// CTAs of the cluster: the largest there is.  us a step on 2 / 4 / 8 / 16: 128
+// rows of a 31K-page pool 13.3 / 11.0 / 10.9 / 11.2, 64 prompts admitted 46.5 /
+// 28.1 / 18.8 / 14.7, 512 rows of a 288K-page pool 73.6 / 43.1 / 29.1 / 21.6.
 constexpr int kStepCtas = 16;
 
 __device__ __forceinline__ int pages_of(int tokens) { return (tokens + kBlockSize - 1) / kBlockSize; }
@@ -96,10 +95,18 @@ __device__ __forceinline__ int row_of(const int *ends, int n, int i)
     return lo;
 }
 
-// Lanes whose count is zero among the 32 from id on (ids from `end` on are not).
-__device__ __forceinline__ unsigned zero_mask(const int32_t *ref, long id, long end, int lane)
+// Lanes whose count is zero among the 32 from id on (ids from p.num_blocks on
+// are not).  A count below zero, of a page dropped more often than held, is
+// reported and becomes zero.
+__device__ __forceinline__ unsigned zero_mask(const TablesParams &p, long id, int lane)
 {
-    return __ballot_sync(kFullMask, id + lane < end && __ldcg(ref + id + lane) == 0);
+    const bool in = id + lane < p.num_blocks;
+    const int refs = in ? __ldcg(p.ref_counts + id + lane) : 1;
+    if (refs < 0) {
+        p.ref_counts[id + lane] = 0;
+        set_status(p.status, PKV_ERR_OUT_OF_RANGE);
+    }
+    return __ballot_sync(kFullMask, refs <= 0);
 }
 
 constexpr int kStep = 4;     // loads of table entries in flight
@@ -179,22 +186,19 @@ __global__ void __launch_bounds__(kThreads, 1) tables_step_kernel(const TablesPa
                     const int j = j0 + i * 32 * per_row;
                     page[i] = j < last ? __ldcg(row + j) : -1;
                 }
-                bool bad = false;
+                // A page that nobody held falls below zero: the counting below
+                // finds and mends it, so that nothing waits for a result here.
 #pragma unroll
                 for (int i = 0; i < kStep; ++i) {
                     const int j = j0 + i * 32 * per_row;
                     if (j >= last)
                         continue;
                     row[j] = -1;
-                    bool ok = page[i] >= 0 && page[i] < p.num_blocks;
-                    if (ok && atomicSub(p.ref_counts + page[i], 1) <= 0) {
-                        atomicAdd(p.ref_counts + page[i], 1);  // nobody held it: put it back
-                        ok = false;
-                    }
-                    bad = bad || !ok;
+                    if (page[i] >= 0 && page[i] < p.num_blocks)
+                        atomicSub(p.ref_counts + page[i], 1);
+                    else
+                        set_status(p.status, PKV_ERR_OUT_OF_RANGE);
                 }
-                if (bad)
-                    set_status(p.status, PKV_ERR_OUT_OF_RANGE);
             }
         }
         cluster_arrive();
@@ -204,7 +208,6 @@ __global__ void __launch_bounds__(kThreads, 1) tables_step_kernel(const TablesPa
     // Zero counts.  The warps go through the pool in turns of `chunk` ids each,
     // so that the low ids, where the free pages are taken, are spread over all.
     const int chunk = static_cast<int>((p.num_blocks / (static_cast<long>(warps) * kRounds) + 32) & ~31L);
-    const long end = p.num_blocks;
 #pragma unroll 1
     for (int r0 = 0; r0 < kRounds; r0 += kStep) {
         int zeros[kStep] = {};
@@ -212,8 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) tables_step_kernel(const TablesPa
         for (int i = 0; i < chunk; i += 32)
 #pragma unroll
             for (int x = 0; x < kStep; ++x)
-                zeros[x] += __popc(zero_mask(p.ref_counts, (static_cast<long>(r0 + x) * warps + gw) * chunk + i,
-                                             end, lane));
+                zeros[x] += __popc(zero_mask(p, (static_cast<long>(r0 + x) * warps + gw) * chunk + i, lane));
         if (lane == 0)
 #pragma unroll
             for (int x = 0; x < kStep; ++x)
@@ -334,11 +336,11 @@ __global__ void __launch_bounds__(kThreads, 1) tables_step_kernel(const TablesPa
     for (int r = 0; r < kRounds; ++r) {
         const long b = (static_cast<long>(r) * warps + gw) * chunk;
         int rank = __shfl_sync(kFullMask, ahead, r) + s_warp_base[r][warp];
-        if (b >= end || rank >= taken)
+        if (b >= p.num_blocks || rank >= taken)
             break;
 #pragma unroll 1
         for (int i = 0; i < chunk && rank < taken; i += 32) {
-            const unsigned m = zero_mask(p.ref_counts, b + i, end, lane);
+            const unsigned m = zero_mask(p, b + i, lane);
             const int at = rank + __popc(m & ((1u << lane) - 1u));
             rank += __popc(m);
             if (!(m >> lane & 1u) || at >= taken)
@@ -440,18 +442,28 @@ __global__ void __launch_bounds__(kForkThreads)
     }
     const int32_t *src = block_tables + static_cast<size_t>(parent) * max_blocks;
     int32_t *dst = block_tables + static_cast<size_t>(child) * max_blocks;
-    for (int j = threadIdx.x; j < pages_of(L); j += kForkThreads) {
-        int32_t page = src[j];
-        bool ok = page >= 0 && page < num_blocks;
-        if (ok && atomicAdd(ref_counts + page, 1) <= 0) {
-            atomicSub(ref_counts + page, 1);  // not a held page: nothing to share
-            ok = false;
+    // No pair of the call drops a page or adds one that nobody holds: a count
+    // read as positive stays so.
+    const int pages = pages_of(L);
+    for (int j0 = threadIdx.x; j0 < pages; j0 += kStep * kForkThreads) {
+        int32_t page[kStep];
+        int refs[kStep];
+#pragma unroll
+        for (int x = 0; x < kStep; ++x)
+            page[x] = j0 + x * kForkThreads < pages ? __ldcg(src + j0 + x * kForkThreads) : -1;
+#pragma unroll
+        for (int x = 0; x < kStep; ++x)
+            refs[x] = page[x] >= 0 && page[x] < num_blocks ? __ldcg(ref_counts + page[x]) : 0;
+#pragma unroll
+        for (int x = 0; x < kStep; ++x) {
+            if (j0 + x * kForkThreads >= pages)
+                continue;
+            if (refs[x] > 0)
+                atomicAdd(ref_counts + page[x], 1);
+            else
+                set_status(status, PKV_ERR_OUT_OF_RANGE);  // not a held page: nothing to share
+            dst[j0 + x * kForkThreads] = refs[x] > 0 ? page[x] : -1;
         }
-        if (!ok) {
-            set_status(status, PKV_ERR_OUT_OF_RANGE);
-            page = -1;
-        }
-        dst[j] = page;
     }
     if (threadIdx.x == 0)
         seq_lens[child] = L;
