@@ -98,7 +98,8 @@ def parse_args(argv=None):
 
 # Sources that do not define or launch the decode kernels.
 _NOT_DECODE = {"pkv_cache.cu", "pkv_noalloc.cu", "pkv_prefill.cu", "pkv_prefill_tc.cu",
-               "pkv_prefill.cuh"}
+               "pkv_prefill.cuh", "pkv_tc.cuh", "pkv_prompt.cu", "pkv_prompt.cuh",
+               "pkv_prompt_tc.cu", "pkv_tables.cu", "pkv_ops.h", "pkv_ops_api.cu"}
 
 
 def source_hash() -> str:

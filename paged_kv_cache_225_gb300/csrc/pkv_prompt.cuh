@@ -13,7 +13,7 @@
 #pragma once
 
 #include "pkv_common.cuh"
-#include "pkv_internal.h"
+#include "pkv_ops.h"
 
 namespace pkv {
 

@@ -15,7 +15,7 @@
 // count is zero.  Both orders are prefix sums: over the rows in shared memory,
 // over the pool by counting zero counts per warp and ranking them by ballot.
 #include "pkv_common.cuh"
-#include "pkv_internal.h"
+#include "pkv_ops.h"
 
 namespace pkv {
 
