@@ -12,14 +12,17 @@
 // Everything stays in f32: tensor-core products of split operands would lose
 // the last bits in their accumulation.
 //
-// A CTA holds 64 rows (token, grouped head) and walks 64 keys at a time, all
-// operands in shared memory; a thread owns 8 rows x 4 keys of the scores and 8
-// rows x D / 16 columns of the output.  Products are packed two to an
-// instruction (fma.rn.f32x2): the scores sum even and odd dims in the halves,
-// the output holds pairs of columns.  Shared-memory loads bound it: a 16-byte
-// load of a warp takes four cycles, and a thread needs 12 of them for 64 packed
-// multiply-adds of the scores (32 cycles), 16 for 128 of the output (8 prompts of
-// 256 to 1024 tokens, 32 heads of 128 over 8 KV heads: PKV_F32).
+// A CTA of 256 threads holds 64 rows (token, grouped head) and walks 64 keys at a
+// time, all operands in shared memory; a thread owns 4 rows x 4 keys of the scores
+// and 4 rows x D / 16 columns of the output.  Products are packed two to an
+// instruction (fma.rn.f32x2): the scores sum even and odd dims in the halves, the
+// output holds pairs of columns.  Shared-memory loads and their latency bound it.
+// Rows per thread trade loads for warps that hide them: 8 rows (128 threads, 250
+// registers) load least, but two CTAs are then 8 warps to an SM; 2 rows load twice
+// as often as 4.  8 prompts of 256 to 1024 tokens, 32 heads of 128 over 8 KV
+// heads: 919 us with 8 rows, 898 us (33 TFLOP/s) with 4, 1241 us with 2; one
+// prompt of a few tokens 11.8, 10.0 and 10.5 us.  Single multiply-adds with one
+// shared load per operand pair took 1233 us.
 #include "pkv_prompt.cuh"
 
 namespace pkv {
@@ -28,7 +31,9 @@ namespace {
 
 constexpr int kRows = 64;
 constexpr int kKeys = 64;
-constexpr int kSimtThreads = 128;
+constexpr int kRpt = 4;  // rows per thread
+constexpr int kTy = kRows / kRpt;
+constexpr int kSimtThreads = 16 * kTy;
 
 template <int D> struct SimtGeom {
     static constexpr int kLd = D + 4;          // row stride of Q and K: rows 4 banks apart
@@ -104,14 +109,14 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
             *reinterpret_cast<float4 *>(sq + r * kLd + d) = x;
         }
 
-        uint64_t o[8][2 * kCols];
-        float m[8], l[8];
-        int pos[8];
+        uint64_t o[kRpt][2 * kCols];
+        float m[kRpt], l[kRpt];
+        int pos[kRpt];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kRpt; ++i) {
             m[i] = -INFINITY;
             l[i] = 0.f;
-            pos[i] = t0 + min((ty + 8 * i) / G, nt - 1);  // rows past the item repeat its last token
+            pos[i] = t0 + min((ty + kTy * i) / G, nt - 1);  // rows past the item repeat its last token
 #pragma unroll
             for (int x = 0; x < 2 * kCols; ++x)
                 o[i][x] = 0;
@@ -141,9 +146,9 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
             cp_async_commit();
             asm volatile("cp.async.wait_group 1;" ::: "memory");  // K; V may still be on its way
             __syncthreads();
-            uint64_t acc[8][4];
+            uint64_t acc[kRpt][4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < kRpt; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     acc[i][j] = 0;
@@ -154,8 +159,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
                 for (int j = 0; j < 4; ++j)
                     kf[j] = *reinterpret_cast<const ulonglong2 *>(sk + (tx + 16 * j) * kLd + d);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const ulonglong2 qf = *reinterpret_cast<const ulonglong2 *>(sq + (ty + 8 * i) * kLd + d);
+                for (int i = 0; i < kRpt; ++i) {
+                    const ulonglong2 qf = *reinterpret_cast<const ulonglong2 *>(sq + (ty + kTy * i) * kLd + d);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         fma2(acc[i][j], qf.x, kf[j].x);
@@ -168,7 +173,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
 
             const bool masked = k0 + kKeys > t0 + 1;  // some row does not see some key
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kRpt; ++i) {
                 float x[4];
                 float mx = -INFINITY;
 #pragma unroll
@@ -190,7 +195,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
                 for (int j = 0; j < 4; ++j) {
                     const float w = exp2f(x[j] - off);
                     l[i] += w;
-                    sp[(ty + 8 * i) * kPLd + tx + 16 * j] = w;
+                    sp[(ty + kTy * i) * kPLd + tx + 16 * j] = w;
                 }
                 const uint64_t a2 = pair(alpha, alpha);
 #pragma unroll
@@ -219,8 +224,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
                         for (int x = 0; x < kCols; ++x)
                             vf[kk][x] = *reinterpret_cast<const ulonglong2 *>(sv + (key + kk) * D + 4 * tx + 64 * x);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 w = *reinterpret_cast<const float4 *>(sp + (ty + 8 * i) * kPLd + key);
+                    for (int i = 0; i < kRpt; ++i) {
+                        const float4 w = *reinterpret_cast<const float4 *>(sp + (ty + kTy * i) * kPLd + key);
                         const float ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
@@ -238,10 +243,10 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
 #pragma unroll 1
                 for (int key = 0; key < keys; ++key)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < kRpt; ++i) {
                         if (k0 + key > pos[i])
                             continue;
-                        const float w1 = sp[(ty + 8 * i) * kPLd + key];
+                        const float w1 = sp[(ty + kTy * i) * kPLd + key];
                         const uint64_t w = pair(w1, w1);
 #pragma unroll
                         for (int x = 0; x < kCols; ++x) {
@@ -255,12 +260,12 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
         }
 
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kRpt; ++i) {
             float sum = l[i];
 #pragma unroll
             for (int w = 8; w >= 1; w >>= 1)
                 sum += __shfl_xor_sync(kFullMask, sum, w);
-            const int r = ty + 8 * i;
+            const int r = ty + kTy * i;
             if (r >= nt * G)
                 continue;
             const size_t orow = ((static_cast<size_t>(it.row0) + t0 + r / G) * p.num_q_heads +

@@ -8,8 +8,8 @@
 // longest sequence's last block down, in a class sequence by sequence from the
 // largest index to the smallest, KV heads innermost.  CTAs that take items
 // from such a list in turn end within about one short item of each other
-// (sixteen prompts of 512 to 4096 tokens on the tensor cores, same box: 643 us,
-// sequence after sequence 742 us).
+// (sixteen prompts of 512 to 4096 tokens on the tensor cores, same box: 575 us,
+// sequence after sequence 646 us).
 #pragma once
 
 #include "pkv_common.cuh"
