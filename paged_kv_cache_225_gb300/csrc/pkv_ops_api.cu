@@ -102,7 +102,9 @@ pkv_status pkv_tables_step(int32_t *seq_lens, int32_t *block_tables, int32_t *re
         return PKV_ERR_INVALID_ARG;
     if (block_size != kBlockSize || num_seqs > kTablesMaxRows)
         return PKV_ERR_UNSUPPORTED;
-    if (num_seqs > 0 && (!seq_lens || !block_tables || !ref_counts))
+    if (num_seqs == 0 && max_tokens == 0 && !q_start)
+        return PKV_OK;
+    if (!ref_counts || (num_seqs > 0 && (!seq_lens || !block_tables)))
         return PKV_ERR_INVALID_ARG;
     if (max_tokens > 0 && !slot_mapping)
         return PKV_ERR_INVALID_ARG;
@@ -114,8 +116,6 @@ pkv_status pkv_tables_step(int32_t *seq_lens, int32_t *block_tables, int32_t *re
             return PKV_ERR_INVALID_ARG;
     if (!aligned(ref_counts, 16) || !aligned(slot_mapping, 8))
         return PKV_ERR_INVALID_ARG;
-    if (num_seqs == 0 && max_tokens == 0 && !q_start)
-        return PKV_OK;
     TablesParams p;
     std::memset(&p, 0, sizeof p);
     p.drop_lens = num_seqs > 0 ? drop_lens : nullptr;

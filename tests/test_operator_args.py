@@ -58,6 +58,8 @@ def step(**kw):
     (dict(lens=P + 2), INVALID), (dict(tables=P + 1), INVALID), (dict(drop=P + 2), INVALID),
     (dict(new=P + 3), INVALID), (dict(start=P + 2), INVALID), (dict(pairs=P + 2), INVALID),
     (dict(status=P + 2), INVALID), (dict(S=0, most=0, start=None, lens=None), OK),
+    (dict(S=0, ref=None), INVALID), (dict(S=0, most=0, ref=None), INVALID),
+    (dict(S=0, most=0, start=None, ref=None), OK),
 ])
 def test_step_arguments(kw, want):
     assert step(**kw) == want
