@@ -641,6 +641,7 @@ def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, pairs: torch.Tenso
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's pointer, without an object
 _I32, _I64 = torch.int32, torch.int64
+_INT_MAX = 2 ** 31 - 1  # sizes are ints of the C interface, which would wrap
 
 
 def _launch(name: str, index: int, stream: Optional[torch.cuda.Stream], args) -> None:
@@ -735,9 +736,11 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torc
         raise ValueError("inconsistent shapes")
     if S < 0 or (status is not None and status.numel() != 1):
         raise ValueError("q_start needs at least one entry, status exactly one")
+    if T > _INT_MAX or S > _INT_MAX:
+        raise ValueError("at most 2^31 - 1 rows and sequences")
     _launch("pkv_prompt_attn", index, stream,
             (q.data_ptr(), k.data_ptr(), v.data_ptr(), code, qs, ks, vs, starts, S, T, Hq,
-             kshape[1], D, T if max_q_len is None else int(max_q_len), float(scale), o, ocode, st,
+             kshape[1], D, T if max_q_len is None else min(int(max_q_len), T), float(scale), o, ocode, st,
              int(flags)))
     return out
 
@@ -750,6 +753,8 @@ def _pool(seq_lens, block_tables, ref_counts):
     S, width = block_tables.shape
     if S != seq_lens.numel():
         raise ValueError("block_tables needs one row per entry of seq_lens")
+    if S > _INT_MAX or width > _INT_MAX or ref_counts.numel() > _INT_MAX:
+        raise ValueError("at most 2^31 - 1 rows, entries of a row and pages")
     return index, ptrs, S, width
 
 
@@ -779,7 +784,8 @@ def tables_step(seq_lens: torch.Tensor, block_tables: torch.Tensor, ref_counts: 
     if ((drop is not None and drop_lens.numel() != S) or (new is not None and new_lens.numel() != S)
             or (starts is not None and q_start.numel() != S + 1)
             or (pairs is not None and copy_pairs.shape != (S, 2))
-            or (st is not None and status.numel() != 1)):
+            or (st is not None and status.numel() != 1)
+            or (slots is not None and slot_mapping.numel() > _INT_MAX)):
         raise ValueError("inconsistent shapes")
     _launch("pkv_tables_step", index, stream,
             (lens, tables, refs, S, width, block_size, ref_counts.numel(), drop, new, starts, slots,
@@ -797,7 +803,7 @@ def tables_fork(pairs: torch.Tensor, seq_lens: torch.Tensor, block_tables: torch
     ptr = _ptr(pairs, "pairs", 2, _I32, index)
     st = _ptr(status, "status", 1, _I32, index)
     n, two = pairs.shape
-    if two != 2 or (st is not None and status.numel() != 1):
+    if two != 2 or n > _INT_MAX or (st is not None and status.numel() != 1):
         raise ValueError("pairs must be int32 [n, 2], status int32 [1]")
     _launch("pkv_tables_fork", index, stream,
             (ptr, n, lens, tables, refs, S, width, block_size, ref_counts.numel(), st))

@@ -19,6 +19,7 @@ struct PromptParams {
     int dtype, out_dtype;
     int num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, group;
     int max_q_len;           // bound on a sequence's rows
+    unsigned max_items;      // bound on the work items of a valid q_start (set at launch)
     float score_scale;       // |scale| * log2(e), at least 2^-120
     int negate;              // scale < 0: the kernels negate the scores
     int drop_first_copy;     // test hook: never issue the first copy of CTA 0

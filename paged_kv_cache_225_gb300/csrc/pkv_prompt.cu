@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
     }
 }
 
-template <int D> pkv_status launch_simt_d(const PromptParams &p, cudaStream_t stream)
+template <int D> pkv_status launch_simt_d(PromptParams p, cudaStream_t stream)
 {
     static ContextCache cache;
     int set = 0;
@@ -307,6 +307,7 @@ template <int D> pkv_status launch_simt_d(const PromptParams &p, cudaStream_t st
         return PKV_OK;
     if (items > 0x40000000L)
         return PKV_ERR_UNSUPPORTED;
+    p.max_items = static_cast<unsigned>(items);
     // Two CTAs to an SM; the costliest items go first, one at a time.
     const long slots = 2L * device_sm_count();
     prompt_simt_kernel<D><<<static_cast<unsigned>(items < slots ? items : slots), kSimtThreads,

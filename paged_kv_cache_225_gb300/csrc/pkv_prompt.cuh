@@ -36,7 +36,9 @@ __device__ __forceinline__ int prompt_len(const PromptParams &p, int s, int &sta
 }
 
 // Items there can be at most (host): every sequence's tokens / `tokens` and one
-// more, or the longest's for each of them.
+// more, or the longest's for each of them.  Row starts that step back can
+// make sequences that overlap, and any number of items: the look-up stops at
+// this bound.
 inline long prompt_max_items(const PromptParams &p, long tokens)
 {
     const long per_seq = (static_cast<long>(p.max_q_len) + tokens - 1) / tokens;
@@ -90,6 +92,8 @@ struct PromptScan {
         PromptItem it;
         it.s = -1;
         it.hkv = it.row0 = it.n = it.index = 0;
+        if (u >= p.max_items)
+            return it;
         const unsigned unit = u / p.num_kv_heads;
         while (unit >= before + here) {
             before += here;

@@ -1026,7 +1026,7 @@ bool encode_rows(EncodeTiledFn enc, CUtensorMap *map, const void *base, int D, i
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kSplit> pkv_status launch_ptc(const PromptParams &p, cudaStream_t stream)
+template <int D, bool kSplit> pkv_status launch_ptc(PromptParams p, cudaStream_t stream)
 {
     static ContextCache cache;
     int set = 0;
@@ -1054,6 +1054,7 @@ template <int D, bool kSplit> pkv_status launch_ptc(const PromptParams &p, cudaS
         return PKV_OK;
     if (items > 0x40000000L)
         return PKV_ERR_UNSUPPORTED;
+    p.max_items = static_cast<unsigned>(items);
     const long sms = device_sm_count();
     const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
     prompt_tc_kernel<D, kSplit><<<grid, kThreads, PtGeom<D>::kSmem, stream>>>(p, maps);

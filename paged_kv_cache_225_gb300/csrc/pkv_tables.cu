@@ -31,13 +31,16 @@ constexpr int kStepCtas = 16;
 __device__ __forceinline__ int pages_of(int tokens) { return (tokens + kBlockSize - 1) / kBlockSize; }
 
 // A cluster barrier in two halves: what a CTA did before the first (shared and
-// global memory) is visible to every CTA after the second.
+// global memory) is visible to every CTA after the second.  `.aligned`: a
+// warp's lanes arrive together.
 __device__ __forceinline__ void cluster_arrive()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 

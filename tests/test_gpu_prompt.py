@@ -195,6 +195,28 @@ def test_invalid_ranges_are_reported_and_not_written(dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+def test_starts_that_step_back_end(dtype):
+    # Every other range is the whole batch: a thousand times the items that its
+    # rows allow.  The call ends, reports it and writes nothing but right rows.
+    q, k, v = make([700], 4, 2, 64, dtype, 22)
+    good = torch.zeros(q.shape, dtype=dtype, device=DEV)
+    pkv.prompt_attn(q, k, v, starts([700]), 0.1, good)
+    out = torch.full(q.shape, 7.0, dtype=dtype, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkv.prompt_attn(q, k, v, torch.tensor([0, 700] * 1000, dtype=torch.int32, device=DEV), 0.1, out, status=status)
+    assert int(status) == 4
+    assert bool(((out == good) | (out == 7)).all())
+
+
+def test_a_bound_past_the_rows_is_no_bound():
+    q, k, v = make([40, 50], 4, 2, 64, BF16, 23)
+    a, b = torch.zeros_like(q), torch.zeros_like(q)
+    pkv.prompt_attn(q, k, v, starts([40, 50]), 0.1, a)
+    pkv.prompt_attn(q, k, v, starts([40, 50]), 0.1, b, max_q_len=2 ** 32 + 1)
+    assert torch.equal(a, b) and bool((a != 0).any())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_no_rows(dtype):
     e = torch.empty((0, 4, 64), dtype=dtype, device=DEV)
     out = pkv.prompt_attn(e, e, e, torch.zeros(3, dtype=torch.int32, device=DEV), 0.1, e.clone())
