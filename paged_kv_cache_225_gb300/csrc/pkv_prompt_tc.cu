@@ -32,7 +32,8 @@
 //    diagonal block, which may hold infinities or NaN.  Rows past the item's
 //    keys are zeroed in shared memory; a row whose output is not finite is
 //    computed again from global memory over its own keys when a V row that it
-//    must not see is not finite (redo_rows).
+//    must not see is not finite (redo_rows), after the CTA's last item: a wait
+//    of the other roles for it would have no bound.
 //  * Every wait is bounded; a timeout records PKV_ERR_TIMEOUT, stops every role,
 //    lets copies and MMAs in flight finish and frees TMEM.
 //
@@ -54,6 +55,7 @@
 // instruction caches), two threads per row 8.3 ms / 945 us, the outputs written by
 // the softmax warps 5.8 ms / 525 us, Q prefetched into L2 5.7 ms / 558 us.
 #include <climits>
+#include <type_traits>
 
 #include "pkv_prompt.cuh"
 #include "pkv_tc.cuh"
@@ -287,25 +289,37 @@ __device__ __noinline__ void redo_rows(const PromptParams &p, unsigned rows, int
                                        int hkv, int key_end, int lane)
 {
     constexpr int kPer = D / 32;  // dims per lane
+    using Dims = std::conditional_t<kPer == 4, uint2, uint32_t>;
     const int G = p.group;
+    __syncwarp();  // the rows' first stores come before the ones below
     const unsigned short *kb = static_cast<const unsigned short *>(p.k) +
                                static_cast<size_t>(row0) * p.k_stride + hkv * D;
     const unsigned short *vb = static_cast<const unsigned short *>(p.v) +
                                static_cast<size_t>(row0) * p.v_stride + hkv * D;
     const int first = tok + (r0 + __ffs(rows) - 1) / G;  // earliest token among the rows
     int last_bad = -1, first_inf = INT_MAX;
-    for (int j = kSplit ? 0 : first + 1; j < key_end; ++j) {
-        bool bad = false, inf = false;
+    // Eight keys at a time, so that their loads overlap.
+    for (int j0 = kSplit ? 0 : first + 1; j0 < key_end; j0 += 8) {
+        bool bad[8] = {}, inf[8] = {};
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const unsigned w = vb[j * p.v_stride + lane * kPer + e] & 0x7fffu;
-            bad = bad || w >= 0x7f80u;
-            inf = inf || w == 0x7f80u;
+        for (int i = 0; i < 8; ++i) {
+            const int j = min(j0 + i, key_end - 1);
+            unsigned short w[kPer];
+            *reinterpret_cast<Dims *>(w) = *reinterpret_cast<const Dims *>(vb + j * p.v_stride + lane * kPer);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                bad[i] = bad[i] || (w[e] & 0x7fffu) >= 0x7f80u;
+                inf[i] = inf[i] || (w[e] & 0x7fffu) == 0x7f80u;
+            }
         }
-        if (__any_sync(kFullMask, bad))
-            last_bad = j;
-        if (kSplit && first_inf == INT_MAX && __any_sync(kFullMask, inf))
-            first_inf = j;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = min(j0 + i, key_end - 1);
+            if (__any_sync(kFullMask, bad[i]))
+                last_bad = j;
+            if (kSplit && first_inf == INT_MAX && __any_sync(kFullMask, inf[i]))
+                first_inf = j;
+        }
     }
     for (; rows; rows &= rows - 1) {
         const int r = r0 + __ffs(rows) - 1;
@@ -349,9 +363,12 @@ __device__ __noinline__ void redo_rows(const PromptParams &p, unsigned rows, int
             for (int e = 0; e < kPer; ++e)
                 o[e] *= alpha;
             const int cnt = min(32, pos + 1 - j0);
+#pragma unroll 8
             for (int i = 0; i < cnt; ++i) {
                 const float w = __shfl_sync(kFullMask, wgt, i);
-                const unsigned short *vr = vb + (j0 + i) * p.v_stride + lane * kPer;
+                unsigned short vr[kPer];
+                *reinterpret_cast<Dims *>(vr) =
+                    *reinterpret_cast<const Dims *>(vb + (j0 + i) * p.v_stride + lane * kPer);
 #pragma unroll
                 for (int e = 0; e < kPer; ++e)
                     o[e] = fmaf(w, __uint_as_float(static_cast<uint32_t>(vr[e]) << 16), o[e]);
@@ -368,6 +385,52 @@ __device__ __noinline__ void redo_rows(const PromptParams &p, unsigned rows, int
                 static_cast<float *>(p.out)[off + e] = y;
             else
                 static_cast<__nv_bfloat16 *>(p.out)[off + e] = __float2bfloat16(y);
+        }
+    }
+}
+
+// The k-th item of this CTA.  Alternating direction: a CTA late in one row of
+// items is early in the next, so that the CTAs' totals stay even.
+__device__ __forceinline__ unsigned item_number(unsigned k)
+{
+    return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+// The items first .. last of this CTA once more: a warp looks at the rows that
+// it has stored (lane i at row r0 + i) and hands those that are not finite to
+// redo_rows.
+template <int D, bool kSplit>
+__device__ __noinline__ void redo_items(const PromptParams &p, unsigned first, unsigned last, int r0, int lane)
+{
+    const int G = p.group, R = kM / G;
+    const int r = r0 + lane;
+    PromptScan scan;
+    scan.init(p, 2 * R, lane, false);
+    for (unsigned k = first; k <= last; ++k) {
+        const PromptItem found = scan.find(p, 2 * R, item_number(k), lane);
+        const int w[5] = {found.s, found.hkv, found.row0, found.n, found.index * 2 * R};
+        PtItem it;
+        it.fill(w, R);
+        for (int t = 0; t < 2; ++t) {
+            const int nt = it.nt[t], nb = it.nb[t], tok = it.tok0 + t * R;
+            bool bad = false;
+            if (r < nt * G) {
+                const size_t off = (static_cast<size_t>(it.row0 + tok + r / G) * p.num_q_heads +
+                                    it.hkv * G + r % G) * D;
+                for (int e = 0; e < D; ++e) {
+                    float y;
+                    if constexpr (kSplit)
+                        y = static_cast<const float *>(p.out)[off + e];
+                    else
+                        y = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.out)[off + e]);
+                    bad = bad || !(y * 0.f == 0.f);
+                }
+            }
+            const unsigned rows = __ballot_sync(kFullMask, bad);
+            if (rows)
+                redo_rows<D, kSplit>(p, rows, r0, tok, it.row0, it.hkv,
+                                     min((nb - 1) * kKeys + block_cols(nb, it.end[t], nb - 1),
+                                         max(it.end[0], it.end[1])), lane);
         }
     }
 }
@@ -564,10 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         scan.init(p, 2 * R, lane, blockIdx.x == 0);
         bool ok = true;
         for (unsigned k = 0; ok; ++k) {
-            // Alternating direction: a CTA late in one row of items is early
-            // in the next, so that the CTAs' totals stay even.
-            const unsigned u = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-            const PromptItem found = scan.find(p, 2 * R, u, lane);
+            const PromptItem found = scan.find(p, 2 * R, item_number(k), lane);
             if (lane == 0) {
                 const int slot = k % kQueue;
                 if (k >= kQueue)
@@ -932,6 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         uint32_t par = 0;  // bit t: parity of the tile's barriers
+        unsigned redo0 = ~0u, redo1 = 0;  // first and last item with a row that is not finite
         bool failed = false;
         for (unsigned k = 0; !failed; ++k) {
             const int slot = k % kQueue;
@@ -949,7 +1010,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int t = 0; t < 2; ++t) {
                 const int nt = t ? it.nt[1] : it.nt[0], nb = t ? it.nb[1] : it.nb[0];
-                const int end = t ? it.end[1] : it.end[0];
                 if (nb == 0)
                     continue;
                 const int first = it.tok0 + t * R;
@@ -985,13 +1045,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (live)
                         store_out32<kSplit>(p, orow + c0, ov, wide);
                 }
-                const unsigned redo = __ballot_sync(kFullMask, live && bad != 0.f);
-                if (redo)
-                    redo_rows<D, kSplit>(p, redo, 32 * (warp & 3), first, it.row0, it.hkv,
-                                         min((nb - 1) * kKeys + block_cols(nb, end, nb - 1),
-                                             max(it.end[0], it.end[1])), lane);
+                if (__any_sync(kFullMask, live && bad != 0.f)) {
+                    redo0 = min(redo0, k);
+                    redo1 = k;
+                }
             }
         }
+        if (!failed && redo0 <= redo1)
+            redo_items<D, kSplit>(p, redo0, redo1, 32 * (warp & 3), lane);
         if (failed && lane == 0) {
             set_status(p.status, PKV_ERR_TIMEOUT);
             *abort = 1;

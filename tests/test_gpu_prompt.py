@@ -348,3 +348,23 @@ def test_two_calls_at_once(dtype):
     torch.cuda.synchronize()
     for _, _, _, _, want, got, _ in runs:
         assert torch.equal(want, got)
+
+
+def test_rows_of_a_very_long_prompt_are_computed_again():
+    # The last V row is infinite: the rows before it in its block are computed
+    # again over half a million keys each, which the waits must allow for.
+    n, D, scale = 1 << 19, 64, 0.125
+    q, k, v = make([n], 1, 1, D, BF16, 24)
+    v[-1] = math.inf
+    out = torch.zeros(q.shape, dtype=BF16, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkv.prompt_attn(q, k, v, starts([n]), scale, out, status=status)
+    assert int(status) == 0
+    assert bool((out[-1] == math.inf).all()) and bool(torch.isfinite(out[:-1]).all())
+    for i in (0, 1000, n // 2, n - 130, n - 128, n - 77, n - 2):
+        qq, kk, vv = q[i, 0].double(), k[:i + 1, 0].double(), v[:i + 1, 0].double()
+        p = torch.softmax(kk @ qq * scale, 0)
+        ref, mass = p @ vv, p @ vv.abs()
+        most = float((kk.abs() @ qq.abs()).max())
+        tol = tolerance(ref, mass, most, [i + 1], D, scale, BF16, BF16)
+        assert bool(((out[i, 0].double() - ref).abs() <= tol).all()), i
