@@ -140,38 +140,49 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a, uint64_t 
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u));
 }
 
-// 32 columns of the warp's 32 lanes; valid after tmem_wait_ld.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v)
+// 32 columns of the warp's 32 lanes.  Load and wait are one statement: between
+// two, the compiler may copy registers that the load has yet to fill.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
 {
-    uint32_t r[32];
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        v[i] = __uint_as_float(r[i]);
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+        "%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+          "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
+          "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
+          "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]),
+          "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr)
+        : "memory");
 }
-
-// Waits for the loads above and ties the values to the wait: nothing that
-// uses them can be scheduled before it.
-template <int N> __device__ __forceinline__ void tie(float (&v)[N])
+// 64 columns.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&x)[32], float (&y)[32])
 {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        asm volatile("" : "+f"(v[i]));
-}
-template <int N> __device__ __forceinline__ void tmem_wait_ld(float (&v)[N])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        asm volatile("" : "+f"(v[i]));
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+        "%28,%29,%30,%31}, [%64];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,"
+        "%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,"
+        "%60,%61,%62,%63}, [%65];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]),
+          "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]),
+          "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15]), "=f"(x[16]), "=f"(x[17]),
+          "=f"(x[18]), "=f"(x[19]), "=f"(x[20]), "=f"(x[21]), "=f"(x[22]), "=f"(x[23]),
+          "=f"(x[24]), "=f"(x[25]), "=f"(x[26]), "=f"(x[27]), "=f"(x[28]), "=f"(x[29]),
+          "=f"(x[30]), "=f"(x[31]),
+          "=f"(y[0]), "=f"(y[1]), "=f"(y[2]), "=f"(y[3]), "=f"(y[4]), "=f"(y[5]),
+          "=f"(y[6]), "=f"(y[7]), "=f"(y[8]), "=f"(y[9]), "=f"(y[10]), "=f"(y[11]),
+          "=f"(y[12]), "=f"(y[13]), "=f"(y[14]), "=f"(y[15]), "=f"(y[16]), "=f"(y[17]),
+          "=f"(y[18]), "=f"(y[19]), "=f"(y[20]), "=f"(y[21]), "=f"(y[22]), "=f"(y[23]),
+          "=f"(y[24]), "=f"(y[25]), "=f"(y[26]), "=f"(y[27]), "=f"(y[28]), "=f"(y[29]),
+          "=f"(y[30]), "=f"(y[31])
+        : "r"(taddr), "r"(taddr + 32)
+        : "memory");
 }
 
 // Two f32 fused multiply-adds / adds in one instruction.
@@ -879,10 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int c0 = 0; c0 < (second ? kKeys : kPart); c0 += 64) {
                     float x[32], y[32];
-                    tmem_ld32(scol + c0, x);
-                    tmem_ld32(scol + c0 + 32, y);
-                    tmem_wait_ld(x);
-                    tie(y);
+                    tmem_ld64(scol + c0, x, y);
                     if (tail) {
                         mask32(x, lim - c0);
                         mask32(y, lim - c0 - 32);
@@ -941,10 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (kPart * part < cols) {
                         const uint32_t pc = scol + kPart * part;
                         float x[32], y[32];
-                        tmem_ld32(pc, x);
-                        tmem_ld32(pc + 32, y);
-                        tmem_wait_ld(x);
-                        tie(y);
+                        tmem_ld64(pc, x, y);
                         if (tail) {
                             mask32(x, lim - kPart * part);
                             mask32(y, lim - kPart * part - 32);
@@ -1030,7 +1035,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     float ov[32];
                     tmem_ld32(ocol + c0, ov);
-                    tmem_wait_ld(ov);
                     if (c0 + 32 == D) {  // read whole: the next item's P V may start
                         tc_fence_before();
                         __syncwarp();
