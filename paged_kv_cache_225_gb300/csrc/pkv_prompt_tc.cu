@@ -38,17 +38,17 @@
 //    lets copies and MMAs in flight finish and frees TMEM.
 //
 // What bounds it.  Long prompts: the tensor cores (a 32K prompt of 32 heads of
-// 128 over 8 KV heads: 5.7 ms, 1.54 PFLOP/s, 91% of what a cuBLAS product
+// 128 over 8 KV heads: 5.5 ms, 1.6 PFLOP/s, 94% of what a cuBLAS product
 // sustains on the same part).  A block takes them 2 x 1024 cycles; a tile's
 // softmax of about 1200 cycles hides behind the other tile's products.  The
 // queue of the tensor cores holds about three MMAs, so the issuing thread may
 // spend only some 200 cycles between two groups: hence one barrier per group
 // (the gate), one commit per step for the ring, and a loop of its own for
-// whole blocks.  Short prompts (128 of 256 to 512 tokens, 64 heads: 521 us,
-// 3.4 TB/s): the chain load - S - softmax - P V - store of items two blocks long,
+// whole blocks.  Short prompts (128 of 256 to 512 tokens, 64 heads: 498 us,
+// 3.6 TB/s): the chain load - S - softmax - P V - store of items two blocks long,
 // and the issuing thread's general steps.
 //
-// Measured and not taken (same box; 32K prompt / chat batch): an issuing thread
+// Measured and not taken (32K prompt / chat batch, 5.7 ms / 521 us then): an issuing thread
 // per tile 8.1 ms / 501 us (both tiles' products run interleaved, then both
 // softmaxes; taking turns costs more), scores kept in registers between the
 // maximum and the weights 5.9 ms / 530 us (spills, and code that leaves the
@@ -120,6 +120,42 @@ struct PtItem {
 __device__ __forceinline__ int block_cols(int nb, int end, int j)
 {
     return j + 1 < nb ? kKeys : (end - j * kKeys + 15) & ~15;
+}
+
+// As tc_wait, but asleep until the phase ends: try_wait gives up soon by itself,
+// and a thread that then reads the timer and the flag and looks again notices
+// the end late and takes issue slots from the softmax warps.  The softmax warps' own
+// waits are short and keep tc_wait.  Asleep none / the others / all: chat batch
+// (above) 516 / 498 / 498 us, a 32K prompt 5.59 / 5.50 / 5.75 ms.
+__device__ __forceinline__ bool mbar_try_wait_long(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)  // ns
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool sleep_wait(uint64_t *bar, uint32_t parity, const volatile int *abort)
+{
+    if (mbar_try_wait_long(bar, parity))
+        return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (mbar_try_wait_long(bar, parity))
+            return true;
+        if (*abort)
+            return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs)
+            return false;
+    }
+}
+__device__ __forceinline__ bool warp_sleep_wait(uint64_t *bar, uint32_t parity, const volatile int *abort)
+{
+    return __all_sync(kFullMask, sleep_wait(bar, parity, abort));
 }
 
 // Shared-memory descriptor of a 128-byte-swizzled operand (atoms of 8 rows x
@@ -531,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Step i (from 0) gives back tiles 2 i - 1 and 2 i of the ring's
                 // sequence K, V, K, V, ...: V of a block and the next K.
                 for (; kv >= NS && 2 * steps < kv - NS + 2; ++steps)
-                    if (!tc_wait(&step_done[steps % kSteps], (steps / kSteps) & 1, abort))
+                    if (!sleep_wait(&step_done[steps % kSteps], (steps / kSteps) & 1, abort))
                         return false;
                 mbar_arrive_expect_tx(&full[st], Geo::kTile);
                 for (int h = 0; h < D / 64; ++h) {
@@ -545,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             for (unsigned k = 0; ok; ++k) {
                 const int slot = k % kQueue;
-                ok = tc_wait(&item_full[slot], (k / kQueue) & 1, abort);
+                ok = sleep_wait(&item_full[slot], (k / kQueue) & 1, abort);
                 if (!ok)
                     break;
                 PtItem it;
@@ -559,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (it.nt[t] == 0)
                             continue;
                         if (qn[t] > 0)
-                            ok = tc_wait(&q_empty[t], (qn[t] - 1) & 1, abort);
+                            ok = sleep_wait(&q_empty[t], (qn[t] - 1) & 1, abort);
                         if (!ok)
                             break;
                         mbar_arrive_expect_tx(&q_full[t], (D / 64) * G * R * 128);
@@ -595,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t blocks = 0;  // of tile 0
             bool ok = true;
             auto arrived = [&] {
-                ok = ok && tc_wait(&full[st], par, abort);
+                ok = ok && sleep_wait(&full[st], par, abort);
                 if (++st == NS) {
                     st = 0;
                     par ^= 1;
@@ -603,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             for (unsigned k = 0; ok; ++k) {
                 const int slot = k % kQueue;
-                ok = tc_wait(&item_full[slot], (k / kQueue) & 1, abort);
+                ok = sleep_wait(&item_full[slot], (k / kQueue) & 1, abort);
                 if (!ok)
                     break;
                 PtItem it;
@@ -620,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         continue;
                     // Not before the block before has all its arrivals.
                     if (blocks > 0)
-                        ok = ok && tc_wait(&p_full[0][0], (blocks - 1) & 1, abort);
+                        ok = ok && sleep_wait(&p_full[0][0], (blocks - 1) & 1, abort);
                     ++blocks;
                     if (ok)
                         mbar_arrive(&p_full[0][0]);
@@ -642,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 const int slot = k % kQueue;
                 if (k >= kQueue)
-                    ok = tc_wait(&item_empty[slot], ((k / kQueue) - 1) & 1, abort);
+                    ok = sleep_wait(&item_empty[slot], ((k / kQueue) - 1) & 1, abort);
                 if (ok) {
                     int *w = s_item[slot];
                     w[0] = found.s;
@@ -714,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int nnb0 = 0, nnb1 = 0, nend0 = 0, nend1 = 0, nblocks = 0;   // the next one
             auto next_item = [&] {
                 const int slot = k % kQueue;
-                ok = ok && tc_wait(&item_full[slot], (k / kQueue) & 1, abort);
+                ok = ok && sleep_wait(&item_full[slot], (k / kQueue) & 1, abort);
                 nblocks = 0;
                 if (!ok)
                     return;
@@ -744,14 +780,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int whole = min(nb0, nb1) - 2;
                 for (; j >= 0 && j < whole && ok; ++j) {
                     if (j == 0) {
-                        ok = tc_wait(&o_free[0], o_par & 1, abort) && tc_wait(&o_free[1], o_par >> 1, abort);
+                        ok = sleep_wait(&o_free[0], o_par & 1, abort) && sleep_wait(&o_free[1], o_par >> 1, abort);
                         o_par ^= 3;
                     }
 #pragma unroll
                     for (uint32_t t = 0; t < 2; ++t) {
 #pragma unroll
                         for (int part = 0; part < kParts; ++part) {
-                            ok = ok && tc_wait(&p_full[t][part], p_par >> t & 1, abort);
+                            ok = ok && sleep_wait(&p_full[t][part], p_par >> t & 1, abort);
                             tc_fence_after();
                             if (ok)
                                 mma_pv(t, part, kPart / 16, j == 0 && part == 0);
@@ -776,16 +812,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int nb = t ? nb1 : nb0, end = t ? end1 : end0;
                     if (j >= 0 && j < nb) {
                         if (j == 0) {  // the output of the tile's item before this one is read
-                            ok = ok && tc_wait(&o_free[t], o_par >> t & 1, abort);
+                            ok = ok && sleep_wait(&o_free[t], o_par >> t & 1, abort);
                             o_par ^= 1u << t;
                         }
                         // V is there: the gate's arrival stands for it, and tile
                         // 0 comes first in the step.
                         if (j >= nb0)
-                            ok = ok && tc_wait(&full[vst], vpar, abort);
+                            ok = ok && sleep_wait(&full[vst], vpar, abort);
                         const int steps = block_cols(nb, end, j) / 16;
                         for (int part = 0; part < kParts && kPart / 16 * part < steps; ++part) {
-                            ok = ok && tc_wait(&p_full[t][part], p_par >> t & 1, abort);
+                            ok = ok && sleep_wait(&p_full[t][part], p_par >> t & 1, abort);
                             tc_fence_after();
                             if (ok)
                                 mma_pv(t, part, steps - kPart / 16 * part, j == 0 && part == 0);
@@ -801,13 +837,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int qnb = last ? (t ? nnb1 : nnb0) : nb, qend = last ? (t ? nend1 : nend0) : end;
                     if (ok && more && nj < qnb) {
                         if (nj == 0) {
-                            ok = tc_wait(&q_full[t], q_par >> t & 1, abort);
+                            ok = sleep_wait(&q_full[t], q_par >> t & 1, abort);
                             q_par ^= 1u << t;
                         }
                         // So is K, but for an item's first block and those that
                         // tile 0 does not see.
                         if (t == 0 ? nj == 0 : nj >= (last ? nnb0 : nb0))
-                            ok = ok && tc_wait(&full[kst], kpar, abort);
+                            ok = ok && sleep_wait(&full[kst], kpar, abort);
                         tc_fence_after();
                         if (ok)
                             mma_s(t, id_s0 | (static_cast<uint32_t>(block_cols(qnb, qend, nj)) >> 3) << 17);
@@ -1001,7 +1037,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool failed = false;
         for (unsigned k = 0; !failed; ++k) {
             const int slot = k % kQueue;
-            if (!warp_wait(&item_full[slot], (k / kQueue) & 1, abort)) {
+            if (!warp_sleep_wait(&item_full[slot], (k / kQueue) & 1, abort)) {
                 failed = true;
                 break;
             }
@@ -1019,8 +1055,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     continue;
                 const int first = it.tok0 + t * R;
                 const uint32_t ocol = tmem + lanes + Geo::kOCol + t * D;
-                if (!warp_wait(&l_full[t], par >> t & 1, abort) ||
-                    !warp_wait(&o_full[t], par >> t & 1, abort)) {
+                if (!warp_sleep_wait(&l_full[t], par >> t & 1, abort) ||
+                    !warp_sleep_wait(&o_full[t], par >> t & 1, abort)) {
                     failed = true;
                     break;
                 }
