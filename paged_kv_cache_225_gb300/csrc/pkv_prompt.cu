@@ -20,8 +20,8 @@
 // Rows per thread trade loads for warps that hide them: 8 rows (128 threads, 250
 // registers) load least, but two CTAs are then 8 warps to an SM; 2 rows load twice
 // as often as 4.  8 prompts of 256 to 1024 tokens, 32 heads of 128 over 8 KV
-// heads: 919 us with 8 rows, 898 us (33 TFLOP/s) with 4, 1241 us with 2; one
-// prompt of a few tokens 11.8, 10.0 and 10.5 us.  Single multiply-adds with one
+// heads: 919 us with 8 rows, 898 us (33 TFLOP/s) with 4, 1241 us with 2; four
+// prompts of 1 to 64 tokens 11.8, 10.0 and 10.5 us.  Single multiply-adds with one
 // shared load per operand pair took 1233 us.
 #include "pkv_prompt.cuh"
 
