@@ -480,7 +480,8 @@ pkv_status pkv_copy_blocks(void *k_cache, void *v_cache, pkv_dtype kv_dtype, int
  *   status       optional device int32, as for pkv_reshape_and_cache: a sequence
  *                whose q_start range is invalid or longer than max_q_len is
  *                reported as PKV_ERR_OUT_OF_RANGE and not written (with starts
- *                that step back, other sequences may not be either).
+ *                that step back, other sequences may not be either).  Without
+ *                status, rows left as they were are the only sign of it.
  *   flags        0, or PKV_FLAG_TEST_DROP_FIRST_COPY (BF16 only): the failure path,
  *                PKV_ERR_TIMEOUT in *status and undefined output rows.
  * Needs no workspace and no host copy of q_start; can be captured in a graph.

@@ -45,6 +45,8 @@ constexpr int kTablesRowBytes = 16;   // shared memory per row
 // Each launches on `stream` and returns a status, as the units of pkv_internal.h.
 pkv_status launch_prompt_simt(const PromptParams &p, cudaStream_t stream);  // fp32
 pkv_status launch_prompt_tc(const PromptParams &p, cudaStream_t stream);    // bf16
+// Row ranges alone, for calls without a row to attend: invalid ones are reported.
+pkv_status launch_prompt_ranges(const PromptParams &p, cudaStream_t stream);
 pkv_status launch_tables_step(const TablesParams &p, cudaStream_t stream);
 pkv_status launch_tables_fork(const int32_t *pairs, int num_pairs, int32_t *seq_lens,
                               int32_t *block_tables, int32_t *ref_counts, int num_seqs,

@@ -43,8 +43,21 @@ pkv_status pkv_prompt_attn(const void *q, const void *k, const void *v, pkv_dtyp
     if (!std::isfinite(scale) || (flags & ~PKV_FLAG_TEST_DROP_FIRST_COPY) != 0 ||
         (flags != 0 && dtype != PKV_BF16))
         return PKV_ERR_INVALID_ARG;
-    if (num_seqs == 0 || num_tokens == 0 || max_q_len == 0)
+    // A call without rows computes nothing, but its ranges are looked at all the same.
+    const bool no_rows = num_tokens == 0 || max_q_len == 0;
+    if (num_seqs == 0 || (no_rows && (!status || !q_start)))
         return PKV_OK;
+    if (no_rows) {
+        if (!aligned(q_start, 4) || !aligned(status, 4))
+            return PKV_ERR_INVALID_ARG;
+        PromptParams p;
+        std::memset(&p, 0, sizeof p);
+        p.q_start = q_start;
+        p.status = status;
+        p.num_seqs = num_seqs;
+        p.num_tokens = num_tokens;
+        return launch_prompt_ranges(p, static_cast<cudaStream_t>(stream));
+    }
     if (!q || !k || !v || !q_start || !out)
         return PKV_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||

@@ -289,6 +289,13 @@ __global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const Prom
     }
 }
 
+__global__ void __launch_bounds__(kSimtThreads) prompt_ranges_kernel(const PromptParams p)
+{
+    int start;
+    for (int s = threadIdx.x; s < p.num_seqs; s += kSimtThreads)
+        prompt_len(p, s, start, true);
+}
+
 template <int D> pkv_status launch_simt_d(PromptParams p, cudaStream_t stream)
 {
     static ContextCache cache;
@@ -316,6 +323,12 @@ template <int D> pkv_status launch_simt_d(PromptParams p, cudaStream_t stream)
 }
 
 }  // namespace
+
+pkv_status launch_prompt_ranges(const PromptParams &p, cudaStream_t stream)
+{
+    prompt_ranges_kernel<<<1, kSimtThreads, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
 
 pkv_status launch_prompt_simt(const PromptParams &p, cudaStream_t stream)
 {

@@ -368,3 +368,25 @@ def test_rows_of_a_very_long_prompt_are_computed_again():
         most = float((kk.abs() @ qq.abs()).max())
         tol = tolerance(ref, mass, most, [i + 1], D, scale, BF16, BF16)
         assert bool(((out[i, 0].double() - ref).abs() <= tol).all()), i
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_calls_without_rows_report_their_ranges(dtype):
+    # No rows, or a bound of 0: nothing is computed, a range that is not empty is reported.
+    q, k, v = make([5], 4, 2, 64, dtype, 1)
+
+    def run(qs, n, **kw):
+        out = torch.full((n,) + tuple(q.shape[1:]), 7.0, dtype=dtype, device=DEV)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        pkv.prompt_attn(q[:n], k[:n], v[:n], torch.tensor(qs, dtype=torch.int32, device=DEV), 0.1, out,
+                        status=status, **kw)
+        assert bool((out == 7).all())
+        return int(status)
+
+    assert run([0, 0, 0], 0) == 0
+    assert run([0, 0, 5], 0) == 4
+    assert run([0, -1, 0], 0) == 4
+    assert run([0] * 700 + [1], 0) == 4
+    assert run([0, 5], 5, max_q_len=0) == 4
+    assert run([3, 3, 3], 5, max_q_len=0) == 0
+    assert run([6, 6], 5, max_q_len=0) == 4
