@@ -106,6 +106,9 @@ typedef enum {
  * PKV_ERR_TIMEOUT (after about one second) instead of hanging.  Output rows
  * are then undefined. */
 #define PKV_FLAG_TEST_DROP_FIRST_COPY 0x100
+/* Test hook of pkv_prompt_attn (BF16): the warp that watches the copies for the
+ * MMA thread looks at each one 20 us late.  The results are the same. */
+#define PKV_FLAG_TEST_SLOW_GATE 0x400
 
 /*
  * Workspace bytes pkv_paged_attn_decode needs for these sizes (always >= 256:
@@ -482,8 +485,9 @@ pkv_status pkv_copy_blocks(void *k_cache, void *v_cache, pkv_dtype kv_dtype, int
  *                reported as PKV_ERR_OUT_OF_RANGE and not written (with starts
  *                that step back, other sequences may not be either).  Without
  *                status, rows left as they were are the only sign of it.
- *   flags        0, or PKV_FLAG_TEST_DROP_FIRST_COPY (BF16 only): the failure path,
- *                PKV_ERR_TIMEOUT in *status and undefined output rows.
+ *   flags        0, or for BF16 the test hooks PKV_FLAG_TEST_DROP_FIRST_COPY (the
+ *                failure path, PKV_ERR_TIMEOUT in *status and undefined output
+ *                rows) and PKV_FLAG_TEST_SLOW_GATE (the same results, later).
  * Needs no workspace and no host copy of q_start; can be captured in a graph.
  */
 pkv_status pkv_prompt_attn(const void *q, const void *k, const void *v, pkv_dtype dtype,

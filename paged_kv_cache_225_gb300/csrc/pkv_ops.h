@@ -23,6 +23,7 @@ struct PromptParams {
     float score_scale;       // |scale| * log2(e), at least 2^-120
     int negate;              // scale < 0: the kernels negate the scores
     int drop_first_copy;     // test hook: never issue the first copy of CTA 0
+    int slow_gate;           // test hook: the warp that watches the loads looks 20 us late
 };
 
 // One scheduling step of a page pool kept in device memory.

@@ -40,7 +40,7 @@ pkv_status pkv_prompt_attn(const void *q, const void *k, const void *v, pkv_dtyp
         return PKV_ERR_UNSUPPORTED;
     if (num_q_heads / num_kv_heads > 16)
         return PKV_ERR_UNSUPPORTED;
-    if (!std::isfinite(scale) || (flags & ~PKV_FLAG_TEST_DROP_FIRST_COPY) != 0 ||
+    if (!std::isfinite(scale) || (flags & ~(PKV_FLAG_TEST_DROP_FIRST_COPY | PKV_FLAG_TEST_SLOW_GATE)) != 0 ||
         (flags != 0 && dtype != PKV_BF16))
         return PKV_ERR_INVALID_ARG;
     // A call without rows computes nothing, but its ranges are looked at all the same.
@@ -101,6 +101,7 @@ pkv_status pkv_prompt_attn(const void *q, const void *k, const void *v, pkv_dtyp
     p.score_scale = factor < least ? least : factor > most ? most : factor;
     p.negate = scale < 0.f ? 1 : 0;
     p.drop_first_copy = (flags & PKV_FLAG_TEST_DROP_FIRST_COPY) ? 1 : 0;
+    p.slow_gate = (flags & PKV_FLAG_TEST_SLOW_GATE) ? 1 : 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return dtype == PKV_BF16 ? launch_prompt_tc(p, st) : launch_prompt_simt(p, st);
 }

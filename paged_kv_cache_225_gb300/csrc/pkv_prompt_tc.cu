@@ -625,13 +625,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------- K / V gate
         // Waits for V of block j and K of the next one and counts as the fifth
         // arrival on tile 0's first part of P, so that the MMA thread has one
-        // barrier to look at where it would have three.
+        // barrier to look at where it would have three.  It looks at no other
+        // load: the ring gives a slot back when the MMA thread has used it, and
+        // only the arrival that follows holds the MMA thread back until the
+        // gate has seen the slot full.  A wait for K of an item's first block,
+        // or for V that only tile 1 sees, could come a whole turn of the ring
+        // late and never end.
         if (lane == 0) {
             uint32_t st = 0, par = 0;
             uint32_t blocks = 0;  // of tile 0
             bool ok = true;
-            auto arrived = [&] {
-                ok = ok && sleep_wait(&full[st], par, abort);
+            auto pass = [&](bool look) {  // one tile of the ring
+                if (look && p.slow_gate)
+                    for (int i = 0; i < 20; ++i)
+                        __nanosleep(1000);
+                ok = ok && (!look || sleep_wait(&full[st], par, abort));
                 if (++st == NS) {
                     st = 0;
                     par ^= 1;
@@ -647,12 +655,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&item_empty[slot]);
                 if (it.s < 0)
                     break;
-                arrived();  // K of block 0: the MMA thread waits for it itself
+                pass(false);  // K of block 0: the MMA thread waits for it itself
                 for (int j = 0; j < it.blocks && ok; ++j) {
-                    arrived();
+                    const bool gated = j < it.nb[0];
+                    pass(gated);
                     if (j + 1 < it.blocks)
-                        arrived();
-                    if (j >= it.nb[0])
+                        pass(gated);
+                    if (!gated)
                         continue;
                     // Not before the block before has all its arrivals.
                     if (blocks > 0)

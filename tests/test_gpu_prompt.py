@@ -390,3 +390,16 @@ def test_calls_without_rows_report_their_ranges(dtype):
     assert run([0, 5], 5, max_q_len=0) == 4
     assert run([3, 3, 3], 5, max_q_len=0) == 0
     assert run([6, 6], 5, max_q_len=0) == 4
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[2000], [130] * 200, [700, 1, 129, 300, 17, 255, 1100] * 4])
+def test_a_late_watcher_of_the_loads(lens, D):
+    # The warp that watches the loads looks at each 20 us late, when all that does not wait for it has
+    # run ahead: the same bits, and no wait runs out.
+    q, k, v = make(lens, 8, 2, D, BF16, 26)
+    a, b = torch.zeros_like(q), torch.zeros_like(q)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkv.prompt_attn(q, k, v, starts(lens), 0.1, a)
+    pkv.prompt_attn(q, k, v, starts(lens), 0.1, b, status=status, flags=pkv.FLAG_TEST_SLOW_GATE)
+    assert int(status) == 0 and torch.equal(a, b) and bool((a != 0).any())

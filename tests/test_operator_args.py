@@ -127,3 +127,8 @@ def test_tensors_that_do_not_fit():
         pkv.tables_step(lens, tab[:2], ref)
     with pytest.raises(ValueError):
         pkv.tables_fork(torch.zeros((1, 3), **i32), lens, tab, ref)
+
+
+def test_slow_gate_flag_is_for_bf16():
+    assert prompt(flags=pkv.FLAG_TEST_SLOW_GATE, dtype=pkv.F32) == INVALID
+    assert prompt(flags=pkv.FLAG_TEST_SLOW_GATE, T=0, q=None) == OK
