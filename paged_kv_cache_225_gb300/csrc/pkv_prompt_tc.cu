@@ -655,13 +655,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&item_empty[slot]);
                 if (it.s < 0)
                     break;
-                pass(false);  // K of block 0: the MMA thread waits for it itself
-                for (int j = 0; j < it.blocks && ok; ++j) {
-                    const bool gated = j < it.nb[0];
+                // K of block 0, which the MMA thread waits for itself, is tile 0.
+                for (int i = 0, tiles = 2 * it.blocks; i < tiles && ok; ++i) {
+                    const int j = (i - 1) >> 1;  // the block whose step uses it
+                    const bool gated = i > 0 && j < it.nb[0];
                     pass(gated);
-                    if (j + 1 < it.blocks)
-                        pass(gated);
-                    if (!gated)
+                    // After K of the next block, or the last V.
+                    if (!gated || ((i & 1) && i + 1 < tiles))
                         continue;
                     // Not before the block before has all its arrivals.
                     if (blocks > 0)
