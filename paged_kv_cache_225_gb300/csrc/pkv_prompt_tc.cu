@@ -324,6 +324,10 @@ __device__ __forceinline__ void store_out32(const PromptParams &p, size_t off, c
     }
 }
 
+// The e-th bf16 of two or four loaded as one word, as its bits.
+__device__ __forceinline__ uint32_t bf16_bits(uint32_t x, int e) { return e ? x >> 16 : x & 0xffffu; }
+__device__ __forceinline__ uint32_t bf16_bits(uint2 x, int e) { return bf16_bits(e & 2 ? x.y : x.x, e & 1); }
+
 // The rows of a warp that came out infinite or NaN (lane mask `rows`, lane i
 // owning row r0 + i of the tile).  A row is computed again over the keys it
 // sees if a V row after them, before `key_end`, the end of the keys the MMAs
@@ -351,12 +355,11 @@ __device__ __noinline__ void redo_rows(const PromptParams &p, unsigned rows, int
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int j = min(j0 + i, key_end - 1);
-            unsigned short w[kPer];
-            *reinterpret_cast<Dims *>(w) = *reinterpret_cast<const Dims *>(vb + j * p.v_stride + lane * kPer);
+            const Dims w = *reinterpret_cast<const Dims *>(vb + j * p.v_stride + lane * kPer);
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
-                bad[i] = bad[i] || (w[e] & 0x7fffu) >= 0x7f80u;
-                inf[i] = inf[i] || (w[e] & 0x7fffu) == 0x7f80u;
+                bad[i] = bad[i] || (bf16_bits(w, e) & 0x7fffu) >= 0x7f80u;
+                inf[i] = inf[i] || (bf16_bits(w, e) & 0x7fffu) == 0x7f80u;
             }
         }
 #pragma unroll
@@ -413,12 +416,10 @@ __device__ __noinline__ void redo_rows(const PromptParams &p, unsigned rows, int
 #pragma unroll 8
             for (int i = 0; i < cnt; ++i) {
                 const float w = __shfl_sync(kFullMask, wgt, i);
-                unsigned short vr[kPer];
-                *reinterpret_cast<Dims *>(vr) =
-                    *reinterpret_cast<const Dims *>(vb + (j0 + i) * p.v_stride + lane * kPer);
+                const Dims vr = *reinterpret_cast<const Dims *>(vb + (j0 + i) * p.v_stride + lane * kPer);
 #pragma unroll
                 for (int e = 0; e < kPer; ++e)
-                    o[e] = fmaf(w, __uint_as_float(static_cast<uint32_t>(vr[e]) << 16), o[e]);
+                    o[e] = fmaf(w, __uint_as_float(bf16_bits(vr, e) << 16), o[e]);
             }
         }
 #pragma unroll
