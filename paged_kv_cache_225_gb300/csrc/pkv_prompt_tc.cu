@@ -30,10 +30,9 @@
 //    then rescaled in TMEM by the rows' threads.
 //  * P V multiplies a masked weight 0 with the V rows of later tokens in the
 //    diagonal block, which may hold infinities or NaN.  Rows past the item's
-//    keys are zeroed in shared memory; a row whose output is not finite is
-//    computed again from global memory over its own keys when a V row that it
-//    must not see is not finite (redo_rows), after the CTA's last item: a wait
-//    of the other roles for it would have no bound.
+//    keys are zeroed in shared memory; items with an output that is not finite
+//    are looked at again by all warps after the CTA's last one (redo_items): in
+//    between, the other roles would have to wait for it.
 //  * Every wait is bounded; a timeout records PKV_ERR_TIMEOUT, stops every role,
 //    lets copies and MMAs in flight finish and frees TMEM.
 //
@@ -324,116 +323,294 @@ __device__ __forceinline__ void store_out32(const PromptParams &p, size_t off, c
     }
 }
 
+// ------------------------------------------- rows with values not to be seen
+
+// Where V is not finite, the products above may be wrong: a masked weight 0
+// times an infinity or NaN of a later row is NaN, and with P in two parts so is
+// an infinity that the row does see times a part that is zero or negative.  The
+// output warps note the items with an output that is not finite; when the CTA's
+// last item is done, all its warps go through them again.
+//
+// A dim of a row is told from the first NaN and infinities of either sign that
+// V holds in it: those at or before the row decide the output (NaN; or the
+// infinity, as the weight of a finite score is positive), those after it must
+// not reach it.  Only where the row sees none and a later one spoilt the sum is
+// the sum computed again, with V's NaN and infinities as zeros and the item's
+// keys in steps of 64 through shared memory (mma.sync, a warp for 16 rows, P in
+// two parts).  So a row costs at most one such pass, and nothing but the look at
+// V where the NaN is its own.  An 8K prompt of 32/8 heads (371 us): V all NaN
+// 1.1 ms, its last token NaN 1.3 ms, every 10^4-th value NaN 3.1 ms; a chat batch
+// (500 us) at most 3.9 ms.
+constexpr int kRedoKeys = 64;
+
+template <int D> struct RedoSmem {
+    static constexpr int kLd = D + 8;           // rows of Q and K: 4 banks apart
+    static constexpr int kVLd = kRedoKeys + 8;  // and of V, which is transposed
+    int nan_at[D], pinf_at[D], ninf_at[D];      // first row of V with one
+    int last[2][D];                             // last one among a tile's products
+    int first;                                  // first token with an output to look at
+    int upto;                                   // last token to be computed again
+    int key_bad;                                // first row of K that is not finite
+    alignas(16) unsigned short q[2 * kM * kLd];
+    alignas(16) unsigned short k[kRedoKeys * kLd];
+    alignas(16) unsigned short v[D * kVLd];
+};
+
 // The e-th bf16 of two or four loaded as one word, as its bits.
 __device__ __forceinline__ uint32_t bf16_bits(uint32_t x, int e) { return e ? x >> 16 : x & 0xffffu; }
 __device__ __forceinline__ uint32_t bf16_bits(uint2 x, int e) { return bf16_bits(e & 2 ? x.y : x.x, e & 1); }
-
-// The rows of a warp that came out infinite or NaN (lane mask `rows`, lane i
-// owning row r0 + i of the tile).  A row is computed again over the keys it
-// sees if a V row after them, before `key_end`, the end of the keys the MMAs
-// multiplied, is not finite; with P in two parts also if a V row that it sees
-// holds an infinity (a part that is zero or negative turns it into NaN).  Keys
-// on the lanes for the scores, dims on the lanes for the sums.  Rare, so kept
-// out of line.
-template <int D, bool kSplit>
-__device__ __noinline__ void redo_rows(const PromptParams &p, unsigned rows, int r0, int tok, int row0,
-                                       int hkv, int key_end, int lane)
+__device__ __forceinline__ bool bf16_bad(uint32_t bits) { return (bits & 0x7fffu) >= 0x7f80u; }
+template <typename Dims, int kPer> __device__ __forceinline__ bool any_bad(Dims x)
 {
-    constexpr int kPer = D / 32;  // dims per lane
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+        bad = bad || bf16_bad(bf16_bits(x, e));
+    return bad;
+}
+
+template <bool kF32> __device__ __forceinline__ float load_out(const PromptParams &p, size_t at)
+{
+    if constexpr (kF32)
+        return static_cast<const float *>(p.out)[at];
+    else
+        return __bfloat162float(static_cast<const __nv_bfloat16 *>(p.out)[at]);
+}
+template <bool kF32> __device__ __forceinline__ void store_out(const PromptParams &p, size_t at, float y)
+{
+    if constexpr (kF32)
+        static_cast<float *>(p.out)[at] = y;
+    else
+        static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16(y);
+}
+
+// Rows [from, to) of the item's V (and K): first and last bad ones per dim.  A
+// lane has D / 32 dims, a warp eight rows at a time so that their loads overlap.
+template <int D>
+__device__ __noinline__ void redo_look(const PromptParams &p, RedoSmem<D> &sm, const PtItem &it, int from, int to,
+                                       int end0, int end1)
+{
+    constexpr int kPer = D / 32;
     using Dims = std::conditional_t<kPer == 4, uint2, uint32_t>;
-    const int G = p.group;
-    __syncwarp();  // the rows' first stores come before the ones below
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned short *kb = static_cast<const unsigned short *>(p.k) +
-                               static_cast<size_t>(row0) * p.k_stride + hkv * D;
+                               static_cast<size_t>(it.row0) * p.k_stride + it.hkv * D + lane * kPer;
     const unsigned short *vb = static_cast<const unsigned short *>(p.v) +
-                               static_cast<size_t>(row0) * p.v_stride + hkv * D;
-    const int first = tok + (r0 + __ffs(rows) - 1) / G;  // earliest token among the rows
-    int last_bad = -1, first_inf = INT_MAX;
-    // Eight keys at a time, so that their loads overlap.
-    for (int j0 = kSplit ? 0 : first + 1; j0 < key_end; j0 += 8) {
-        bool bad[8] = {}, inf[8] = {};
+                               static_cast<size_t>(it.row0) * p.v_stride + it.hkv * D + lane * kPer;
+    int first_nan[kPer], first_p[kPer], first_n[kPer], last0[kPer], last1[kPer], key_bad = INT_MAX;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        first_nan[e] = first_p[e] = first_n[e] = INT_MAX;
+        last0[e] = last1[e] = -1;
+    }
+    for (int j0 = from + 8 * warp; j0 < to; j0 += 8 * (kThreads / 32)) {
+        Dims kw[8], vw[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int j = min(j0 + i, key_end - 1);
-            const Dims w = *reinterpret_cast<const Dims *>(vb + j * p.v_stride + lane * kPer);
+            const int64_t j = min(j0 + i, to - 1);
+            kw[i] = *reinterpret_cast<const Dims *>(kb + j * p.k_stride);
+            vw[i] = *reinterpret_cast<const Dims *>(vb + j * p.v_stride);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = min(j0 + i, to - 1);
+            // A score that is not finite gives an infinite V row no positive weight.
+            const bool kbad = __any_sync(kFullMask, any_bad<Dims, kPer>(kw[i]));
+            if (kbad)
+                key_bad = min(key_bad, j);
+            if (!any_bad<Dims, kPer>(vw[i]))
+                continue;
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
-                bad[i] = bad[i] || (bf16_bits(w, e) & 0x7fffu) >= 0x7f80u;
-                inf[i] = inf[i] || (bf16_bits(w, e) & 0x7fffu) == 0x7f80u;
+                const uint32_t x = bf16_bits(vw[i], e);
+                if (!bf16_bad(x))
+                    continue;
+                if ((x & 0x7fffu) != 0x7f80u || kbad)
+                    first_nan[e] = min(first_nan[e], j);
+                else if (x & 0x8000u)
+                    first_n[e] = min(first_n[e], j);
+                else
+                    first_p[e] = min(first_p[e], j);
+                if (j < end0)
+                    last0[e] = max(last0[e], j);
+                if (j < end1)
+                    last1[e] = max(last1[e], j);
             }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int j = min(j0 + i, key_end - 1);
-            if (__any_sync(kFullMask, bad[i]))
-                last_bad = j;
-            if (kSplit && first_inf == INT_MAX && __any_sync(kFullMask, inf[i]))
-                first_inf = j;
         }
     }
-    for (; rows; rows &= rows - 1) {
-        const int r = r0 + __ffs(rows) - 1;
-        const int pos = tok + r / G;
-        if (pos >= last_bad && pos < first_inf)
-            continue;  // no product went wrong: the row stands
-        const size_t head = hkv * G + r % G;
-        const unsigned short *q = static_cast<const unsigned short *>(p.q) +
-                                  static_cast<size_t>(row0 + pos) * p.q_stride + head * D;
-        float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e)
-            o[e] = 0.f;
-        for (int j0 = 0; j0 <= pos; j0 += 32) {
-            const int j = j0 + lane;
-            float x = -INFINITY;
-            if (j <= pos) {
-                const uint4 *kr = reinterpret_cast<const uint4 *>(kb + j * p.k_stride);
-                const uint4 *qr = reinterpret_cast<const uint4 *>(q);
-                float a = 0.f;
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 kw = __ldg(kr + c), qw = __ldg(qr + c);
-                    const uint32_t kk[4] = {kw.x, kw.y, kw.z, kw.w}, qq[4] = {qw.x, qw.y, qw.z, qw.w};
+    for (int e = 0; e < kPer; ++e) {
+        const int d = lane * kPer + e;
+        atomicMin(&sm.nan_at[d], first_nan[e]);
+        atomicMin(&sm.pinf_at[d], first_p[e]);
+        atomicMin(&sm.ninf_at[d], first_n[e]);
+        atomicMax(&sm.last[0][d], last0[e]);
+        atomicMax(&sm.last[1][d], last1[e]);
+    }
+    if (lane == 0)
+        atomicMin(&sm.key_bad, key_bad);
+}
+
+// Dim d of a row at token `pos`: NaN or an infinity when the row sees one, else 0.
+template <int D> __device__ __forceinline__ float seen_value(const RedoSmem<D> &sm, int d, int pos)
+{
+    const bool up = sm.pinf_at[d] <= pos, down = sm.ninf_at[d] <= pos;
+    if (sm.nan_at[d] <= pos || (up && down))
+        return __int_as_float(0x7fffffff);
+    return up ? INFINITY : down ? -INFINITY : 0.f;
+}
+
+// The sums of the rows `rows` of this warp's 16 once more, and their outputs where they
+// were not finite.  All warps of the CTA call it.
+template <int D, bool kF32>
+__device__ __noinline__ void redo_rows(const PromptParams &p, RedoSmem<D> &sm, const PtItem &it, unsigned rows)
+{
+    using Sm = RedoSmem<D>;
+    constexpr int kLd = Sm::kLd, kVLd = Sm::kVLd;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, tq = lane & 3;  // fragment row, and pair of columns
+    const int G = p.group, R = kM / G;
+    const unsigned short *qb = static_cast<const unsigned short *>(p.q) + static_cast<size_t>(it.hkv) * G * D;
+    const unsigned short *kb = static_cast<const unsigned short *>(p.k) + it.hkv * D;
+    const unsigned short *vb = static_cast<const unsigned short *>(p.v) + it.hkv * D;
+    const int keys = min(sm.upto + 1, it.n);
+
+    for (int e = threadIdx.x; e < 2 * kM * (D / 8); e += kThreads) {
+        const int r = e / (D / 8), c = e % (D / 8), t = r / kM, rr = r % kM;
+        const int nt = t ? it.nt[1] : it.nt[0];
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (rr < nt * G)
+            x = *reinterpret_cast<const uint4 *>(
+                qb + (static_cast<size_t>(it.row0) + it.tok0 + t * R + rr / G) * p.q_stride + (rr % G) * D + 8 * c);
+        *reinterpret_cast<uint4 *>(sm.q + r * kLd + 8 * c) = x;
+    }
+
+    int pos[2];        // tokens of fragment rows g and g + 8, or -1
+    size_t orow[2];    // and their outputs
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        a = fmaf(bf16_lo(qq[e]), bf16_lo(kk[e]), fmaf(bf16_hi(qq[e]), bf16_hi(kk[e]), a));
+    for (int i = 0; i < 2; ++i) {
+        const int rr = 16 * (warp & 7) + g + 8 * i, t = warp >> 3;
+        const int tok = it.tok0 + t * R + rr / G;
+        pos[i] = rows >> (g + 8 * i) & 1u ? tok : -1;
+        orow[i] = (static_cast<size_t>(it.row0 + tok) * p.num_q_heads + it.hkv * G + rr % G) * D;
+    }
+    const int my_keys = rows ? __reduce_max_sync(kFullMask, max(pos[0], pos[1])) + 1 : 0;
+    const float c = p.negate ? -p.score_scale : p.score_scale;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[D / 8][4];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            o[n][e] = 0.f;
+
+    for (int k0 = 0; k0 < keys; k0 += kRedoKeys) {
+        __syncthreads();  // the keys before these are used
+        for (int e = threadIdx.x; e < kRedoKeys * (D / 8); e += kThreads) {
+            const int r = e / (D / 8), d = 8 * (e % (D / 8));
+            uint4 x = make_uint4(0, 0, 0, 0), y = x;
+            if (k0 + r < keys) {
+                const int64_t row = static_cast<int64_t>(it.row0) + k0 + r;
+                x = *reinterpret_cast<const uint4 *>(kb + row * p.k_stride + d);
+                y = *reinterpret_cast<const uint4 *>(vb + row * p.v_stride + d);
+            }
+            *reinterpret_cast<uint4 *>(sm.k + r * kLd + d) = x;
+            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t b = bf16_bits(w[i / 2], i & 1);
+                sm.v[(d + i) * kVLd + r] = static_cast<unsigned short>(bf16_bad(b) ? 0u : b);
+            }
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int h = k0; h < min(k0 + kRedoKeys, my_keys); h += 32) {
+            const int at = h - k0;
+            float s[4][4] = {};
+#pragma unroll 2
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const unsigned short *qr = sm.q + (16 * warp + g) * kLd + 16 * ks + 2 * tq;
+                const uint32_t a[4] = {*reinterpret_cast<const uint32_t *>(qr),
+                                       *reinterpret_cast<const uint32_t *>(qr + 8 * kLd),
+                                       *reinterpret_cast<const uint32_t *>(qr + 8),
+                                       *reinterpret_cast<const uint32_t *>(qr + 8 * kLd + 8)};
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const unsigned short *kr = sm.k + (at + 8 * n + g) * kLd + 16 * ks + 2 * tq;
+                    mma_bf16(s[n], a, *reinterpret_cast<const uint32_t *>(kr),
+                             *reinterpret_cast<const uint32_t *>(kr + 8));
                 }
-                x = a * (p.negate ? -p.score_scale : p.score_scale);
             }
-            float mx = x;
+            float alpha[2];
 #pragma unroll
-            for (int w = 16; w >= 1; w >>= 1)
-                mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, w));
-            const float mn = fmaxf(m, mx);
-            const float off = mn == -INFINITY ? 0.f : mn;
-            const float alpha = MmaSoftmax::ex2(m - off);
-            const float wgt = j <= pos ? MmaSoftmax::ex2(x - off) : 0.f;
-            m = mn;
-            l = l * alpha + wgt;
+            for (int i = 0; i < 2; ++i) {
+                float mx = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < kPer; ++e)
-                o[e] *= alpha;
-            const int cnt = min(32, pos + 1 - j0);
-#pragma unroll 8
-            for (int i = 0; i < cnt; ++i) {
-                const float w = __shfl_sync(kFullMask, wgt, i);
-                const Dims vr = *reinterpret_cast<const Dims *>(vb + (j0 + i) * p.v_stride + lane * kPer);
+                for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int e = 0; e < kPer; ++e)
-                    o[e] = fmaf(w, __uint_as_float(bf16_bits(vr, e) << 16), o[e]);
+                    for (int e = 0; e < 2; ++e) {
+                        float &x = s[n][2 * i + e];
+                        x = h + 8 * n + 2 * tq + e <= pos[i] ? x * c : -INFINITY;
+                        mx = fmaxf(mx, x);
+                    }
+                mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 2));
+                mx = fmaxf(mx, m[i]);
+                // Nothing but -inf so far: any finite offset gives weights 0.
+                const float off = mx == -INFINITY ? 0.f : mx;
+                alpha[i] = MmaSoftmax::ex2(m[i] - off);
+                m[i] = mx;
+                l[i] *= alpha[i];
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float &x = s[n][2 * i + e];
+                        x = MmaSoftmax::ex2(x - off);
+                        l[i] += x;
+                    }
+            }
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[n][e] *= alpha[e / 2];
+#pragma unroll
+            for (int kc = 0; kc < 2; ++kc) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // rows g, g + 8 of the chunk's keys, then of its last eight
+                    const float x = s[2 * kc + i / 2][2 * (i & 1)], y = s[2 * kc + i / 2][2 * (i & 1) + 1];
+                    hi[i] = pack_bf16(x, y);
+                    lo[i] = pack_bf16(x - bf16_lo(hi[i]), y - bf16_hi(hi[i]));
+                }
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    const unsigned short *vr = sm.v + (8 * n + g) * kVLd + at + 16 * kc + 2 * tq;
+                    const uint32_t b0 = *reinterpret_cast<const uint32_t *>(vr),
+                                   b1 = *reinterpret_cast<const uint32_t *>(vr + 8);
+                    mma_bf16(o[n], hi, b0, b1);
+                    mma_bf16(o[n], lo, b0, b1);
+                }
             }
         }
+    }
 #pragma unroll
-        for (int w = 16; w >= 1; w >>= 1)
-            l += __shfl_xor_sync(kFullMask, l, w);
-        const size_t off = (static_cast<size_t>(row0 + pos) * p.num_q_heads + head) * D + lane * kPer;
+    for (int i = 0; i < 2; ++i) {
+        float sum = l[i];
+        sum += __shfl_xor_sync(kFullMask, sum, 1);
+        sum += __shfl_xor_sync(kFullMask, sum, 2);
+        if (pos[i] < 0)
+            continue;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const float y = o[e] / l;
-            if constexpr (kSplit)
-                static_cast<float *>(p.out)[off + e] = y;
-            else
-                static_cast<__nv_bfloat16 *>(p.out)[off + e] = __float2bfloat16(y);
-        }
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int d = 8 * n + 2 * tq + e;
+                const float y = load_out<kF32>(p, orow[i] + d);
+                if (!(y * 0.f == 0.f))  // the others stand
+                    store_out<kF32>(p, orow[i] + d, seen_value(sm, d, pos[i]) + o[n][2 * i + e] / sum);
+            }
     }
 }
 
@@ -444,14 +621,18 @@ __device__ __forceinline__ unsigned item_number(unsigned k)
     return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
-// The items first .. last of this CTA once more: a warp looks at the rows that
-// it has stored (lane i at row r0 + i) and hands those that are not finite to
-// redo_rows.
+// The items first .. last of this CTA once more, by all its warps: warp w has rows
+// 16 w .. 16 w + 15 of an item's 256.
 template <int D, bool kSplit>
-__device__ __noinline__ void redo_items(const PromptParams &p, unsigned first, unsigned last, int r0, int lane)
+__device__ __noinline__ void redo_items(const PromptParams &p, unsigned char *smem, unsigned first, unsigned last)
 {
+    constexpr int kPer = D / 32;
+    using Dims = std::conditional_t<kPer == 4, uint2, uint32_t>;
+    RedoSmem<D> &sm = *reinterpret_cast<RedoSmem<D> *>(smem);
+    static_assert(sizeof(RedoSmem<D>) <= PtGeom<D>::kSmem - 1024, "fits where the ring was");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = p.group, R = kM / G;
-    const int r = r0 + lane;
+    const int t = warp >> 3;
     PromptScan scan;
     scan.init(p, 2 * R, lane, false);
     for (unsigned k = first; k <= last; ++k) {
@@ -459,27 +640,100 @@ __device__ __noinline__ void redo_items(const PromptParams &p, unsigned first, u
         const int w[5] = {found.s, found.hkv, found.row0, found.n, found.index * 2 * R};
         PtItem it;
         it.fill(w, R);
-        for (int t = 0; t < 2; ++t) {
-            const int nt = it.nt[t], nb = it.nb[t], tok = it.tok0 + t * R;
-            bool bad = false;
-            if (r < nt * G) {
-                const size_t off = (static_cast<size_t>(it.row0 + tok + r / G) * p.num_q_heads +
-                                    it.hkv * G + r % G) * D;
-                for (int e = 0; e < D; ++e) {
-                    float y;
-                    if constexpr (kSplit)
-                        y = static_cast<const float *>(p.out)[off + e];
-                    else
-                        y = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.out)[off + e]);
-                    bad = bad || !(y * 0.f == 0.f);
-                }
-            }
-            const unsigned rows = __ballot_sync(kFullMask, bad);
-            if (rows)
-                redo_rows<D, kSplit>(p, rows, r0, tok, it.row0, it.hkv,
-                                     min((nb - 1) * kKeys + block_cols(nb, it.end[t], nb - 1),
-                                         max(it.end[0], it.end[1])), lane);
+        // Keys that the products of the tiles have gone through.
+        const int item_end = max(it.end[0], it.end[1]);
+        int key_end[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            key_end[x] = it.nb[x] == 0 ? 0
+                                       : min((it.nb[x] - 1) * kKeys + block_cols(it.nb[x], it.end[x], it.nb[x] - 1),
+                                             item_end);
+        const int tok = it.tok0 + t * R, nt = t ? it.nt[1] : it.nt[0];
+        __syncthreads();  // the item before has left shared memory
+        if (threadIdx.x < D) {
+            sm.nan_at[threadIdx.x] = sm.pinf_at[threadIdx.x] = sm.ninf_at[threadIdx.x] = INT_MAX;
+            sm.last[0][threadIdx.x] = sm.last[1][threadIdx.x] = -1;
         }
+        if (threadIdx.x == 0) {
+            sm.first = sm.key_bad = INT_MAX;
+            sm.upto = -1;
+        }
+        __syncthreads();
+        // Outputs of this lane's dims that are not finite, kPer bits a row.
+        uint64_t bad = 0;
+        unsigned rows = 0;
+        for (int i = 0; i < 16; ++i) {
+            const int r = 16 * (warp & 7) + i;
+            if (r >= nt * G)
+                break;
+            const size_t at = (static_cast<size_t>(it.row0 + tok + r / G) * p.num_q_heads + it.hkv * G + r % G) * D;
+            uint64_t b = 0;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const float y = load_out<kSplit>(p, at + lane * kPer + e);
+                b |= static_cast<uint64_t>(!(y * 0.f == 0.f)) << e;
+            }
+            bad |= b << (kPer * i);
+            rows |= __any_sync(kFullMask, b != 0) ? 1u << i : 0u;
+        }
+        if (rows && lane == 0)
+            atomicMin(&sm.first, tok + (16 * (warp & 7) + __ffs(rows) - 1) / G);
+        if (!__syncthreads_or(rows != 0))
+            continue;
+        // What they must not see first: mostly nothing, and the outputs stand.
+        const int from = kSplit ? 0 : sm.first + 1;
+        redo_look<D>(p, sm, it, from, max(key_end[0], key_end[1]), key_end[0], key_end[1]);
+        __syncthreads();
+        if (!kSplit) {
+            bool hidden = false;
+            for (int i = 0; i < 16; ++i)
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    hidden = hidden || ((bad >> (kPer * i + e) & 1) &&
+                                        sm.last[t][lane * kPer + e] > tok + (16 * (warp & 7) + i) / G);
+            if (!__syncthreads_or(hidden))
+                continue;
+            redo_look<D>(p, sm, it, 0, from, key_end[0], key_end[1]);
+            __syncthreads();
+        }
+        unsigned again = 0;  // rows whose sums are computed again
+        for (unsigned left = rows; left; left &= left - 1) {
+            const int i = __ffs(left) - 1, r = 16 * (warp & 7) + i, pos = tok + r / G;
+            const size_t head = it.hkv * G + r % G, row = it.row0 + pos;
+            float y[kPer];
+            int write = 0;  // dims of this lane to be written
+            bool sum = false;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const int d = lane * kPer + e;
+                const bool here = bad >> (kPer * i + e) & 1, hidden = sm.last[t][d] > pos;
+                y[e] = seen_value(sm, d, pos);
+                sum = sum || (here && hidden && y[e] == 0.f);
+                if (here && (kSplit || hidden) && fabsf(y[e]) == INFINITY)
+                    write |= 1 << e;
+            }
+            sum = __any_sync(kFullMask, sum);
+            if (!sum && !__any_sync(kFullMask, write != 0))
+                continue;
+            if (!sum) {
+                // An infinity has a positive weight if the scores are finite: else look.
+                const Dims qw = *reinterpret_cast<const Dims *>(static_cast<const unsigned short *>(p.q) +
+                                                                row * p.q_stride + head * D + lane * kPer);
+                sum = sm.key_bad <= pos || __any_sync(kFullMask, any_bad<Dims, kPer>(qw));
+            }
+            if (sum) {
+                again |= 1u << i;
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+                if (write >> e & 1)
+                    store_out<kSplit>(p, (row * p.num_q_heads + head) * D + lane * kPer + e, y[e]);
+        }
+        if (again && lane == 0)
+            atomicMax(&sm.upto, tok + (16 * (warp & 7) + 31 - __clz(again)) / G);
+        if (__syncthreads_or(again != 0))
+            redo_rows<D, kSplit>(p, sm, it, again);
     }
 }
 
@@ -498,6 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ float s_sum[2][kM];  // the rows' sums of weights, for the output warps
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
+    __shared__ unsigned s_redo[2];  // first and last item with an output that is not finite
     volatile int *abort = &s_abort;
 
     const int warp = threadIdx.x >> 5;
@@ -530,6 +785,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&drain, 1);
         s_abort = 0;
+        s_redo[0] = ~0u;
+        s_redo[1] = 0;
         fence_mbar_init();
     }
     if (warp == kProducerWarp && lane < 3) {
@@ -1043,7 +1300,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         uint32_t par = 0;  // bit t: parity of the tile's barriers
-        unsigned redo0 = ~0u, redo1 = 0;  // first and last item with a row that is not finite
         bool failed = false;
         for (unsigned k = 0; !failed; ++k) {
             const int slot = k % kQueue;
@@ -1095,14 +1351,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (live)
                         store_out32<kSplit>(p, orow + c0, ov, wide);
                 }
-                if (__any_sync(kFullMask, live && bad != 0.f)) {
-                    redo0 = min(redo0, k);
-                    redo1 = k;
+                if (live && bad != 0.f) {
+                    atomicMin(&s_redo[0], k);
+                    atomicMax(&s_redo[1], k);
                 }
             }
         }
-        if (!failed && redo0 <= redo1)
-            redo_items<D, kSplit>(p, redo0, redo1, 32 * (warp & 3), lane);
         if (failed && lane == 0) {
             set_status(p.status, PKV_ERR_TIMEOUT);
             *abort = 1;
@@ -1117,6 +1371,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                      : "memory");
     }
+    // Every copy has landed and every MMA is done: shared memory is free.
+    if (s_redo[0] <= s_redo[1] && !s_abort)
+        redo_items<D, kSplit>(p, smem, s_redo[0], s_redo[1]);
 }
 
 // ------------------------------------------------------------------ host

@@ -403,3 +403,120 @@ def test_a_late_watcher_of_the_loads(lens, D):
     pkv.prompt_attn(q, k, v, starts(lens), 0.1, a)
     pkv.prompt_attn(q, k, v, starts(lens), 0.1, b, status=status, flags=pkv.FLAG_TEST_SLOW_GATE)
     assert int(status) == 0 and torch.equal(a, b) and bool((a != 0).any())
+
+
+def value_reference(q, k, v, lens, scale):
+    """reference() with V's NaN and infinities as the values they are: a row that sees one in a
+    dim gives it (NaN for both signs), whatever its weight; the others sum what is finite."""
+    ref, mass, most = reference(q, k, torch.where(torch.isfinite(v), v, torch.zeros_like(v)), lens, scale)
+    G, at = q.shape[1] // k.shape[1], 0
+    for n in lens:
+        x = v[at:at + n].float().repeat_interleave(G, 1)
+        nan, up, down = (torch.cumsum(b, 0) > 0 for b in (torch.isnan(x), x == math.inf, x == -math.inf))
+        r = ref[at:at + n]
+        r[up], r[down], r[nan | (up & down)] = math.inf, -math.inf, math.nan
+        at += n
+    return ref, mass, most
+
+
+def check_values(q, k, v, lens, scale, out_dtype):
+    out = torch.zeros(q.shape, dtype=out_dtype, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkv.prompt_attn(q, k, v, starts(lens), scale, out, status=status)
+    assert int(status) == 0
+    ref, mass, most = value_reference(q, k, v, lens, scale)
+    n = sum(lens)
+    o, ref = out[:n].double(), ref[:n]
+    assert torch.equal(torch.isnan(o), torch.isnan(ref))
+    inf = torch.isinf(ref)
+    assert torch.equal(o[inf], ref[inf]) and not torch.isinf(o[~inf]).any()
+    fine = torch.isfinite(ref)
+    tol = tolerance(torch.where(fine, ref, 0), mass[:n], most, lens, q.shape[2], scale, q.dtype, out_dtype)
+    off = (o - ref).abs()
+    assert bool((off[fine] <= tol[fine]).all()), f"worst {float((off[fine] / tol[fine]).max()):.3g}"
+    return out
+
+
+@pytest.mark.parametrize("dtype,out_dtype", TYPES)
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 64), (4, 1, 128), (6, 2, 128), (16, 1, 64)])
+@pytest.mark.parametrize("what", ["all", "last", "tokens", "one_inf", "sparse", "both_signs", "dims"])
+def test_values_that_are_not_finite(what, Hq, Hkv, D, dtype, out_dtype):
+    lens = [70, 700, 1, 0, 257, 300]
+    q, k, v = make(lens, Hq, Hkv, D, dtype, 30, fused=False, tail=9)
+    r = np.random.RandomState(31)
+    T = v.shape[0]
+    inf, nan = math.inf, math.nan
+    if what == "all":
+        v.fill_(nan)
+    elif what == "last":
+        for e in np.cumsum(lens)[:-1]:
+            v[max(0, int(e) - 1)] = nan
+    elif what == "tokens":
+        for t, x in zip(r.choice(T, 12, replace=False), [nan, inf, -inf] * 4):
+            v[int(t)] = x
+    elif what == "one_inf":
+        v[72, 0, 5], v[300, Hkv - 1, 7], v[1030, 0, 0] = inf, -inf, inf
+    elif what == "sparse":
+        u = torch.from_numpy(r.rand(*v.shape)).to(DEV)
+        v[u < 1e-3] = nan
+        v[(u > 0.5) & (u < 0.5005)] = inf
+        v[u > 0.9995] = -inf
+    elif what == "both_signs":
+        v[100:130, :, ::3] = inf
+        v[400:410, :, ::2] = -inf
+    elif what == "dims":
+        for d in range(D):                         # each dim's first one some rows later
+            v[70 + 11 * d % 690, :, d] = [nan, inf, -inf][d % 3]
+    check_values(q, k, v, lens, 1 / math.sqrt(D), out_dtype)
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+def test_values_and_scores_that_are_not_finite(out_dtype):
+    # An infinite V row whose own score is -inf has weight 0: NaN, as in the formula.
+    q, k, v = make([400], 2, 1, 64, BF16, 32, fused=False)
+    q.copy_(q.abs() + 0.1)
+    k[50, 0, 3], v[50, 0, 9] = -math.inf, math.inf
+    v[130, 0, 20] = math.nan
+    out = torch.zeros(q.shape, dtype=out_dtype, device=DEV)
+    pkv.prompt_attn(q, k, v, starts([400]), 0.1, out)
+    o = out.float()
+    dims = torch.arange(64, device=DEV)
+    assert torch.isfinite(o[:50]).all()
+    assert torch.isnan(o[50:, :, 9]).all() and torch.isnan(o[130:, :, 20]).all()
+    assert torch.isfinite(o[50:130][..., dims != 9]).all()
+    assert torch.isfinite(o[130:][..., (dims != 9) & (dims != 20)]).all()
+    # A score that is NaN gives a NaN row, whatever V holds after it.
+    k[60, 0, 0] = math.nan
+    pkv.prompt_attn(q, k, v, starts([400]), 0.1, out)
+    o = out.float()
+    assert torch.isnan(o[60:]).all() and torch.isfinite(o[:50]).all()
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("what", ["all", "last", "one_inf", "sparse"])
+def test_what_values_that_are_not_finite_cost(what, out_dtype):
+    # At most one slower pass more, 8 times the time in all where it was measured.
+    q, k, v = make([8192], 32, 8, 128, BF16, 33, fused=False)
+    bad = v.clone()
+    if what == "all":
+        bad.fill_(math.nan)
+    elif what == "last":
+        bad[-1] = math.nan
+    elif what == "one_inf":
+        bad[3, :, 5] = math.inf
+    else:
+        bad[torch.rand(v.shape, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1)) < 1e-4] = math.nan
+    out = torch.zeros(q.shape, dtype=out_dtype, device=DEV)
+
+    def ms(x):
+        best = math.inf
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            pkv.prompt_attn(q, k, x, starts([8192]), 0.1, out)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    assert ms(bad) <= 20 * ms(v)
