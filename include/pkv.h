@@ -478,6 +478,8 @@ pkv_status pkv_copy_blocks(void *k_cache, void *v_cache, pkv_dtype kv_dtype, int
  *   q_start      int32 [num_seqs + 1] (device), non-decreasing, within
  *                [0, num_tokens].  Rows of out that belong to no sequence are
  *                not written.
+ *                num_seqs up to 2^20 (else PKV_ERR_UNSUPPORTED); many empty ones
+ *                cost time (2^17: 10 ms).
  *   head_dim     64 or 128.
  *   max_q_len    host bound on every sequence's rows.
  *   scale        finite, any sign.

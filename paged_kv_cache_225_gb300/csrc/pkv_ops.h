@@ -26,6 +26,11 @@ struct PromptParams {
     int slow_gate;           // test hook: the warp that watches the loads looks 20 us late
 };
 
+// Every look-up of an item may walk all row starts once per cost class (2^20 of
+// them, most empty: 10 ms a class, and a 32K prompt has some 20 classes), while
+// the bf16 kernel's other roles wait for at most a second.
+constexpr int kPromptMaxSeqs = 1 << 20;
+
 // One scheduling step of a page pool kept in device memory.
 struct TablesParams {
     const int32_t *drop_lens;  // [S] or null

@@ -38,7 +38,7 @@ pkv_status pkv_prompt_attn(const void *q, const void *k, const void *v, pkv_dtyp
         return PKV_ERR_UNSUPPORTED;
     if (head_dim != 64 && head_dim != 128)
         return PKV_ERR_UNSUPPORTED;
-    if (num_q_heads / num_kv_heads > 16)
+    if (num_q_heads / num_kv_heads > 16 || num_seqs > kPromptMaxSeqs)
         return PKV_ERR_UNSUPPORTED;
     if (!std::isfinite(scale) || (flags & ~(PKV_FLAG_TEST_DROP_FIRST_COPY | PKV_FLAG_TEST_SLOW_GATE)) != 0 ||
         (flags != 0 && dtype != PKV_BF16))

@@ -520,3 +520,19 @@ def test_what_values_that_are_not_finite_cost(what, out_dtype):
         return best
 
     assert ms(bad) <= 20 * ms(v)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_as_many_sequences_as_there_may_be(dtype):
+    # 2^20 of them, all but three empty, the longest with many blocks: no wait runs out.
+    lens = np.zeros(1 << 20, np.int64)
+    lens[[5, 1 << 19, (1 << 20) - 1]] = 3000, 17, 40
+    q, k, v = make([3000, 17, 40], 4, 4, 64, dtype, 40)
+    out, want = torch.zeros(q.shape, dtype=dtype, device=DEV), torch.zeros(q.shape, dtype=dtype, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkv.prompt_attn(q, k, v, starts(lens), 0.125, out, status=status)
+    pkv.prompt_attn(q, k, v, starts([3000, 17, 40]), 0.125, want)
+    assert int(status) == 0 and torch.equal(out, want)
+    with pytest.raises(pkv.PkvError) as e:
+        pkv.prompt_attn(q, k, v, torch.zeros((1 << 20) + 2, dtype=torch.int32, device=DEV), 0.125, out)
+    assert e.value.code == 2

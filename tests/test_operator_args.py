@@ -132,3 +132,10 @@ def test_tensors_that_do_not_fit():
 def test_slow_gate_flag_is_for_bf16():
     assert prompt(flags=pkv.FLAG_TEST_SLOW_GATE, dtype=pkv.F32) == INVALID
     assert prompt(flags=pkv.FLAG_TEST_SLOW_GATE, T=0, q=None) == OK
+
+
+def test_number_of_sequences():
+    # More would let the bf16 kernel's waits run out while items are looked up.
+    for dtype, qs, kv in ((pkv.BF16, 32 * 128, 8 * 128), (pkv.F32, 32 * 128, 8 * 128)):
+        assert prompt(S=(1 << 20) + 1, dtype=dtype, qs=qs, ks=kv, vs=kv) == UNSUPPORTED
+        assert prompt(S=1 << 20, dtype=dtype, qs=qs, ks=kv, vs=kv, T=0, q=None) == OK
