@@ -869,14 +869,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 set_status(p.status, PKV_ERR_TIMEOUT);
                 *abort = 1;
             }
-            if (*abort) {
-                // Let every copy still in flight land before the CTA exits.
-                for (uint32_t c = kv > NS ? kv - NS : 0; c < kv; ++c)
-                    mbar_wait_bounded(&full[c % NS], (c / NS) & 1, kWaitLimitNs);
-                for (int t = 0; t < 2; ++t)
-                    if (qn[t] > 0)
-                        mbar_wait_bounded(&q_full[t], (qn[t] - 1) & 1, kWaitLimitNs);
-            }
+            // Every copy still in flight lands before the CTA exits, also when
+            // another role gives up after the last one was issued.
+            for (uint32_t c = kv > NS ? kv - NS : 0; c < kv; ++c)
+                mbar_wait_bounded(&full[c % NS], (c / NS) & 1, kWaitLimitNs);
+            for (int t = 0; t < 2; ++t)
+                if (qn[t] > 0)
+                    mbar_wait_bounded(&q_full[t], (qn[t] - 1) & 1, kWaitLimitNs);
         }
         __syncwarp();
     } else if (warp == kGateWarp) {

@@ -536,3 +536,15 @@ def test_as_many_sequences_as_there_may_be(dtype):
     with pytest.raises(pkv.PkvError) as e:
         pkv.prompt_attn(q, k, v, torch.zeros((1 << 20) + 2, dtype=torch.int32, device=DEV), 0.125, out)
     assert e.value.code == 2
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[1], [40], [200], [3000, 5]])
+def test_timeout_with_copies_issued_and_in_flight(lens, D):
+    # The copies are all issued (short prompts), or wait for the ring, when the MMA thread gives up.
+    q, k, v = make(lens, 8, 2, D, BF16, 41)
+    out = torch.zeros(q.shape, dtype=BF16, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkv.prompt_attn(q, k, v, starts(lens), 0.1, out, status=status, flags=pkv.FLAG_TEST_DROP_FIRST_COPY)
+    assert int(status) == 5
+    check(q, k, v, lens, 0.1)
