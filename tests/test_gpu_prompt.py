@@ -548,3 +548,27 @@ def test_timeout_with_copies_issued_and_in_flight(lens, D):
     pkv.prompt_attn(q, k, v, starts(lens), 0.1, out, status=status, flags=pkv.FLAG_TEST_DROP_FIRST_COPY)
     assert int(status) == 5
     check(q, k, v, lens, 0.1)
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 0.7])
+@pytest.mark.parametrize("Hq,Hkv", [(7, 1), (10, 2), (13, 1)])
+def test_values_that_are_not_finite_in_views(Hq, Hkv, scale, out_dtype):
+    # Rows of a fused projection, head groups that leave rows of a tile empty, scales of either sign; twice
+    # in a graph, then with other values in the same buffers.
+    lens = [300, 33, 0, 150]
+    q, k, v = make(lens, Hq, Hkv, 128, BF16, 34)
+    clean = v.clone()
+    out = torch.zeros(q.shape, dtype=out_dtype, device=DEV)
+    qs = starts(lens)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkv.prompt_attn(q, k, v, qs, scale, out)
+    for rows in ((299, 310, 480), (100, 301), ()):
+        v.copy_(clean)
+        for i, t in enumerate(rows):
+            v[t, :, i::3] = [math.nan, math.inf, -math.inf][i % 3]
+        want = check_values(q, k, v, lens, scale, out_dtype)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[:sum(lens)].nan_to_num(nan=7.0), want[:sum(lens)].nan_to_num(nan=7.0))
