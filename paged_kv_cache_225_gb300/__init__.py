@@ -713,8 +713,12 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torc
     multiple of 16 bytes apart, so views of a fused QKV projection are fine;
     q_start int32 [S+1]: sequence s is rows q_start[s]..q_start[s+1]-1, row i of
     it attends its rows 0..i; out [T, Hq, D] f32/bf16.  ``max_q_len`` bounds the
-    sequences (default T).  ``status`` (int32 [1], optional) records device-side
-    errors.  Returns ``out``.
+    sequences (default T): a longer one, or one outside the rows, is not computed
+    and its rows of ``out`` stay as they were.  ``status`` (int32 [1], optional)
+    records that and other device-side errors; without it nothing tells.  bf16
+    inputs with a bf16 ``out`` round the softmax weights to bf16, where
+    ``paged_attn_prefill`` carries 16 bits; an f32 ``out`` carries them here too.
+    Returns ``out``.
     """
     index = _cuda_index(q, "q")
     dtype = q.dtype

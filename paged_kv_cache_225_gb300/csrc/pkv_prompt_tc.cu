@@ -37,15 +37,24 @@
 //    lets copies and MMAs in flight finish and frees TMEM.
 //
 // What bounds it.  Long prompts: the tensor cores (a 32K prompt of 32 heads of
-// 128 over 8 KV heads: 5.5 ms, 1.6 PFLOP/s, 94% of what a cuBLAS product
-// sustains on the same part).  A block takes them 2 x 1024 cycles; a tile's
+// 128 over 8 KV heads: 5.7 to 5.85 ms, 1.5 PFLOP/s, 90% of what a cuBLAS product
+// sustains on the same part; a burst takes 5.5 ms).  A block takes them 2 x 1024 cycles; a tile's
 // softmax of about 1200 cycles hides behind the other tile's products.  The
 // queue of the tensor cores holds about three MMAs, so the issuing thread may
 // spend only some 200 cycles between two groups: hence one barrier per group
 // (the gate), one commit per step for the ring, and a loop of its own for
-// whole blocks.  Short prompts (128 of 256 to 512 tokens, 64 heads: 498 us,
+// whole blocks.  Short prompts (128 of 256 to 512 tokens, 64 heads: 500 us,
 // 3.6 TB/s): the chain load - S - softmax - P V - store of items two blocks long,
-// and the issuing thread's general steps.
+// and the issuing thread's general steps.  With heads of 64 (37 prompts of up to
+// 1000 tokens, 24/2 heads: 96 us): the same steps, some 4500 cycles each for 1000
+// of products, and scores that wait for P V because P lies over them.
+//
+// Bits of P.  A bf16 output takes its weights rounded to bf16 (2^-8 of each at
+// most), an f32 output in two bf16 parts (2^-16), which is twice the products of
+// P V.  Against 64 bits the bf16 outputs are then 0.0017 to 0.0020 off (2-norm),
+// of which 0.0014 to 0.0016 is the rounding of the output itself.  One part / two,
+// us: chat batch 499 / 676, 16 prompts of 512 to 4096 tokens 530 / 739, 32K prompt
+// 5713 / 7997, heads of 64 above 104 / 131.
 //
 // Measured and not taken (32K prompt / chat batch, 5.7 ms / 521 us then): an issuing thread
 // per tile 8.1 ms / 501 us (both tiles' products run interleaved, then both
