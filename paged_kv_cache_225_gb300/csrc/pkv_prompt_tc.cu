@@ -1308,6 +1308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         uint32_t par = 0;  // bit t: parity of the tile's barriers
+        unsigned redo0 = ~0u, redo1 = 0;  // first and last item with a row that is not finite
         bool failed = false;
         for (unsigned k = 0; !failed; ++k) {
             const int slot = k % kQueue;
@@ -1359,11 +1360,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (live)
                         store_out32<kSplit>(p, orow + c0, ov, wide);
                 }
-                if (live && bad != 0.f) {
-                    atomicMin(&s_redo[0], k);
-                    atomicMax(&s_redo[1], k);
+                if (__any_sync(kFullMask, live && bad != 0.f)) {
+                    redo0 = min(redo0, k);
+                    redo1 = k;
                 }
             }
+        }
+        if (lane == 0 && redo0 <= redo1) {
+            atomicMin(&s_redo[0], redo0);
+            atomicMax(&s_redo[1], redo1);
         }
         if (failed && lane == 0) {
             set_status(p.status, PKV_ERR_TIMEOUT);
