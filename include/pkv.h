@@ -30,6 +30,11 @@
  *  - pkv_prompt_attn: causal attention over whole prompts, straight from
  *    packed q, k and v rows (no cache read).
  *
+ *  - pkv_rope_append: the cache write with the rotation of queries and keys by
+ *    their positions on the way; pkv_latent_append, pkv_latent_attn_decode and
+ *    pkv_latent_prompt_attn: the same write, the decode and the whole-prompt
+ *    attention of a cache with one latent row per token for all heads.
+ *
  *  - pkv_tables_step and pkv_tables_fork: the page pool's bookkeeping on the
  *    GPU, for steps without a host round trip.
  *
@@ -109,6 +114,9 @@ typedef enum {
 /* Test hook of pkv_prompt_attn (BF16): the warp that watches the copies for the
  * MMA thread looks at each one 20 us late.  The results are the same. */
 #define PKV_FLAG_TEST_SLOW_GATE 0x400
+/* pkv_rope_append, pkv_latent_append: the rotated pairs are neighbouring dims
+ * (2i, 2i + 1) instead of halves (i, i + rot_dim / 2). */
+#define PKV_FLAG_ROPE_INTERLEAVED 0x800
 
 /*
  * Workspace bytes pkv_paged_attn_decode needs for these sizes (always >= 256:
@@ -572,6 +580,127 @@ pkv_status pkv_tables_fork(const int32_t *pairs, int num_pairs, int32_t *seq_len
                            int32_t *block_tables, int32_t *ref_counts, int num_seqs,
                            int max_blocks_per_seq, int block_size, int num_blocks,
                            int32_t *status, void *stream);
+
+/*
+ * The cache write of pkv_reshape_and_cache with the rotation of rotary positions
+ * on the way ("Inference optimization" lesson, section "Caches de KV"), for the
+ * queries too.  For every token i with slot_mapping[i] >= 0 and row
+ * (cos, sin) = table[positions[i]], each pair (a, b) of the first rot_dim dims of
+ * a head of q and k becomes (a cos - b sin, b cos + a sin); dims from rot_dim on
+ * stay as they are.  q's heads go to q_out, k's and v's (not rotated) to the
+ * token's slot, converted as by pkv_reshape_and_cache.  The arithmetic is f32,
+ * each product and sum rounded on its own, and one rounding to the type written.
+ *
+ *   q, q_out      [num_tokens, num_q_heads, head_dim] of in_dtype (F32 or BF16),
+ *                 row t at q + t * q_stride elements, heads dense.  q_out may be q
+ *                 itself (same pointer, same stride); it may not overlap the
+ *                 inputs otherwise.  num_q_heads 0: no queries (both NULL).
+ *   k, v          [num_tokens, num_kv_heads, head_dim] of in_dtype, rows likewise.
+ *                 Strides are at least the row and a multiple of 16 bytes: views of
+ *                 one fused projection are fine.
+ *   positions     int32 [num_tokens].
+ *   table         float32 [max_positions, rot_dim]: rot_dim / 2 cosines, then as
+ *                 many sines, of each position's angles.
+ *   rot_dim       a multiple of 16, at most head_dim (64 or 128).
+ *   slot_mapping  as for pkv_reshape_and_cache.  A token with a negative slot is
+ *                 padding: nothing of it is read or written, its row of q_out stays.
+ *   caches, scales, kv_dtype   as for pkv_reshape_and_cache (scales finite and not 0).
+ *   flags         0 (pairs (i, i + rot_dim / 2)) or PKV_FLAG_ROPE_INTERLEAVED.
+ *   status        optional device int32, as for pkv_reshape_and_cache: a token whose
+ *                 slot or position lies outside the pool or the table is reported as
+ *                 PKV_ERR_OUT_OF_RANGE and skipped like padding.
+ */
+pkv_status pkv_rope_append(const void *q, const void *k, const void *v, pkv_dtype in_dtype, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, const int32_t *positions, const float *table,
+                           int rot_dim, int max_positions, const int64_t *slot_mapping, int num_tokens,
+                           int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                           void *q_out, int64_t q_out_stride, void *k_cache, void *v_cache, pkv_dtype kv_dtype,
+                           float k_scale, float v_scale, int flags, int32_t *status, void *stream);
+
+/*
+ * Latent attention: all heads share one row per token, a latent vector of
+ * latent_dim numbers and a rotated key of rope_dim numbers.  The cache is
+ * [num_blocks, 16, latent_dim + rope_dim], paged like the K/V caches (the same
+ * block tables and slots).  latent_dim 256 or 512, rope_dim 64, block_size 16.
+ *
+ * pkv_latent_append writes new tokens' rows: latent[i] as it is (converted to the
+ * cache's type), k_rope[i] rotated as by pkv_rope_append with rot_dim = rope_dim,
+ * and rotates the queries' parts q_rope into q_out.
+ *
+ *   latent        [num_tokens, latent_dim], k_rope [num_tokens, rope_dim] of
+ *                 in_dtype (F32 or BF16), rows `stride` elements apart (views of one
+ *                 projection are fine); strides are multiples of 16 bytes.
+ *   q_rope, q_out [num_tokens, num_q_heads, rope_dim] of in_dtype, a token stride and a
+ *                 head stride each: views of wider heads are fine, such as the last
+ *                 rope_dim numbers of the decode's q.  q_out may be q_rope itself.
+ *                 num_q_heads 0: no queries (both NULL).
+ *   cache_dtype   F32 or BF16.
+ * positions, table, slot_mapping, flags, status as for pkv_rope_append.
+ */
+pkv_status pkv_latent_append(const void *latent, const void *k_rope, pkv_dtype in_dtype, int64_t latent_stride,
+                             int64_t k_rope_stride, const void *q_rope, int64_t q_stride, int64_t q_head_stride,
+                             const int32_t *positions, const float *table, int max_positions,
+                             const int64_t *slot_mapping, int num_tokens, int num_q_heads, int latent_dim,
+                             int rope_dim, int block_size, int num_blocks, void *q_out, int64_t q_out_stride,
+                             int64_t q_out_head_stride, void *cache, pkv_dtype cache_dtype, int flags,
+                             int32_t *status, void *stream);
+
+/*
+ * Latent decode, the absorbed form: one query per sequence, its heads already in
+ * the rows' space (the non-rotated part multiplied with the key's up-projection),
+ * and the result still in it (to be multiplied with the value's):
+ *   out[s, h, :] = sum_{t < seq_lens[s]} softmax_t(scale * q[s, h] . row_t) row_t[:latent_dim]
+ * with row_t read through the block table.  Several queries of one sequence
+ * (verification of drafts) are several rows with the same block table row and
+ * lengths of their own: a row never sees past its length, whatever lies there.
+ *
+ *   q             [num_seqs, num_q_heads, latent_dim + rope_dim] of dtype (F32 or
+ *                 BF16, the cache's and out's type too), dense.  1 to 128 heads.
+ *   block_tables, seq_lens, max_seq_len   as for pkv_paged_attn_decode; 0 gives a
+ *                 zero output row.  A block id outside the pool counts as 16 rows of
+ *                 zeros and is reported as PKV_ERR_OUT_OF_RANGE, as is a length
+ *                 outside [0, max_seq_len], which is clamped.
+ *   num_seqs      up to 2^20 (else PKV_ERR_UNSUPPORTED).
+ *   scale         finite, any sign.
+ *   out           [num_seqs, num_q_heads, latent_dim] of dtype.  With BF16 the softmax
+ *                 weights are rounded to bf16 on the tensor cores; sums are f32.
+ *   workspace     >= pkv_latent_attn_workspace_size(...) bytes, 256-byte aligned.  Its
+ *                 content does not matter; concurrent calls need separate ones.
+ *   status        optional device int32, as for pkv_reshape_and_cache.
+ *   flags         0, or for BF16 PKV_FLAG_TEST_DROP_FIRST_COPY (the failure path,
+ *                 PKV_ERR_TIMEOUT in *status and undefined output rows).
+ * pkv_latent_attn_workspace_size returns 0 for sizes the call refuses.
+ */
+size_t pkv_latent_attn_workspace_size(pkv_dtype dtype, int num_seqs, int num_q_heads, int latent_dim, int rope_dim,
+                                      int block_size, int max_seq_len);
+pkv_status pkv_latent_attn_decode(const void *q, const void *cache, pkv_dtype dtype, const int32_t *block_tables,
+                                  const int32_t *seq_lens, int num_seqs, int num_q_heads, int latent_dim,
+                                  int rope_dim, int block_size, int num_blocks, int max_blocks_per_seq,
+                                  int max_seq_len, float scale, void *out, void *workspace, size_t workspace_bytes,
+                                  int32_t *status, int flags, void *stream);
+
+/*
+ * Latent attention over whole prompts, the expanded form: keys and values of every
+ * head multiplied out from the latent vectors, the rotated key shared by the heads.
+ * Sequences are packed rows as for pkv_prompt_attn; row i of a sequence:
+ *   out[i, h, :] = sum_{j <= i} softmax_j(scale * (q[i, h, :nope] . k[j, h]
+ *                                                  + q[i, h, nope:] . k_rope[j])) v[j, h]
+ *
+ *   q             [num_tokens, num_heads, nope_dim + rope_dim] of dtype (F32 or BF16),
+ *                 heads dense, rows q_stride elements apart.
+ *   k, v          [num_tokens, num_heads, nope_dim] of dtype, a token stride and a head
+ *                 stride each: the halves of one up-projection's heads are fine.
+ *   k_rope        [num_tokens, rope_dim] of dtype, rotated.
+ *   nope_dim      64 or 128; rope_dim 64.  Strides are multiples of 16 bytes.
+ *   out           [num_tokens, num_heads, nope_dim] of dtype, dense.
+ * Other arguments, values that are not finite, bf16 weights and errors as for
+ * pkv_prompt_attn (flags: 0, or for BF16 PKV_FLAG_TEST_DROP_FIRST_COPY).
+ */
+pkv_status pkv_latent_prompt_attn(const void *q, const void *k, const void *k_rope, const void *v, pkv_dtype dtype,
+                                  int64_t q_stride, int64_t k_stride, int64_t k_head_stride, int64_t k_rope_stride,
+                                  int64_t v_stride, int64_t v_head_stride, const int32_t *q_start, int num_seqs,
+                                  int num_tokens, int num_heads, int nope_dim, int rope_dim, int max_q_len,
+                                  float scale, void *out, int32_t *status, int flags, void *stream);
 
 /*
  * Host-side block manager (no GPU calls; thread-safe).  It keeps the page

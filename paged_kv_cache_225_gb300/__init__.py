@@ -13,6 +13,10 @@ current stream and the workspace allocation.
     prompt_attn(q, k, v, q_start, scale, out)          (whole prompts, no cache read)
     tables_step(seq_lens, block_tables, ref_counts, drop_lens=, new_lens=, ...)
     tables_fork(pairs, seq_lens, block_tables, ref_counts)   (page pool on the GPU)
+    rope_append(q, k, v, positions, table, slot_mapping, k_cache, v_cache)   (rotating cache write)
+    latent_append(latent, k_rope, positions, table, slot_mapping, cache, q_rope=, q_out=)
+    latent_attn_decode(q, cache, block_tables, seq_lens, scale, out)
+    latent_prompt_attn(q, k, k_rope, v, q_start, scale, out)   (latent attention, whole prompts)
     copy_blocks(k_cache, v_cache, pairs)
     BlockManager(num_blocks)   (host-side page pool: add / fork / append / free / tables)
 """
@@ -32,6 +36,8 @@ __all__ = ["paged_attn_decode", "paged_attn_decode_append", "paged_attn_prefill"
            "reshape_and_cache", "workspace_size", "partition_tokens",
            "prefill_workspace_size", "prefill_partition_tokens", "copy_blocks",
            "prompt_attn", "tables_step", "tables_fork",
+           "rope_append", "latent_append", "latent_attn_decode", "latent_prompt_attn",
+           "latent_workspace_size",
            "BlockManager",
            "read_status", "PkvError", "lib", "F32", "BF16", "FP8_E5M2", "FP8_E4M3",
            "INT4"]
@@ -41,6 +47,7 @@ IMPL = {"auto": 0x0, "simt": 0x1, "mma": 0x2, "tc": 0x3}  # "tc": several-querie
 FLAG_SEPARATE_MERGE = 0x4
 FLAG_TEST_DROP_FIRST_COPY = 0x100
 FLAG_TEST_SLOW_GATE = 0x400
+FLAG_ROPE_INTERLEAVED = 0x800
 STATUS = {0: "PKV_OK", 1: "PKV_ERR_INVALID_ARG", 2: "PKV_ERR_UNSUPPORTED", 3: "PKV_ERR_CUDA",
           4: "PKV_ERR_OUT_OF_RANGE", 5: "PKV_ERR_TIMEOUT", 6: "PKV_ERR_WORKSPACE",
           7: "PKV_ERR_NO_BLOCKS"}
@@ -134,6 +141,20 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
             L.pkv_tables_step.restype = i
             L.pkv_tables_fork.argtypes = [vp, i, vp, vp, vp, i, i, i, i, vp, vp]
             L.pkv_tables_fork.restype = i
+            L.pkv_rope_append.argtypes = [vp, vp, vp, i, i64, i64, i64, vp, vp, i, i, vp, i, i, i, i, i, i,
+                                          vp, i64, vp, vp, i, f, f, i, vp, vp]
+            L.pkv_rope_append.restype = i
+            L.pkv_latent_append.argtypes = [vp, vp, i, i64, i64, vp, i64, i64, vp, vp, i, vp, i, i, i, i, i, i,
+                                            vp, i64, i64, vp, i, i, vp, vp]
+            L.pkv_latent_append.restype = i
+            L.pkv_latent_attn_workspace_size.argtypes = [i] * 7
+            L.pkv_latent_attn_workspace_size.restype = sz
+            L.pkv_latent_attn_decode.argtypes = [vp, vp, i, vp, vp, i, i, i, i, i, i, i, i, f, vp, vp, sz, vp,
+                                                 i, vp]
+            L.pkv_latent_attn_decode.restype = i
+            L.pkv_latent_prompt_attn.argtypes = [vp, vp, vp, vp, i, i64, i64, i64, i64, i64, i64, vp, i, i, i, i,
+                                                 i, i, f, vp, vp, i, vp]
+            L.pkv_latent_prompt_attn.restype = i
             L.pkv_read_status.argtypes = [vp, i, ctypes.POINTER(ctypes.c_int32), vp]
             L.pkv_read_status.restype = i
             L.pkv_status_string.argtypes = [i]
@@ -747,6 +768,266 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torc
             (q.data_ptr(), k.data_ptr(), v.data_ptr(), code, qs, ks, vs, starts, S, T, Hq,
              kshape[1], D, T if max_q_len is None else min(int(max_q_len), T), float(scale), o, ocode, st,
              int(flags)))
+    return out
+
+
+def _heads(t: torch.Tensor, what: str, dtype: torch.dtype, index: int):
+    """(shape, token stride, head stride) of a [T, H, D] tensor whose heads are dense."""
+    if _cuda_index(t, what) != index:
+        raise ValueError(f"{what} is on {t.device}, expected cuda:{index}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {str(dtype).replace('torch.', '')}")
+    if t.dim() != 3:
+        raise ValueError(f"{what} must have 3 dims, got {tuple(t.shape)}")
+    T, H, D = t.shape
+    row, head, elem = t.stride()
+    if T > 0 and H > 0 and D > 1 and elem != 1:
+        raise ValueError(f"{what}: every head must be dense")
+    if H <= 1:
+        head = D
+    return t.shape, (row if T > 1 else max(H - 1, 0) * head + D), head
+
+
+def _vectors(t: torch.Tensor, what: str, dtype: torch.dtype, index: int):
+    """(shape, row stride) of a [T, D] tensor whose rows are dense."""
+    if _cuda_index(t, what) != index:
+        raise ValueError(f"{what} is on {t.device}, expected cuda:{index}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {str(dtype).replace('torch.', '')}")
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have 2 dims, got {tuple(t.shape)}")
+    T, D = t.shape
+    row, elem = t.stride()
+    if T > 0 and D > 1 and elem != 1:
+        raise ValueError(f"{what}: every row must be dense")
+    return t.shape, (row if T > 1 else D)
+
+
+def _new_tokens(positions, table, slot_mapping, status, T, index):
+    """Pointers of what the rotating cache writes share, and the table's shape."""
+    pos = _ptr(positions, "positions", 1, _I32, index)
+    tab = _ptr(table, "table", 2, torch.float32, index)
+    slots = _ptr(slot_mapping, "slot_mapping", 1, _I64, index)
+    st = _ptr(status, "status", 1, _I32, index)
+    if pos is None or tab is None or slots is None:
+        raise TypeError("positions, table and slot_mapping must be tensors")
+    if positions.numel() != T or slot_mapping.numel() != T or (st is not None and status.numel() != 1):
+        raise ValueError("positions and slot_mapping need one entry per token, status exactly one")
+    if T > _INT_MAX or table.shape[0] > _INT_MAX:
+        raise ValueError("at most 2^31 - 1 tokens and positions")
+    return pos, tab, slots, st
+
+
+def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                table: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                v_cache: torch.Tensor, *, q_out: Optional[torch.Tensor] = None, interleaved: bool = False,
+                k_scale: float = 1.0, v_scale: float = 1.0, status: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """The cache write with the rotation of queries and keys by their positions on the way.
+
+    q [T, Hq, D], k, v [T, Hkv, D] (all f32 or all bf16), rows dense and any multiple of 16
+    bytes apart (views of a fused projection are fine); positions int32 [T]; table f32
+    [max_positions, rot] (rot / 2 cosines, then as many sines of each position's angles; the
+    first rot dims of a head are turned); slot_mapping int64 [T] and the caches as for
+    ``reshape_and_cache``.  Pairs are dims (i, i + rot / 2), or (2i, 2i + 1) if
+    ``interleaved``.  The turned queries go to ``q_out`` (default: in place), which is
+    returned; q may be None.  Tokens with a negative slot are padding: nothing of them is
+    read or written.  ``status`` int32 [1] (optional) records slots and positions out of
+    range, whose tokens are skipped too.
+    """
+    index = _cuda_index(k, "k")
+    dtype = k.dtype
+    code = _FLOATS.get(dtype)
+    if code is None:
+        raise TypeError(f"k: unsupported dtype {dtype}")
+    kshape, ks = _rows(k, "k", dtype, index)
+    vshape, vs = _rows(v, "v", dtype, index)
+    T, Hkv, D = kshape
+    qp = op = None
+    qs = qos = Hq = 0
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        qshape, qs = _rows(q, "q", dtype, index)
+        if q_out is None:
+            q_out = q
+        oshape, qos = _rows(q_out, "q_out", dtype, index)
+        if qshape[0] != T or qshape[2] != D or oshape != qshape:
+            raise ValueError("inconsistent shapes")
+        Hq = qshape[1]
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    pos, tab, slots, st = _new_tokens(positions, table, slot_mapping, status, T, index)
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _check(t, name, 4, torch.device("cuda", index))
+    N, Hkv2, D2, B = _pool_dims(k_cache)
+    if (vshape != kshape or Hkv2 != Hkv or D2 != D or v_cache.shape != k_cache.shape
+            or v_cache.dtype != k_cache.dtype):
+        raise ValueError("inconsistent shapes")
+    if N > _INT_MAX:
+        raise ValueError("at most 2^31 - 1 pages")
+    _launch("pkv_rope_append", index, stream,
+            (qp, k.data_ptr(), v.data_ptr(), code, qs, ks, vs, pos, tab, table.shape[1], table.shape[0], slots, T,
+             Hq, Hkv, D, B, N, op, qos, k_cache.data_ptr(), v_cache.data_ptr(), _dtype_code(k_cache, "k_cache"),
+             float(k_scale), float(v_scale), FLAG_ROPE_INTERLEAVED if interleaved else 0, st))
+    return q_out
+
+
+def latent_append(latent: torch.Tensor, k_rope: torch.Tensor, positions: torch.Tensor, table: torch.Tensor,
+                  slot_mapping: torch.Tensor, cache: torch.Tensor, *, q_rope: Optional[torch.Tensor] = None,
+                  q_out: Optional[torch.Tensor] = None, interleaved: bool = False,
+                  status: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """Writes new tokens' rows (latent vector, rotated key) into a paged latent cache.
+
+    latent [T, R], k_rope [T, 64] (both f32 or both bf16; views of one projection are fine);
+    cache [N, 16, R + 64] (f32 or bf16), R 256 or 512; positions, table [max_positions, 64],
+    slot_mapping, ``interleaved`` and ``status`` as for ``rope_append``.  The queries'
+    rotated parts q_rope [T, H, 64] are turned into ``q_out`` (default: in place; a view of
+    wider heads is fine, such as ``q[..., R:]`` of the decode's q), which is returned.
+    """
+    index = _cuda_index(latent, "latent")
+    dtype = latent.dtype
+    code = _FLOATS.get(dtype)
+    if code is None:
+        raise TypeError(f"latent: unsupported dtype {dtype}")
+    (T, R), ls = _vectors(latent, "latent", dtype, index)
+    (T2, rope), rs = _vectors(k_rope, "k_rope", dtype, index)
+    qp = op = None
+    qs = qh = qos = qoh = H = 0
+    if q_rope is None:
+        if q_out is not None:
+            raise ValueError("q_out without q_rope")
+    else:
+        qshape, qs, qh = _heads(q_rope, "q_rope", dtype, index)
+        if q_out is None:
+            q_out = q_rope
+        oshape, qos, qoh = _heads(q_out, "q_out", dtype, index)
+        if qshape[0] != T or qshape[2] != rope or oshape != qshape:
+            raise ValueError("inconsistent shapes")
+        H = qshape[1]
+        qp, op = q_rope.data_ptr(), q_out.data_ptr()
+    pos, tab, slots, st = _new_tokens(positions, table, slot_mapping, status, T, index)
+    _check(cache, "cache", 3, torch.device("cuda", index))
+    ccode = _FLOATS.get(cache.dtype)
+    if ccode is None:
+        raise TypeError(f"cache: unsupported dtype {cache.dtype}")
+    N, B, row = cache.shape
+    if T2 != T or row != R + rope or table.shape[1] != rope:
+        raise ValueError("inconsistent shapes")
+    if N > _INT_MAX:
+        raise ValueError("at most 2^31 - 1 pages")
+    _launch("pkv_latent_append", index, stream,
+            (latent.data_ptr(), k_rope.data_ptr(), code, ls, rs, qp, qs, qh, pos, tab, table.shape[0], slots, T, H,
+             R, rope, B, N, op, qos, qoh, cache.data_ptr(), ccode, FLAG_ROPE_INTERLEAVED if interleaved else 0,
+             st))
+    return q_out
+
+
+_ROPE = 64  # rotated numbers of a latent row
+
+
+def latent_workspace_size(dtype: torch.dtype, num_seqs: int, num_heads: int, latent_dim: int,
+                          max_seq_len: int) -> int:
+    """Workspace bytes of ``latent_attn_decode`` (pkv_latent_attn_workspace_size)."""
+    code = _FLOATS.get(dtype)
+    n = 0 if code is None else lib().pkv_latent_attn_workspace_size(code, num_seqs, num_heads, latent_dim, _ROPE,
+                                                                    16, max_seq_len)
+    if n == 0:
+        raise ValueError("sizes that latent_attn_decode does not take")
+    return int(n)
+
+
+def latent_attn_decode(q: torch.Tensor, cache: torch.Tensor, block_tables: torch.Tensor,
+                       seq_lens: torch.Tensor, scale: float, out: torch.Tensor, *,
+                       max_seq_len: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
+                       status: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None, flags: int = 0) -> torch.Tensor:
+    """Latent attention of one query per sequence, absorbed form.
+
+    out[s, h] = softmax(scale q[s, h] . rows_s) rows_s[:, :R]: q [S, H, R + 64], cache
+    [N, 16, R + 64] (all f32 or all bf16), R 256 or 512, H up to 128; block_tables int32
+    [S, max_blocks], seq_lens int32 [S] (0: a zero row); out [S, H, R].  ``max_seq_len``
+    bounds seq_lens (default: max_blocks * 16).  Several queries of one sequence are several
+    rows with the same table row.  ``workspace``: ``latent_workspace_size`` bytes (default:
+    allocated for the call on its stream).  ``status`` int32 [1] (optional) records lengths
+    and block ids out of range.  Returns ``out``.
+    """
+    index = _cuda_index(q, "q")
+    dtype = q.dtype
+    code = _FLOATS.get(dtype)
+    if code is None:
+        raise TypeError(f"q: unsupported dtype {dtype}")
+    qp, cp = _ptr(q, "q", 3, dtype, index), _ptr(cache, "cache", 3, dtype, index)
+    tables, lens = _ptr(block_tables, "block_tables", 2, _I32, index), _ptr(seq_lens, "seq_lens", 1, _I32, index)
+    op, st = _ptr(out, "out", 3, dtype, index), _ptr(status, "status", 1, _I32, index)
+    if cp is None or tables is None or lens is None or op is None:
+        raise TypeError("cache, block_tables, seq_lens and out must be tensors")
+    S, H, row = q.shape
+    N, B, row2 = cache.shape
+    R = row - _ROPE
+    width = block_tables.shape[1]
+    if (row2 != row or out.shape != (S, H, R) or block_tables.shape[0] != S or seq_lens.numel() != S
+            or (st is not None and status.numel() != 1)):
+        raise ValueError("inconsistent shapes")
+    if max_seq_len is None:
+        max_seq_len = width * B
+    if max(S, H, N, width, max_seq_len) > _INT_MAX:
+        raise ValueError("at most 2^31 - 1 sequences, pages, entries of a row and tokens")
+    L = _lib if _lib is not None else lib()
+    need = L.pkv_latent_attn_workspace_size(code, S, H, R, _ROPE, B, max_seq_len)
+    if workspace is None:
+        # Of the call's own stream: the allocator hands it out again in that stream's order.
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif _cuda_index(workspace, "workspace") != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on q's device")
+    _launch("pkv_latent_attn_decode", index, stream,
+            (qp, cp, code, tables, lens, S, H, R, _ROPE, B, N, width, int(max_seq_len), float(scale), op,
+             workspace.data_ptr(), workspace.numel() * workspace.element_size(), st, int(flags)))
+    return out
+
+
+def latent_prompt_attn(q: torch.Tensor, k: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor,
+                       q_start: torch.Tensor, scale: float, out: torch.Tensor, *,
+                       max_q_len: Optional[int] = None, status: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None, flags: int = 0) -> torch.Tensor:
+    """Causal latent attention over whole prompts, expanded form, packed one after another.
+
+    q [T, H, D + 64]; k, v [T, H, D] (views such as the halves of one up-projection's heads are
+    fine); k_rope [T, 64], the rotated key of all heads; all f32 or all bf16; D 64 or 128; out
+    [T, H, D] of the same type.  Row i of a sequence attends its rows j <= i with score scale
+    (q[i, h, :D] . k[j, h] + q[i, h, D:] . k_rope[j]).  q_start, ``max_q_len`` and ``status``
+    as for ``prompt_attn``.  Returns ``out``.
+    """
+    index = _cuda_index(q, "q")
+    dtype = q.dtype
+    code = _FLOATS.get(dtype)
+    if code is None:
+        raise TypeError(f"q: unsupported dtype {dtype}")
+    (T, H, row), qs = _rows(q, "q", dtype, index)
+    kshape, ks, kh = _heads(k, "k", dtype, index)
+    vshape, vs, vh = _heads(v, "v", dtype, index)
+    rshape, rs = _vectors(k_rope, "k_rope", dtype, index)
+    o = _ptr(out, "out", 3, dtype, index)
+    starts = _ptr(q_start, "q_start", 1, _I32, index)
+    st = _ptr(status, "status", 1, _I32, index)
+    if o is None or starts is None:
+        raise TypeError("q_start and out must be tensors")
+    D = row - _ROPE
+    S = q_start.numel() - 1
+    if kshape != (T, H, D) or vshape != kshape or rshape != (T, _ROPE) or out.shape != kshape:
+        raise ValueError("inconsistent shapes")
+    if S < 0 or (st is not None and status.numel() != 1):
+        raise ValueError("q_start needs at least one entry, status exactly one")
+    if max(T, S, H) > _INT_MAX:
+        raise ValueError("at most 2^31 - 1 rows, sequences and heads")
+    _launch("pkv_latent_prompt_attn", index, stream,
+            (q.data_ptr(), k.data_ptr(), k_rope.data_ptr(), v.data_ptr(), code, qs, ks, kh, rs, vs, vh, starts, S,
+             T, H, D, _ROPE, T if max_q_len is None else min(int(max_q_len), T), float(scale), o, st, int(flags)))
     return out
 
 

@@ -1,0 +1,391 @@
+// Latent attention for one query per sequence on the CUDA cores (fp32), and the
+// kernel that joins the partial sums of sequences that a range's end cut.
+//
+// Absorbed form: out[s, h] = sum_t softmax_t(scale q[s, h] . row_t) row_t[:R], the
+// scaled_dot_product_attention of the "Inference optimization" lesson (Step 2) in
+// which all heads share one row of R + 64 numbers per token, key and value at once.
+//
+// A CTA of 256 threads has 16 heads of a sequence and walks its pages: scores of
+// 16 heads x 16 tokens (a warp: 4 heads, all tokens, half the dims; a lane 4 heads x
+// 2 tokens on every fourth of those dims), one pass of the softmax with a thread
+// per score, then R / 256 output dims of all heads per thread.
+#include "pkv_latent.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kSimtThreads = 256;
+constexpr int kSimtHeads = 16;
+constexpr int kBad = -1;
+
+template <int R> struct LatentSimt {
+    static constexpr int kRow = R + kRopeDim;
+    static constexpr int kLd = kRow + 4;  // rows 4 banks apart
+    static constexpr int kSmem = 3 * 16 * kLd * 4;
+};
+
+__device__ __forceinline__ void fma2(uint64_t &c, uint64_t a, uint64_t b)
+{
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ float sum2(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r.x + r.y;
+}
+
+// 16 rows of 16-byte pieces into shared memory; rows past `rows` are zero.
+template <typename T, int R>
+__device__ __forceinline__ void load_rows(float *dst, const T *src, int rows)
+{
+    constexpr int kRow = LatentSimt<R>::kRow, kLd = LatentSimt<R>::kLd;
+    for (int e = threadIdx.x; e < 16 * (kRow / 4); e += kSimtThreads) {
+        const int r = e / (kRow / 4), d = 4 * (e % (kRow / 4));
+        float *to = dst + r * kLd + d;
+        if (r >= rows) {
+            *reinterpret_cast<float4 *>(to) = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else if constexpr (sizeof(T) == 4) {
+            cp_async_16(to, src + r * kRow + d);
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(src + r * kRow + d);
+            *reinterpret_cast<float4 *>(to) = make_float4(bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y));
+        }
+    }
+    cp_async_commit();
+}
+
+template <typename T, int R>
+__global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const LatentDecodeParams p)
+{
+    constexpr int kRow = LatentSimt<R>::kRow, kLd = LatentSimt<R>::kLd, kDims = R / kSimtThreads;
+    extern __shared__ __align__(16) float smem_f[];
+    float *sq = smem_f, *sk = sq + 16 * kLd;  // the queries, two pages
+    __shared__ float s_half[2][16][17];       // scores of half the dims
+    __shared__ __align__(16) float s_p[16][16], s_alpha[16];
+    __shared__ float2 s_ml[16];
+    __shared__ LatentPiece s_piece;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int team = blockIdx.x / p.head_tiles, h0 = blockIdx.x % p.head_tiles * kSimtHeads;
+    const int heads = min(kSimtHeads, p.num_heads - h0);
+    const float c = p.negate ? -p.score_scale : p.score_scale;
+
+    LatentWalk walk;
+    if (warp == 0)
+        walk.init(p, team, lane, blockIdx.x == 0);
+    int2 cut = make_int2(kBad, kBad);
+    for (;;) {
+        if (warp == 0) {
+            const LatentPiece next = walk.next(p);
+            if (lane == 0)
+                s_piece = next;
+        }
+        __syncthreads();
+        const LatentPiece piece = s_piece;
+        if (piece.s < 0)
+            break;
+        if (piece.first > 0)
+            cut.x = piece.s;
+        if (piece.last < piece.tiles)
+            cut.y = piece.s;
+        load_rows<T, R>(sq, static_cast<const T *>(p.q) + (static_cast<size_t>(piece.s) * p.num_heads + h0) * kRow,
+                        heads);
+        const int from = piece.first * (kLatentTokens / 16);  // pages
+        const int to = min(piece.last * (kLatentTokens / 16), (piece.len + 15) / 16);
+        const int32_t *table = p.block_tables + static_cast<size_t>(piece.s) * p.max_blocks;
+        auto load_page = [&](int page) {
+            const int block = __ldg(table + page);
+            const bool ok = static_cast<unsigned>(block) < static_cast<unsigned>(p.num_blocks);
+            if (!ok && threadIdx.x == 0)
+                set_status(p.status, PKV_ERR_OUT_OF_RANGE);
+            load_rows<T, R>(sk + (page & 1) * 16 * kLd,
+                            static_cast<const T *>(p.cache) + static_cast<size_t>(ok ? block : 0) * 16 * kRow,
+                            ok ? min(16, piece.len - 16 * page) : 0);
+        };
+        uint64_t o[kDims == 2 ? 16 : 8];  // heads x dims, in pairs
+#pragma unroll
+        for (int i = 0; i < (kDims == 2 ? 16 : 8); ++i)
+            o[i] = 0;
+        float m = -INFINITY, l = 0.f;  // of head threadIdx.x / 16
+        if (from < to)
+            load_page(from);
+        for (int page = from; page < to; ++page) {
+            cp_async_wait_all();
+            __syncthreads();
+            if (page + 1 < to)
+                load_page(page + 1);
+            const float *k = sk + (page & 1) * 16 * kLd;
+            {
+                // Heads 4 (warp % 4) .., dims of half warp / 4, tokens lane / 4 and lane / 4 + 8.
+                const int half = warp >> 2, hq = 4 * (warp & 3);
+                uint64_t acc[4][2] = {};
+                const float *kq = sq + hq * kLd + half * (kRow / 2) + 4 * (lane & 3);
+                const float *kr = k + (lane >> 2) * kLd + half * (kRow / 2) + 4 * (lane & 3);
+#pragma unroll 2
+                for (int d = 0; d < kRow / 2; d += 16) {
+                    ulonglong2 kf[2];
+                    kf[0] = *reinterpret_cast<const ulonglong2 *>(kr + d);
+                    kf[1] = *reinterpret_cast<const ulonglong2 *>(kr + 8 * kLd + d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const ulonglong2 qf = *reinterpret_cast<const ulonglong2 *>(kq + i * kLd + d);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            fma2(acc[i][j], qf.x, kf[j].x);
+                            fma2(acc[i][j], qf.y, kf[j].y);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float x = sum2(acc[i][j]);
+                        x += __shfl_xor_sync(kFullMask, x, 1);
+                        x += __shfl_xor_sync(kFullMask, x, 2);
+                        if ((lane & 3) == 0)
+                            s_half[half][hq + i][(lane >> 2) + 8 * j] = x;
+                    }
+            }
+            __syncthreads();
+            {
+                const int h = threadIdx.x >> 4, t = threadIdx.x & 15;
+                const float x = 16 * page + t < piece.len ? (s_half[0][h][t] + s_half[1][h][t]) * c : -INFINITY;
+                float mx = x;
+#pragma unroll
+                for (int w = 8; w >= 1; w >>= 1)
+                    mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, w));
+                const float m_new = fmaxf(m, mx);
+                const float off = m_new == -INFINITY ? 0.f : m_new;  // nothing but -inf: weights 0
+                const float alpha = exp2f(m - off), w = exp2f(x - off);
+                m = m_new;
+                l = l * alpha + w;
+                s_p[t][h] = w;
+                if (t == 0)
+                    s_alpha[h] = alpha;
+            }
+            __syncthreads();
+            // Output dims threadIdx.x (+ R / 2).
+            if constexpr (kDims == 2) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float a = s_alpha[i];
+                    uint64_t a2;
+                    asm("mov.b64 %0, {%1, %1};" : "=l"(a2) : "f"(a));
+                    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(o[i]) : "l"(a2));
+                }
+#pragma unroll 4
+                for (int t = 0; t < 16; ++t) {
+                    const uint64_t v = *reinterpret_cast<const uint64_t *>(k + t * kLd + 2 * threadIdx.x);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 w = *reinterpret_cast<const float4 *>(&s_p[t][i]);
+                        const float ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint64_t w2;
+                            asm("mov.b64 %0, {%1, %1};" : "=l"(w2) : "f"(ww[e]));
+                            fma2(o[i + e], w2, v);
+                        }
+                    }
+                }
+            } else {
+                // One dim: pairs of heads.
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint64_t a2 = *reinterpret_cast<const uint64_t *>(&s_alpha[2 * i]);
+                    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(o[i]) : "l"(a2));
+                }
+#pragma unroll 4
+                for (int t = 0; t < 16; ++t) {
+                    const float x = k[t * kLd + threadIdx.x];
+                    uint64_t v;
+                    asm("mov.b64 %0, {%1, %1};" : "=l"(v) : "f"(x));
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(&s_p[t][2 * i]);
+                        fma2(o[i], w.x, v);
+                        fma2(o[i + 1], w.y, v);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int w = 8; w >= 1; w >>= 1)
+            l += __shfl_xor_sync(kFullMask, l, w);
+        if ((threadIdx.x & 15) == 0)
+            s_ml[threadIdx.x >> 4] = make_float2(m, l);
+        cp_async_wait_all();
+        __syncthreads();
+        const bool whole = piece.whole();
+        const size_t slot = static_cast<size_t>(latent_slot(team, piece)) * p.head_tiles + blockIdx.x % p.head_tiles;
+#pragma unroll
+        for (int h = 0; h < 16; ++h) {
+            if (h >= heads)
+                break;
+            float2 y;
+            if constexpr (kDims == 2) {
+                asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(o[h]));
+            } else {
+                float2 z;
+                asm("mov.b64 {%0, %1}, %2;" : "=f"(z.x), "=f"(z.y) : "l"(o[h / 2]));
+                y.x = h & 1 ? z.y : z.x;
+                y.y = 0.f;
+            }
+            const int d = kDims * threadIdx.x;
+            if (!whole) {
+                float *dst = p.part + (slot * kSimtHeads + h) * R + d;
+                dst[0] = y.x;
+                if constexpr (kDims == 2)
+                    dst[1] = y.y;
+                if (threadIdx.x == 0)
+                    p.part_ml[slot * kSimtHeads + h] = s_ml[h];
+                continue;
+            }
+            const float sum = s_ml[h].y;
+            // An empty sequence's row is zero.
+            y.x = piece.len > 0 ? y.x / sum : 0.f;
+            y.y = piece.len > 0 ? y.y / sum : 0.f;
+            const size_t at = (static_cast<size_t>(piece.s) * p.num_heads + h0 + h) * R + d;
+            if constexpr (sizeof(T) == 4) {
+                static_cast<float *>(p.out)[at] = y.x;
+                if constexpr (kDims == 2)
+                    static_cast<float *>(p.out)[at + 1] = y.y;
+            } else {
+                static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16(y.x);
+                if constexpr (kDims == 2)
+                    static_cast<__nv_bfloat16 *>(p.out)[at + 1] = __float2bfloat16(y.y);
+            }
+        }
+        __syncthreads();  // s_ml, the queries and the piece are read
+    }
+    if (threadIdx.x == 0 && blockIdx.x % p.head_tiles == 0)
+        p.pieces[team] = cut;
+}
+
+// ------------------------------------------------------------------ joining
+
+constexpr int kMergeWarps = 8;
+
+// Block (team - 1, heads): joins the sequence that the start of `team` cuts, if it
+// begins in the team before.  A warp has one head:
+//   M = max_i m_i,  out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i
+// over the pieces i in order, so the result does not depend on who wrote first.
+template <typename T, int R>
+__global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const LatentDecodeParams p)
+{
+    const int lane = threadIdx.x & 31, team = blockIdx.x + 1;
+    const int h = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+    const int s = p.pieces[team].x;
+    // The piece before starts the sequence if nothing before that one belongs to it.
+    if (s < 0 || h >= p.num_heads || p.pieces[team - 1].y != s || p.pieces[team - 1].x == s)
+        return;
+    const int ht = h / p.tile_heads, hh = h % p.tile_heads;
+    int last = team;  // the last team with a piece
+    for (int t = team; t < p.teams; t += 32) {
+        const unsigned same = __ballot_sync(kFullMask, t + lane < p.teams && p.pieces[t + lane].x == s);
+        last = t + __popc(same) - 1;  // its teams are neighbours
+        if (same != kFullMask)
+            break;
+    }
+    auto row = [&](int t) {  // t = team - 1: the piece the sequence starts with
+        const size_t slot = t < team ? 2 * t + 1 : 2 * t;
+        return (slot * p.head_tiles + ht) * p.tile_heads + hh;
+    };
+    float top = -INFINITY;
+    for (int t = team - 1 + lane; t <= last; t += 32)
+        top = fmaxf(top, p.part_ml[row(t)].x);
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, w));
+    constexpr int kVecs = R / 128;
+    float4 sum[kVecs] = {};
+    float total = 0.f;
+#pragma unroll 4
+    for (int t = team - 1; t <= last; ++t) {
+        const float2 ml = p.part_ml[row(t)];
+        const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+        total = fmaf(w, ml.y, total);
+        const float4 *src = reinterpret_cast<const float4 *>(p.part + row(t) * R);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const float4 x = src[32 * i + lane];
+            sum[i].x = fmaf(w, x.x, sum[i].x);
+            sum[i].y = fmaf(w, x.y, sum[i].y);
+            sum[i].z = fmaf(w, x.z, sum[i].z);
+            sum[i].w = fmaf(w, x.w, sum[i].w);
+        }
+    }
+    const size_t at = (static_cast<size_t>(s) * p.num_heads + h) * R;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        const float4 y = make_float4(sum[i].x / total, sum[i].y / total, sum[i].z / total, sum[i].w / total);
+        if constexpr (sizeof(T) == 4)
+            reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at)[32 * i + lane] = y;
+        else
+            reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at)[32 * i + lane] =
+                make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+    }
+}
+
+template <typename T, int R> pkv_status launch_simt(const LatentDecodeParams &p, cudaStream_t stream)
+{
+    static ContextCache cache;
+    int set = 0;
+    const pkv_status rc = cache.get(&set, [](int *out) -> pkv_status {
+        *out = 1;
+        return cudaFuncSetAttribute(latent_simt_kernel<T, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    LatentSimt<R>::kSmem) == cudaSuccess
+                   ? PKV_OK
+                   : PKV_ERR_CUDA;
+    });
+    if (rc != PKV_OK)
+        return rc;
+    latent_simt_kernel<T, R><<<p.teams * p.head_tiles, kSimtThreads, LatentSimt<R>::kSmem, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+template <typename T, int R> pkv_status launch_merge(const LatentDecodeParams &p, cudaStream_t stream)
+{
+    const dim3 grid(p.teams - 1, (p.num_heads + kMergeWarps - 1) / kMergeWarps);
+    latent_merge_kernel<T, R><<<grid, 32 * kMergeWarps, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t latent_plan(LatentDecodeParams &p, int dtype)
+{
+    p.tile_heads = kSimtHeads;
+    p.head_tiles = (p.num_heads + p.tile_heads - 1) / p.tile_heads;
+    // Two CTAs to an SM.
+    const long ctas = 2 * 152;
+    const long tiles = (static_cast<long>(p.max_len) + kLatentTokens - 1) / kLatentTokens;
+    const long units = static_cast<long>(p.num_seqs) * (tiles > 1 ? tiles : 1);
+    const long most = ctas / p.head_tiles;
+    p.teams = static_cast<int>(units < most ? units : most);
+    const size_t rows = 2 * static_cast<size_t>(p.teams) * p.head_tiles * p.tile_heads;
+    return (rows * (p.latent_dim * sizeof(float) + sizeof(float2)) + p.teams * sizeof(int2) + 255) / 256 * 256;
+}
+
+pkv_status launch_latent_decode_simt(const LatentDecodeParams &p, int dtype, cudaStream_t stream)
+{
+    if (dtype == PKV_F32)
+        return p.latent_dim == 512 ? launch_simt<float, 512>(p, stream) : launch_simt<float, 256>(p, stream);
+    return p.latent_dim == 512 ? launch_simt<__nv_bfloat16, 512>(p, stream)
+                               : launch_simt<__nv_bfloat16, 256>(p, stream);
+}
+
+pkv_status launch_latent_merge(const LatentDecodeParams &p, int dtype, cudaStream_t stream)
+{
+    // A sequence of one tile is never cut.
+    if (p.teams <= 1 || p.max_len <= kLatentTokens)
+        return PKV_OK;
+    if (dtype == PKV_F32)
+        return p.latent_dim == 512 ? launch_merge<float, 512>(p, stream) : launch_merge<float, 256>(p, stream);
+    return p.latent_dim == 512 ? launch_merge<__nv_bfloat16, 512>(p, stream)
+                               : launch_merge<__nv_bfloat16, 256>(p, stream);
+}
+
+}  // namespace pkv
