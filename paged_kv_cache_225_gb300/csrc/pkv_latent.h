@@ -89,7 +89,7 @@ constexpr int kLatentMaxSeqs = 1 << 20;  // every CTA reads all lengths once
 // the bytes of workspace, 0 for sizes without a plan.
 size_t latent_plan(LatentDecodeParams &p, int dtype);
 
-pkv_status launch_latent_decode_simt(const LatentDecodeParams &p, int dtype, cudaStream_t stream);
+pkv_status launch_latent_decode_simt(const LatentDecodeParams &p, cudaStream_t stream);
 pkv_status launch_latent_decode_tc(const LatentDecodeParams &p, cudaStream_t stream);
 pkv_status launch_latent_merge(const LatentDecodeParams &p, int dtype, cudaStream_t stream);
 pkv_status launch_latent_prompt_simt(const LatentPromptParams &p, int dtype, cudaStream_t stream);

@@ -37,26 +37,21 @@ __device__ __forceinline__ float sum2(uint64_t v)
 }
 
 // 16 rows of 16-byte pieces into shared memory; rows past `rows` are zero.
-template <typename T, int R>
-__device__ __forceinline__ void load_rows(float *dst, const T *src, int rows)
+template <int R> __device__ __forceinline__ void load_rows(float *dst, const float *src, int rows)
 {
     constexpr int kRow = LatentSimt<R>::kRow, kLd = LatentSimt<R>::kLd;
     for (int e = threadIdx.x; e < 16 * (kRow / 4); e += kSimtThreads) {
         const int r = e / (kRow / 4), d = 4 * (e % (kRow / 4));
         float *to = dst + r * kLd + d;
-        if (r >= rows) {
-            *reinterpret_cast<float4 *>(to) = make_float4(0.f, 0.f, 0.f, 0.f);
-        } else if constexpr (sizeof(T) == 4) {
+        if (r < rows)
             cp_async_16(to, src + r * kRow + d);
-        } else {
-            const uint2 x = *reinterpret_cast<const uint2 *>(src + r * kRow + d);
-            *reinterpret_cast<float4 *>(to) = make_float4(bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y));
-        }
+        else
+            *reinterpret_cast<float4 *>(to) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     cp_async_commit();
 }
 
-template <typename T, int R>
+template <int R>
 __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const LatentDecodeParams p)
 {
     constexpr int kRow = LatentSimt<R>::kRow, kLd = LatentSimt<R>::kLd, kDims = R / kSimtThreads;
@@ -89,8 +84,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const Late
             cut.x = piece.s;
         if (piece.last < piece.tiles)
             cut.y = piece.s;
-        load_rows<T, R>(sq, static_cast<const T *>(p.q) + (static_cast<size_t>(piece.s) * p.num_heads + h0) * kRow,
-                        heads);
+        load_rows<R>(sq, static_cast<const float *>(p.q) + (static_cast<size_t>(piece.s) * p.num_heads + h0) * kRow,
+                     heads);
         const int from = piece.first * (kLatentTokens / 16);  // pages
         const int to = min(piece.last * (kLatentTokens / 16), (piece.len + 15) / 16);
         const int32_t *table = p.block_tables + static_cast<size_t>(piece.s) * p.max_blocks;
@@ -99,9 +94,9 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const Late
             const bool ok = static_cast<unsigned>(block) < static_cast<unsigned>(p.num_blocks);
             if (!ok && threadIdx.x == 0)
                 set_status(p.status, PKV_ERR_OUT_OF_RANGE);
-            load_rows<T, R>(sk + (page & 1) * 16 * kLd,
-                            static_cast<const T *>(p.cache) + static_cast<size_t>(ok ? block : 0) * 16 * kRow,
-                            ok ? min(16, piece.len - 16 * page) : 0);
+            load_rows<R>(sk + (page & 1) * 16 * kLd,
+                         static_cast<const float *>(p.cache) + static_cast<size_t>(ok ? block : 0) * 16 * kRow,
+                         ok ? min(16, piece.len - 16 * page) : 0);
         };
         uint64_t o[kDims == 2 ? 16 : 8];  // heads x dims, in pairs
 #pragma unroll
@@ -247,16 +242,10 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const Late
             // An empty sequence's row is zero.
             y.x = piece.len > 0 ? y.x / sum : 0.f;
             y.y = piece.len > 0 ? y.y / sum : 0.f;
-            const size_t at = (static_cast<size_t>(piece.s) * p.num_heads + h0 + h) * R + d;
-            if constexpr (sizeof(T) == 4) {
-                static_cast<float *>(p.out)[at] = y.x;
-                if constexpr (kDims == 2)
-                    static_cast<float *>(p.out)[at + 1] = y.y;
-            } else {
-                static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16(y.x);
-                if constexpr (kDims == 2)
-                    static_cast<__nv_bfloat16 *>(p.out)[at + 1] = __float2bfloat16(y.y);
-            }
+            float *dst = static_cast<float *>(p.out) + (static_cast<size_t>(piece.s) * p.num_heads + h0 + h) * R + d;
+            dst[0] = y.x;
+            if constexpr (kDims == 2)
+                dst[1] = y.y;
         }
         __syncthreads();  // s_ml, the queries and the piece are read
     }
@@ -329,20 +318,20 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const La
     }
 }
 
-template <typename T, int R> pkv_status launch_simt(const LatentDecodeParams &p, cudaStream_t stream)
+template <int R> pkv_status launch_simt(const LatentDecodeParams &p, cudaStream_t stream)
 {
     static ContextCache cache;
     int set = 0;
     const pkv_status rc = cache.get(&set, [](int *out) -> pkv_status {
         *out = 1;
-        return cudaFuncSetAttribute(latent_simt_kernel<T, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(latent_simt_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     LatentSimt<R>::kSmem) == cudaSuccess
                    ? PKV_OK
                    : PKV_ERR_CUDA;
     });
     if (rc != PKV_OK)
         return rc;
-    latent_simt_kernel<T, R><<<p.teams * p.head_tiles, kSimtThreads, LatentSimt<R>::kSmem, stream>>>(p);
+    latent_simt_kernel<R><<<p.teams * p.head_tiles, kSimtThreads, LatentSimt<R>::kSmem, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -357,10 +346,10 @@ template <typename T, int R> pkv_status launch_merge(const LatentDecodeParams &p
 
 size_t latent_plan(LatentDecodeParams &p, int dtype)
 {
-    p.tile_heads = kSimtHeads;
+    // fp32: two CTAs to an SM.  bf16: one.
+    p.tile_heads = dtype == PKV_F32 || p.num_heads <= 16 ? 16 : p.num_heads <= 32 ? 32 : 64;
     p.head_tiles = (p.num_heads + p.tile_heads - 1) / p.tile_heads;
-    // Two CTAs to an SM.
-    const long ctas = 2 * 152;
+    const long ctas = dtype == PKV_F32 ? 2 * 152 : 152;
     const long tiles = (static_cast<long>(p.max_len) + kLatentTokens - 1) / kLatentTokens;
     const long units = static_cast<long>(p.num_seqs) * (tiles > 1 ? tiles : 1);
     const long most = ctas / p.head_tiles;
@@ -369,12 +358,9 @@ size_t latent_plan(LatentDecodeParams &p, int dtype)
     return (rows * (p.latent_dim * sizeof(float) + sizeof(float2)) + p.teams * sizeof(int2) + 255) / 256 * 256;
 }
 
-pkv_status launch_latent_decode_simt(const LatentDecodeParams &p, int dtype, cudaStream_t stream)
+pkv_status launch_latent_decode_simt(const LatentDecodeParams &p, cudaStream_t stream)
 {
-    if (dtype == PKV_F32)
-        return p.latent_dim == 512 ? launch_simt<float, 512>(p, stream) : launch_simt<float, 256>(p, stream);
-    return p.latent_dim == 512 ? launch_simt<__nv_bfloat16, 512>(p, stream)
-                               : launch_simt<__nv_bfloat16, 256>(p, stream);
+    return p.latent_dim == 512 ? launch_simt<512>(p, stream) : launch_simt<256>(p, stream);
 }
 
 pkv_status launch_latent_merge(const LatentDecodeParams &p, int dtype, cudaStream_t stream)

@@ -1,0 +1,759 @@
+// Latent attention for one query per sequence on the tcgen05 tensor cores (bf16).
+//
+// Absorbed form: out[s, h] = sum_t softmax_t(scale q[s, h] . row_t) row_t[:R] (the
+// scaled_dot_product_attention of the "Inference optimization" lesson, Step 2, with
+// one row of R + 64 numbers per token, key and value at once).  One pass over the
+// rows with the running maximum and sum of the softmax.
+//
+// Layout on the GPU:
+//  * Tokens lie on the rows of the products and heads on their columns: S^T = rows
+//    Q^T (M = 64 tokens, N = heads) and O^T = rows^T P^T (M = 128 dims at a time).
+//    So a call pays for the heads it has, in steps of 16, 32 and 64, and the same
+//    shared-memory copy of a row (64 tokens x 64 dims, 128-byte swizzle) is the
+//    K-major operand of the one and the M-major operand of the other.
+//  * A CTA (one per SM) has up to 64 heads and walks a range of tiles of 64 tokens
+//    (pkv_latent.cuh).  Warp 8 issues the TMA loads (a box per page and 64 dims),
+//    warp 9 the MMAs, warps 0-7 compute the softmax, four for each half of the heads.
+//  * TMEM: two buffers of S^T, and O^T.  P^T goes through shared memory.
+//  * The rings hold the rotated part of a tile (8 KB) and pairs of 64 dims (16 KB)
+//    on their own: the scores start with the first that lands, and a pair's slot is
+//    filled again when its part of O^T is done.
+//  * The MMA warp takes whichever is ready: P V of a tile, which frees the ring, or
+//    the next piece of the scores of the tile after it.
+//  * The reference of a head's weights is raised only when a score exceeds it by 2^8;
+//    O^T is then rescaled in TMEM.  All weights of a head and tile share it, so the
+//    four warps of a half agree through a barrier.
+//  * Rows past the sequence's end are zeroed in shared memory before P V, which
+//    multiplies them with 0: they may hold anything.
+//  * Every wait is bounded; a timeout records PKV_ERR_TIMEOUT, stops every role, lets
+//    copies and MMAs in flight finish and frees TMEM.  The warps of a half leave
+//    together: none waits at a barrier for one that has gone.
+#include <type_traits>
+
+#include "pkv_latent.cuh"
+#include "pkv_tc.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kSoftWarps = 8;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kTok = kLatentTokens;
+constexpr int kChunk = kTok * 128;  // bytes of 64 tokens x 64 dims
+constexpr int kPair = 2 * kChunk;
+constexpr int kPages = kTok / kBlockSize;
+
+template <int R, int NH> struct LtGeom {
+    static constexpr int kPairs = R / 128;               // per tile
+    static constexpr int kQ = (R / 64 + 1) * NH * 128;   // bytes of the queries
+    static constexpr int kP = NH * 128;
+    static constexpr int kRoom = 229 * 1024 - kQ - kP - 4096;  // for the rings, 1 KB of alignment taken off
+    static constexpr int NR = NH == 64 && R == 512 ? 2 : 3;    // slots of rotated parts
+    static constexpr int NP = (kRoom - NR * kChunk) / kPair < 12 ? (kRoom - NR * kChunk) / kPair : 12;
+    static constexpr int kSmem = 1024 + kQ + kP + NR * kChunk + NP * kPair;
+    static constexpr int kOCol = 2 * NH;
+    static constexpr int kCols = kOCol + kPairs * NH;    // TMEM columns
+    static constexpr int kAlloc = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+    static_assert(NP >= kPairs + 1 && kCols <= 512, "a tile and a half fit");
+};
+
+struct LatentMaps {
+    CUtensorMap q, rows;
+};
+
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// D (+)= A B, both from shared memory.
+template <bool kAccumulate> __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc)
+{
+    asm volatile("tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, %4;" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+                 "n"(kAccumulate ? 1 : 0));
+}
+
+__device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) { return static_cast<uint64_t>(hi) << 32 | lo; }
+
+// 16 lanes x 8 J columns of f32 as fragments: registers 4j, 4j + 1 of a thread are row
+// lane / 4, columns 8j + 2 (lane % 4) and the next; 4j + 2, 4j + 3 the same of row + 8.
+// Load and wait are one statement: between two, the compiler may copy registers that
+// the load has yet to fill.
+template <int J> __device__ __forceinline__ void tmem_ld_rows(uint32_t addr, float (&x)[4 * J])
+{
+    if constexpr (J == 1) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+            : "r"(addr)
+            : "memory");
+    } else if constexpr (J == 2) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+            : "r"(addr)
+            : "memory");
+    } else {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]),
+              "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
+            : "r"(addr)
+            : "memory");
+    }
+}
+
+// 8 columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, float (&v)[8])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const float (&v)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "f"(v[0]),
+                 "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
+// 8 x 8 matrices of 16-bit fragments, transposed: lane l gives the address of row
+// l % 8 of matrix l / 8.
+__device__ __forceinline__ void stsm_t4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void stsm_t2(uint32_t addr, uint32_t a, uint32_t b)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b)
+                 : "memory");
+}
+
+// Barrier of the four softmax warps of half g; the second form also ORs a predicate.
+__device__ __forceinline__ void half_sync(int g)
+{
+    asm volatile("barrier.sync %0, 128;" ::"r"(g + 1) : "memory");
+}
+__device__ __forceinline__ bool half_any(int g, bool x)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+        "barrier.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(g + 1), "r"(x ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Whether a phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// A ring's position: slot and parity of its phase.
+template <int N> struct Ring {
+    uint32_t at = 0, par = 0;
+    __device__ __forceinline__ void step()
+    {
+        if (++at == N) {
+            at = 0;
+            par ^= 1;
+        }
+    }
+};
+
+template <int R, int NH>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_tc_kernel(const __grid_constant__ LatentDecodeParams p, const __grid_constant__ LatentMaps maps)
+{
+    using Geo = LtGeom<R, NH>;
+    constexpr int NR = Geo::NR, NP = Geo::NP, kPairs = Geo::kPairs;
+    constexpr int J = NH / 16;          // octets of columns per half
+    constexpr int kHalfCols = NH / 2;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) uint64_t rope_full[NR], rope_empty[NR], pair_full[NP], pair_empty[NP];
+    __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full, pv_done, o_free, drain;
+    __shared__ __align__(16) float s_red[2][4][32];  // per half and warp: maxima or sums of its heads
+    __shared__ __align__(16) float s_col[NH];        // per head: a factor of its column of O^T
+    __shared__ LatentWalk s_walk;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_failed[2][2];
+    volatile int *abort = &s_abort;
+
+    const int warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0);
+    const int lane = threadIdx.x & 31;
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t smem0 = (raw + 1023u) & ~1023u;
+    unsigned char *smem = smem_raw + (smem0 - raw);
+    constexpr int kPOff = Geo::kQ, kRopeOff = kPOff + Geo::kP, kPairOff = kRopeOff + NR * kChunk;
+    const int team = blockIdx.x / p.head_tiles, ht = blockIdx.x % p.head_tiles;
+    const int h0 = ht * NH;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NR; ++i) {
+            mbar_init(&rope_full[i], 1);
+            mbar_init(&rope_empty[i], 1);
+        }
+        for (int i = 0; i < NP; ++i) {
+            mbar_init(&pair_full[i], 1);
+            mbar_init(&pair_empty[i], 1);
+        }
+        mbar_init(&q_full, 1);
+        mbar_init(&q_empty, 1);
+        mbar_init(&s_full[0], 1);
+        mbar_init(&s_full[1], 1);
+        mbar_init(&p_full, kSoftWarps);
+        mbar_init(&pv_done, 1);
+        mbar_init(&o_free, kSoftWarps);
+        mbar_init(&drain, 1);
+        s_abort = 0;
+        s_failed[0][0] = s_failed[0][1] = s_failed[1][0] = s_failed[1][1] = 0;
+        fence_mbar_init();
+    }
+    if (warp == kProducerWarp) {
+        if (lane < 2) {
+            const CUtensorMap *map = lane == 0 ? &maps.q : &maps.rows;
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+        }
+        LatentWalk walk;
+        walk.init(p, team, lane, blockIdx.x == 0);
+        if (lane == 0)
+            s_walk = walk;
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                     "r"(Geo::kAlloc)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    LatentWalk walk = s_walk;
+
+    if (warp == kProducerWarp) {
+        // ------------------------------------------------------- copies
+        Ring<NR> rope;
+        Ring<NP> pair;
+        uint32_t ropes = 0, pairs = 0, pieces = 0;
+        bool ok = true;
+        for (;;) {
+            const LatentPiece piece = walk.next(p);
+            if (piece.s < 0 || !ok)
+                break;
+            if (piece.len == 0)
+                continue;
+            if (pieces > 0)
+                ok = warp_wait(&q_empty, (pieces - 1) & 1, abort);
+            if (!ok)
+                break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&q_full, Geo::kQ);
+                for (int c = 0; c <= R / 64; ++c)
+                    tma_load_3d(smem + c * NH * 128, &maps.q, 64 * c, h0, piece.s, &q_full);
+            }
+            ++pieces;
+            const int32_t *table = p.block_tables + static_cast<size_t>(piece.s) * p.max_blocks;
+            const int pages = (piece.len + kBlockSize - 1) / kBlockSize;
+            // Eight tiles' block ids at a time, a lane each, the next eight on their way.
+            auto ids_at = [&](int j) {
+                const int page = j * kPages + lane;
+                return page < pages ? __ldg(table + page) : 0;
+            };
+            int ids = 0, next_ids = ids_at(piece.first);
+            for (int j = piece.first; j < piece.last; ++j) {
+                const int in8 = (j - piece.first) & 7;
+                if (in8 == 0) {
+                    ids = next_ids;
+                    if (static_cast<unsigned>(ids) >= static_cast<unsigned>(p.num_blocks)) {
+                        set_status(p.status, PKV_ERR_OUT_OF_RANGE);
+                        ids = p.num_blocks;  // past the map: zeros
+                    }
+                    next_ids = j + 8 < piece.last ? ids_at(j + 8) : 0;
+                }
+                const int there = min(kPages, pages - j * kPages);
+                const int page = lane & 3;
+                const int id = __shfl_sync(kFullMask, ids, in8 * kPages + page);
+                ok = warp_wait(&rope_empty[rope.at], rope.par ^ 1, abort);
+                if (!ok)
+                    break;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&rope_full[rope.at], there * 2048);
+                __syncwarp();
+                if (lane < there && !(p.drop_first_copy && blockIdx.x == 0 && ropes == 0 && lane == 0))
+                    tma_load_3d(smem + kRopeOff + rope.at * kChunk + page * 2048, &maps.rows, R, 0, id,
+                                &rope_full[rope.at]);
+                __syncwarp();
+                rope.step();
+                ++ropes;
+                for (int m = 0; m < kPairs; ++m) {
+                    ok = warp_wait(&pair_empty[pair.at], pair.par ^ 1, abort);
+                    if (!ok)
+                        break;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&pair_full[pair.at], 2 * there * 2048);
+                    __syncwarp();
+                    if (lane < 8 && page < there)
+                        tma_load_3d(smem + kPairOff + pair.at * kPair + (lane >> 2) * kChunk + page * 2048,
+                                    &maps.rows, 128 * m + 64 * (lane >> 2), 0, id, &pair_full[pair.at]);
+                    __syncwarp();
+                    pair.step();
+                    ++pairs;
+                }
+                if (!ok)
+                    break;
+            }
+        }
+        if (!ok && lane == 0) {
+            set_status(p.status, PKV_ERR_TIMEOUT);
+            *abort = 1;
+        }
+        // Every copy still in flight lands before the CTA exits.
+        if (lane == 0) {
+            for (uint32_t c = ropes > NR ? ropes - NR : 0; c < ropes; ++c)
+                mbar_wait_bounded(&rope_full[c % NR], (c / NR) & 1, kWaitLimitNs);
+            for (uint32_t c = pairs > NP ? pairs - NP : 0; c < pairs; ++c)
+                mbar_wait_bounded(&pair_full[c % NP], (c / NP) & 1, kWaitLimitNs);
+            if (pieces > 0)
+                mbar_wait_bounded(&q_full, (pieces - 1) & 1, kWaitLimitNs);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------- MMA issue
+        constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;  // 8-row groups 1 KB apart, 128-byte swizzle
+        const uint32_t id_s = tc_idesc(kTok, NH, false) | (p.negate ? 1u << 13 : 0u);
+        constexpr uint32_t kIdPV = tc_idesc(128, NH, false) | 1u << 15;  // A is M-major
+        const bool leader = elect_one();
+        const uint32_t qlo = (smem0 >> 4) | 1u << 16, plo = ((smem0 + kPOff) >> 4) | 1u << 16;
+        const uint32_t rlo = ((smem0 + kRopeOff) >> 4) | 1u << 16, klo = ((smem0 + kPairOff) >> 4) | 1u << 16;
+        const uint32_t vlo = ((smem0 + kPairOff) >> 4) | (kChunk >> 4) << 16;  // 64-dim halves one chunk apart
+        Ring<NR> rope;
+        Ring<NP> kp, vp;                     // pairs as keys, as values
+        uint32_t tiles = 0, pieces = 0;      // scored
+        uint32_t pvs = 0, pv_pieces = 0;     // multiplied with P
+        bool pend = false, pend_first = false;
+        bool ok = true;
+        auto ready = [&](uint64_t *bar, uint32_t par) { return __all_sync(kFullMask, mbar_test(bar, par)); };
+        // 4 steps of 16 dims of 64 tokens' scores.
+        auto scores = [&](uint32_t d, uint32_t a, uint32_t b, bool first) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (first && k == 0)
+                    mma_ss<false>(d, desc64(a, kHi), desc64(b, kHi), id_s);
+                else
+                    mma_ss<true>(d, desc64(a + 2 * k, kHi), desc64(b + 2 * k, kHi), id_s);
+            }
+        };
+        auto issue_pv = [&] {
+            tc_fence_after();
+#pragma unroll 1
+            for (int m = 0; m < kPairs; ++m) {
+                if (leader) {
+                    const uint32_t d = tmem + Geo::kOCol + m * NH, a = vlo + vp.at * (kPair >> 4);
+#pragma unroll
+                    for (int k = 0; k < kTok / 16; ++k) {
+                        const uint64_t ad = desc64(a + k * (2048 >> 4), kHi), bd = desc64(plo + 2 * k, kHi);
+                        if (k == 0 && pend_first)
+                            mma_ss<false>(d, ad, bd, kIdPV);
+                        else
+                            mma_ss<true>(d, ad, bd, kIdPV);
+                    }
+                    tc_commit(&pair_empty[vp.at]);
+                }
+                __syncwarp();
+                vp.step();
+            }
+            if (leader)
+                tc_commit(&pv_done);
+            __syncwarp();
+            ++pvs;
+            if (pend_first)
+                ++pv_pieces;
+            pend = false;
+        };
+        auto pv_ready = [&] {
+            return ready(&p_full, pvs & 1) && (!pend_first || pv_pieces == 0 || ready(&o_free, (pv_pieces - 1) & 1));
+        };
+        for (;;) {
+            const LatentPiece piece = walk.next(p);
+            if (piece.s < 0 || !ok)
+                break;
+            if (piece.len == 0)
+                continue;
+            for (int j = piece.first; j < piece.last && ok; ++j) {
+                const uint32_t d = tmem + (tiles & 1) * NH;
+                int u = 0;  // pieces of the scores issued: the rotated part, then the pairs
+                uint64_t t0 = 0;
+                while (u <= kPairs || pend) {
+                    if (pend && pv_ready()) {
+                        issue_pv();
+                        t0 = 0;
+                    } else if (u <= kPairs &&
+                               (u == 0 ? (j > piece.first || ready(&q_full, pieces & 1)) &&
+                                             ready(&rope_full[rope.at], rope.par)
+                                       : ready(&pair_full[kp.at], kp.par))) {
+                        if (u == 0) {
+                            if (leader) {
+                                scores(d, rlo + rope.at * (kChunk >> 4), qlo + R / 64 * (NH * 128 >> 4), true);
+                                tc_commit(&rope_empty[rope.at]);
+                            }
+                            rope.step();
+                        } else {
+                            if (leader) {
+                                const uint32_t a = klo + kp.at * (kPair >> 4);
+                                const uint32_t b = qlo + 2 * (u - 1) * (NH * 128 >> 4);
+                                scores(d, a, b, false);
+                                scores(d, a + (kChunk >> 4), b + (NH * 128 >> 4), false);
+                                if (u == kPairs) {
+                                    tc_commit(&s_full[tiles & 1]);
+                                    if (j + 1 == piece.last)
+                                        tc_commit(&q_empty);
+                                }
+                            }
+                            kp.step();
+                        }
+                        __syncwarp();
+                        ++u;
+                        t0 = 0;
+                    } else {
+                        const uint64_t now = globaltimer_ns();
+                        if (t0 == 0)
+                            t0 = now;
+                        ok = __all_sync(kFullMask, !*abort && now - t0 <= kWaitLimitNs);
+                        if (!ok)
+                            break;
+                    }
+                }
+                if (!ok)
+                    break;
+                pend = true;
+                pend_first = j == piece.first;
+                ++tiles;
+            }
+            ++pieces;
+        }
+        if (ok && pend) {
+            ok = warp_wait(&p_full, pvs & 1, abort);
+            if (ok && pend_first && pv_pieces > 0)
+                ok = warp_wait(&o_free, (pv_pieces - 1) & 1, abort);
+            if (ok)
+                issue_pv();
+        }
+        if (!ok && lane == 0) {
+            set_status(p.status, PKV_ERR_TIMEOUT);
+            *abort = 1;
+        }
+        // Every MMA issued has completed before TMEM is freed.
+        if (leader) {
+            tc_commit(&drain);
+            mbar_wait_bounded(&drain, 0, kWaitLimitNs);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------- softmax
+        const int g = warp >> 2, quad = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+        const uint32_t ocol = tmem + lanes + Geo::kOCol + g * kHalfCols;
+        const float c = p.score_scale;  // positive
+        constexpr float kLazy = MmaSoftmax::kLazy;
+        const int tok0 = 16 * quad + (lane >> 2);  // this thread's tokens: tok0 and tok0 + 8
+        // Where this lane's row of a weights matrix goes: head, then 8 tokens.
+        const int m_head = g * kHalfCols + 8 * (lane >> 4) + (lane & 7), m_piece = 2 * quad + ((lane >> 3) & 1);
+        const uint32_t p_addr = smem0 + kPOff + m_head * 128 + ((m_piece ^ (m_head & 7)) << 4);
+        uint32_t cnt = 0;  // tiles
+        int2 cut = make_int2(-1, -1);
+        bool failed = false, gone = false;
+        for (;;) {
+            const LatentPiece piece = walk.next(p);
+            if (piece.s < 0)
+                break;
+            if (piece.first > 0)
+                cut.x = piece.s;
+            if (piece.last < piece.tiles)
+                cut.y = piece.s;
+            const int heads = min(NH, p.num_heads - h0);
+            if (piece.len == 0) {
+                const size_t at = (static_cast<size_t>(piece.s) * p.num_heads + h0) * R;
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at);
+                for (int e = threadIdx.x; e < heads * R / 8; e += 32 * kSoftWarps)
+                    dst[e] = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            float m[2 * J], l[2 * J];  // reference and partial sum of columns 8j + 2 (lane % 4) + e
+#pragma unroll
+            for (int i = 0; i < 2 * J; ++i) {
+                m[i] = -INFINITY;
+                l[i] = 0.f;
+            }
+            for (int j = piece.first; j < piece.last; ++j, ++cnt) {
+                failed = !warp_wait(&s_full[cnt & 1], (cnt >> 1) & 1, abort) || failed;
+                tc_fence_after();
+                float x[4 * J];
+                tmem_ld_rows<J>(tmem + lanes + (cnt & 1) * NH + g * kHalfCols, x);
+                const int valid = piece.len - j * kTok;  // tokens of the tile
+                const bool tail = valid < kTok;
+                if (tail) {
+#pragma unroll
+                    for (int i = 0; i < 4 * J; ++i)
+                        if (tok0 + (i & 2 ? 8 : 0) >= valid)
+                            x[i] = -INFINITY;
+                }
+                bool need = false;
+                float mx[2 * J];
+#pragma unroll
+                for (int i = 0; i < 2 * J; ++i) {
+                    const int r = 4 * (i >> 1) + (i & 1);
+                    mx[i] = fmaxf(x[r], x[r + 2]) * c;
+                    need = need || mx[i] > m[i] + kLazy;
+                }
+                if (failed && lane == 0)
+                    s_failed[g][cnt & 1] = 1;
+                need = half_any(g, need);
+                gone = *reinterpret_cast<volatile int *>(&s_failed[g][cnt & 1]) != 0;
+                if (gone)
+                    break;
+                if (need) {
+                    // Maxima over the tile's tokens, of every head of this half.
+#pragma unroll
+                    for (int i = 0; i < 2 * J; ++i) {
+#pragma unroll
+                        for (int w = 4; w <= 16; w <<= 1)
+                            mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFullMask, mx[i], w));
+                        if (lane < 4)
+                            s_red[g][quad][8 * (i >> 1) + 2 * lane + (i & 1)] = mx[i];
+                    }
+                    half_sync(g);
+                    float alpha[2 * J];
+#pragma unroll
+                    for (int i = 0; i < 2 * J; ++i) {
+                        const int col = 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+                        const float top = fmaxf(fmaxf(s_red[g][0][col], s_red[g][1][col]),
+                                                fmaxf(s_red[g][2][col], s_red[g][3][col]));
+                        const float up = fmaxf(m[i], top);
+                        alpha[i] = up == m[i] ? 1.f : ex2(m[i] - up);
+                        m[i] = up;
+                        l[i] *= alpha[i];
+                        if (quad == 0 && lane < 4)
+                            s_col[g * kHalfCols + col] = alpha[i];
+                    }
+                    half_sync(g);
+                    if (j > piece.first) {
+                        // O^T holds earlier tiles: all their products are done.
+                        failed = !warp_wait(&pv_done, (cnt - 1) & 1, abort) || failed;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int t = 0; t < kPairs; ++t)
+#pragma unroll
+                            for (int c0 = 0; c0 < kHalfCols; c0 += 8) {
+                                float o[8];
+                                tmem_ld8(ocol + t * NH + c0, o);
+                                const float4 a = *reinterpret_cast<const float4 *>(&s_col[g * kHalfCols + c0]);
+                                const float4 b = *reinterpret_cast<const float4 *>(&s_col[g * kHalfCols + c0 + 4]);
+                                o[0] *= a.x;
+                                o[1] *= a.y;
+                                o[2] *= a.z;
+                                o[3] *= a.w;
+                                o[4] *= b.x;
+                                o[5] *= b.y;
+                                o[6] *= b.z;
+                                o[7] *= b.w;
+                                tmem_st8(ocol + t * NH + c0, o);
+                            }
+                        tmem_wait_st();
+                    }
+                }
+                // Weights 2^(c x - m); a head of nothing but -inf so far has weights 0.
+                uint32_t w[2 * J];
+#pragma unroll
+                for (int i = 0; i < 2 * J; i += 2) {
+                    const float o0 = m[i] == -INFINITY ? 0.f : -m[i], o1 = m[i + 1] == -INFINITY ? 0.f : -m[i + 1];
+                    const float a0 = ex2(fmaf(x[2 * i], c, o0)), a1 = ex2(fmaf(x[2 * i + 1], c, o1));
+                    const float b0 = ex2(fmaf(x[2 * i + 2], c, o0)), b1 = ex2(fmaf(x[2 * i + 3], c, o1));
+                    l[i] += a0 + b0;
+                    l[i + 1] += a1 + b1;
+                    w[i] = pack_bf16(a0, a1);
+                    w[i + 1] = pack_bf16(b0, b1);
+                }
+                // The last tile's products with P are done: P may be written.
+                if (cnt > 0)
+                    failed = !warp_wait(&pv_done, (cnt - 1) & 1, abort) || failed;
+                if constexpr (J == 1) {
+                    stsm_t2(p_addr, w[0], w[1]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2 * J; i += 4)
+                        stsm_t4(p_addr + 8 * (i / 2) * 128, w[i], w[i + 1], w[i + 2], w[i + 3]);
+                }
+                if (tail) {
+                    // Rows past the end may hold anything.
+                    const int rows = kTok - valid;
+                    for (int e = threadIdx.x; e < rows * kPairs * 16; e += 32 * kSoftWarps) {
+                        const int row = valid + e % rows, piece16 = e / rows % 8, chunk = e / rows / 8;
+                        const uint32_t n = cnt * kPairs + (chunk >> 1);
+                        *reinterpret_cast<uint4 *>(smem + kPairOff + (n % NP) * kPair + (chunk & 1) * kChunk + row * 128 +
+                                                   piece16 * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_proxy_async();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&p_full);
+            }
+            if (gone)
+                break;
+            // Sums of the heads' weights.
+#pragma unroll
+            for (int i = 0; i < 2 * J; ++i) {
+#pragma unroll
+                for (int w = 4; w <= 16; w <<= 1)
+                    l[i] += __shfl_xor_sync(kFullMask, l[i], w);
+                if (lane < 4)
+                    s_red[g][quad][8 * (i >> 1) + 2 * lane + (i & 1)] = l[i];
+            }
+            half_sync(g);
+            const bool whole = piece.whole();
+            const size_t slot = (static_cast<size_t>(latent_slot(team, piece)) * p.head_tiles + ht) * NH;
+            if (quad == 0 && lane < 4) {
+#pragma unroll
+                for (int i = 0; i < 2 * J; ++i) {
+                    const int col = 8 * (i >> 1) + 2 * lane + (i & 1), h = g * kHalfCols + col;
+                    const float sum = s_red[g][0][col] + s_red[g][1][col] + s_red[g][2][col] + s_red[g][3][col];
+                    s_col[h] = whole ? 1.f / sum : 1.f;
+                    if (!whole && h < heads)
+                        p.part_ml[slot + h] = make_float2(m[i], sum);
+                }
+            }
+            half_sync(g);
+            failed = !warp_wait(&pv_done, (cnt - 1) & 1, abort) || failed;
+            tc_fence_after();
+#pragma unroll 1
+            for (int t = 0; t < kPairs; ++t) {
+                const int d = 128 * t + 32 * quad + lane;
+#pragma unroll
+                for (int c0 = 0; c0 < kHalfCols; c0 += 8) {
+                    float o[8];
+                    tmem_ld8(ocol + t * NH + c0, o);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int h = g * kHalfCols + c0 + e;
+                        if (h >= heads)
+                            break;
+                        if (whole)
+                            static_cast<__nv_bfloat16 *>(
+                                p.out)[(static_cast<size_t>(piece.s) * p.num_heads + h0 + h) * R + d] =
+                                __float2bfloat16(o[e] * s_col[h]);
+                        else
+                            p.part[(slot + h) * R + d] = o[e];
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&o_free);
+        }
+        if ((failed || gone) && lane == 0) {
+            set_status(p.status, PKV_ERR_TIMEOUT);
+            *abort = 1;
+        }
+        if (threadIdx.x == 0 && ht == 0)
+            p.pieces[team] = cut;
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Geo::kAlloc)
+                     : "memory");
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+// [outer][rows][numbers] bf16, dense: boxes of 64 numbers x `box_rows` rows in the
+// 128-byte swizzle mode; zeros past the edges.
+bool encode_rows(EncodeTiledFn enc, CUtensorMap *map, const void *base, int numbers, int rows, int64_t outer,
+                 int box_rows)
+{
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(numbers), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(outer)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(numbers) * 2, static_cast<cuuint64_t>(numbers) * 2 * rows};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int R, int NH> pkv_status launch_tc(const LatentDecodeParams &p, cudaStream_t stream)
+{
+    static ContextCache cache;
+    int set = 0;
+    const pkv_status rc = cache.get(&set, [](int *out) -> pkv_status {
+        *out = 1;
+        return cudaFuncSetAttribute(latent_tc_kernel<R, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    LtGeom<R, NH>::kSmem) == cudaSuccess
+                   ? PKV_OK
+                   : PKV_ERR_CUDA;
+    });
+    if (rc != PKV_OK)
+        return rc;
+    EncodeTiledFn enc = encoder();
+    if (!enc)
+        return PKV_ERR_UNSUPPORTED;
+    LatentMaps maps;
+    if (!encode_rows(enc, &maps.q, p.q, R + kRopeDim, p.num_heads, p.num_seqs, NH) ||
+        !encode_rows(enc, &maps.rows, p.cache, R + kRopeDim, kBlockSize, p.num_blocks, kBlockSize))
+        return PKV_ERR_INVALID_ARG;
+    latent_tc_kernel<R, NH><<<p.teams * p.head_tiles, kThreads, LtGeom<R, NH>::kSmem, stream>>>(p, maps);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+template <int R> pkv_status launch_tc_r(const LatentDecodeParams &p, cudaStream_t stream)
+{
+    return p.tile_heads == 16 ? launch_tc<R, 16>(p, stream)
+                              : p.tile_heads == 32 ? launch_tc<R, 32>(p, stream) : launch_tc<R, 64>(p, stream);
+}
+
+}  // namespace
+
+pkv_status launch_latent_decode_tc(const LatentDecodeParams &p, cudaStream_t stream)
+{
+    return p.latent_dim == 512 ? launch_tc_r<512>(p, stream) : launch_tc_r<256>(p, stream);
+}
+
+}  // namespace pkv
