@@ -66,6 +66,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const Late
     const int heads = min(kSimtHeads, p.num_heads - h0);
     const float c = p.negate ? -p.score_scale : p.score_scale;
 
+    // The kernel that joins cut sequences may be set up; it waits for this one's end.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     LatentWalk walk;
     if (warp == 0)
         walk.init(p, team, lane, blockIdx.x == 0);
@@ -257,20 +259,41 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const Late
 
 constexpr int kMergeWarps = 8;
 
-// Block (team - 1, heads): joins the sequence that the start of `team` cuts, if it
-// begins in the team before.  A warp has one head:
+// Joins the pieces of cut sequences.  blockIdx.x is a sequence (fewer sequences than
+// teams) or a team but the first, which stands for the sequence that its start cuts if
+// that begins in the team before.  A warp has 128 dims of one head:
 //   M = max_i m_i,  out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i
-// over the pieces i in order, so the result does not depend on who wrote first.
+// over the pieces i in order, so the result does not depend on who wrote first.  With a
+// whole head to a warp there were too few loads under way when few sequences have many
+// pieces.
 template <typename T, int R>
-__global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const LatentDecodeParams p)
+__global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const LatentDecodeParams p, int by_sequence)
 {
-    const int lane = threadIdx.x & 31, team = blockIdx.x + 1;
-    const int h = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-    const int s = p.pieces[team].x;
-    // The piece before starts the sequence if nothing before that one belongs to it.
-    if (s < 0 || h >= p.num_heads || p.pieces[team - 1].y != s || p.pieces[team - 1].x == s)
+    constexpr int kParts = R / 128;
+    const int lane = threadIdx.x & 31;
+    const int unit = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+    const int h = unit / kParts, d = unit % kParts * 128 + 4 * lane;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (h >= p.num_heads)
         return;
-    const int ht = h / p.tile_heads, hh = h % p.tile_heads;
+    int s, team;  // the first team that goes on with s
+    if (by_sequence) {
+        s = blockIdx.x;
+        team = p.teams;
+        for (int t = 0; t < p.teams && team == p.teams; t += 32) {
+            const unsigned same = __ballot_sync(kFullMask, t + lane < p.teams && p.pieces[t + lane].x == s);
+            if (same)
+                team = t + __ffs(same) - 1;
+        }
+        if (team == p.teams)
+            return;
+    } else {
+        team = blockIdx.x + 1;
+        s = p.pieces[team].x;
+        // The piece before starts the sequence if nothing before that one belongs to it.
+        if (s < 0 || p.pieces[team - 1].x == s)
+            return;
+    }
     int last = team;  // the last team with a piece
     for (int t = team; t < p.teams; t += 32) {
         const unsigned same = __ballot_sync(kFullMask, t + lane < p.teams && p.pieces[t + lane].x == s);
@@ -278,6 +301,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const La
         if (same != kFullMask)
             break;
     }
+    const int ht = h / p.tile_heads, hh = h % p.tile_heads;
     auto row = [&](int t) {  // t = team - 1: the piece the sequence starts with
         const size_t slot = t < team ? 2 * t + 1 : 2 * t;
         return (slot * p.head_tiles + ht) * p.tile_heads + hh;
@@ -288,34 +312,26 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const La
 #pragma unroll
     for (int w = 16; w >= 1; w >>= 1)
         top = fmaxf(top, __shfl_xor_sync(kFullMask, top, w));
-    constexpr int kVecs = R / 128;
-    float4 sum[kVecs] = {};
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     float total = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int t = team - 1; t <= last; ++t) {
         const float2 ml = p.part_ml[row(t)];
+        const float4 x = *reinterpret_cast<const float4 *>(p.part + row(t) * R + d);
         const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
         total = fmaf(w, ml.y, total);
-        const float4 *src = reinterpret_cast<const float4 *>(p.part + row(t) * R);
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const float4 x = src[32 * i + lane];
-            sum[i].x = fmaf(w, x.x, sum[i].x);
-            sum[i].y = fmaf(w, x.y, sum[i].y);
-            sum[i].z = fmaf(w, x.z, sum[i].z);
-            sum[i].w = fmaf(w, x.w, sum[i].w);
-        }
+        sum.x = fmaf(w, x.x, sum.x);
+        sum.y = fmaf(w, x.y, sum.y);
+        sum.z = fmaf(w, x.z, sum.z);
+        sum.w = fmaf(w, x.w, sum.w);
     }
-    const size_t at = (static_cast<size_t>(s) * p.num_heads + h) * R;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        const float4 y = make_float4(sum[i].x / total, sum[i].y / total, sum[i].z / total, sum[i].w / total);
-        if constexpr (sizeof(T) == 4)
-            reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at)[32 * i + lane] = y;
-        else
-            reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at)[32 * i + lane] =
-                make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
-    }
+    const size_t at = (static_cast<size_t>(s) * p.num_heads + h) * R + d;
+    const float4 y = make_float4(sum.x / total, sum.y / total, sum.z / total, sum.w / total);
+    if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = y;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
+            make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
 }
 
 template <int R> pkv_status launch_simt(const LatentDecodeParams &p, cudaStream_t stream)
@@ -337,9 +353,20 @@ template <int R> pkv_status launch_simt(const LatentDecodeParams &p, cudaStream_
 
 template <typename T, int R> pkv_status launch_merge(const LatentDecodeParams &p, cudaStream_t stream)
 {
-    const dim3 grid(p.teams - 1, (p.num_heads + kMergeWarps - 1) / kMergeWarps);
-    latent_merge_kernel<T, R><<<grid, 32 * kMergeWarps, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    const int by_sequence = p.num_seqs < p.teams;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(by_sequence ? p.num_seqs : p.teams - 1,
+                          (p.num_heads * (R / 128) + kMergeWarps - 1) / kMergeWarps);
+    config.blockDim = dim3(32 * kMergeWarps);
+    config.stream = stream;
+    // Set up while the attention kernel runs.
+    cudaLaunchAttribute early = {};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    config.attrs = &early;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, latent_merge_kernel<T, R>, p, by_sequence) == cudaSuccess ? PKV_OK
+                                                                                                 : PKV_ERR_CUDA;
 }
 
 }  // namespace

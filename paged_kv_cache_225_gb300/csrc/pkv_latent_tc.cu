@@ -142,6 +142,27 @@ __device__ __forceinline__ void stsm_t2(uint32_t addr, uint32_t a, uint32_t b)
                  : "memory");
 }
 
+// Hands the warp's part of O^T, `mine` columns of each of kTiles tiles NH columns apart,
+// to put(tile, column, value of this lane's dim).
+template <int kTiles, int NH, int kCols, typename Put>
+__device__ __forceinline__ void store_heads(uint32_t col, int mine, Put put)
+{
+#pragma unroll 1
+    for (int t = 0; t < kTiles; ++t) {
+#pragma unroll
+        for (int c0 = 0; c0 < kCols; c0 += 8) {
+            if (c0 >= mine)
+                break;
+            float o[8];
+            tmem_ld8(col + t * NH + c0, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c0 + e < mine)
+                    put(t, c0 + e, o[e]);
+        }
+    }
+}
+
 // Barrier of the four softmax warps of half g; the second form also ORs a predicate.
 __device__ __forceinline__ void half_sync(int g)
 {
@@ -259,6 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // The kernel that joins cut sequences may be set up; it waits for this one's end.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = s_tmem;
     LatentWalk walk = s_walk;
 
@@ -354,7 +377,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;  // 8-row groups 1 KB apart, 128-byte swizzle
         const uint32_t id_s = tc_idesc(kTok, NH, false) | (p.negate ? 1u << 13 : 0u);
         constexpr uint32_t kIdPV = tc_idesc(128, NH, false) | 1u << 15;  // A is M-major
-        const bool leader = elect_one();
         const uint32_t qlo = (smem0 >> 4) | 1u << 16, plo = ((smem0 + kPOff) >> 4) | 1u << 16;
         const uint32_t rlo = ((smem0 + kRopeOff) >> 4) | 1u << 16, klo = ((smem0 + kPairOff) >> 4) | 1u << 16;
         const uint32_t vlo = ((smem0 + kPairOff) >> 4) | (kChunk >> 4) << 16;  // 64-dim halves one chunk apart
@@ -379,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
 #pragma unroll 1
             for (int m = 0; m < kPairs; ++m) {
-                if (leader) {
+                if (elect_one()) {
                     const uint32_t d = tmem + Geo::kOCol + m * NH, a = vlo + vp.at * (kPair >> 4);
 #pragma unroll
                     for (int k = 0; k < kTok / 16; ++k) {
@@ -394,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 vp.step();
             }
-            if (leader)
+            if (elect_one())
                 tc_commit(&pv_done);
             __syncwarp();
             ++pvs;
@@ -424,13 +446,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ready(&rope_full[rope.at], rope.par)
                                        : ready(&pair_full[kp.at], kp.par))) {
                         if (u == 0) {
-                            if (leader) {
+                            if (elect_one()) {
                                 scores(d, rlo + rope.at * (kChunk >> 4), qlo + R / 64 * (NH * 128 >> 4), true);
                                 tc_commit(&rope_empty[rope.at]);
                             }
                             rope.step();
                         } else {
-                            if (leader) {
+                            if (elect_one()) {
                                 const uint32_t a = klo + kp.at * (kPair >> 4);
                                 const uint32_t b = qlo + 2 * (u - 1) * (NH * 128 >> 4);
                                 scores(d, a, b, false);
@@ -475,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             *abort = 1;
         }
         // Every MMA issued has completed before TMEM is freed.
-        if (leader) {
+        if (elect_one()) {
             tc_commit(&drain);
             mbar_wait_bounded(&drain, 0, kWaitLimitNs);
         }
@@ -658,26 +680,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             half_sync(g);
             failed = !warp_wait(&pv_done, (cnt - 1) & 1, abort) || failed;
             tc_fence_after();
-#pragma unroll 1
-            for (int t = 0; t < kPairs; ++t) {
-                const int d = 128 * t + 32 * quad + lane;
-#pragma unroll
-                for (int c0 = 0; c0 < kHalfCols; c0 += 8) {
-                    float o[8];
-                    tmem_ld8(ocol + t * NH + c0, o);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int h = g * kHalfCols + c0 + e;
-                        if (h >= heads)
-                            break;
-                        if (whole)
-                            static_cast<__nv_bfloat16 *>(
-                                p.out)[(static_cast<size_t>(piece.s) * p.num_heads + h0 + h) * R + d] =
-                                __float2bfloat16(o[e] * s_col[h]);
-                        else
-                            p.part[(slot + h) * R + d] = o[e];
-                    }
-                }
+            {
+                const int d = 32 * quad + lane, h = g * kHalfCols;
+                const int mine = min(kHalfCols, heads - h);
+                const float *f = s_col + h;
+                if (whole)
+                    store_heads<kPairs, NH, kHalfCols>(ocol, mine, [&](int t, int e, float x) {
+                        static_cast<__nv_bfloat16 *>(p.out)[(static_cast<size_t>(piece.s) * p.num_heads + h0 + h + e) * R +
+                                                            128 * t + d] = __float2bfloat16(x * f[e]);
+                    });
+                else
+                    store_heads<kPairs, NH, kHalfCols>(ocol, mine, [&](int t, int e, float x) {
+                        p.part[(slot + h + e) * R + 128 * t + d] = x;
+                    });
             }
             tc_fence_before();
             __syncwarp();
