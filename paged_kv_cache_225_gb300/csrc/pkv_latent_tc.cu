@@ -12,14 +12,13 @@
 //    shared-memory copy of a row (64 tokens x 64 dims, 128-byte swizzle) is the
 //    K-major operand of the one and the M-major operand of the other.
 //  * A CTA (one per SM) has up to 64 heads and walks a range of tiles of 64 tokens
-//    (pkv_latent.cuh).  Warp 8 issues the TMA loads (a box per page and 64 dims),
-//    warp 9 the MMAs, warps 0-7 compute the softmax, four for each half of the heads.
+//    (pkv_latent.cuh).  Warps 0-7 compute the softmax, four for each half of the heads;
+//    warps 8 and 9 issue the TMA loads (a box per page and 64 dims).
 //  * TMEM: two buffers of S^T, and O^T.  P^T goes through shared memory.
 //  * The rings hold the rotated part of a tile (8 KB) and pairs of 64 dims (16 KB)
 //    on their own: the scores start with the first that lands, and a pair's slot is
 //    filled again when its part of O^T is done.
-//  * The MMA warp takes whichever is ready: P V of a tile, which frees the ring, or
-//    the next piece of the scores of the tile after it.
+//  * A warp issues the scores' MMAs, another those of P V, which free the ring.
 //  * The reference of a head's weights is raised only when a score exceeds it by 2^8;
 //    O^T is then rescaled in TMEM.  All weights of a head and tile share it, so the
 //    four warps of a half agree through a barrier.
@@ -37,10 +36,12 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;
-constexpr int kProducerWarp = 8;
-constexpr int kMmaWarp = 9;
+constexpr int kProducerWarp = 8;  // and 9
+constexpr int kProducers = 2;
+constexpr int kScoreWarp = 10;
+constexpr int kValueWarp = 11;
 constexpr int kTok = kLatentTokens;
 constexpr int kChunk = kTok * 128;  // bytes of 64 tokens x 64 dims
 constexpr int kPair = 2 * kChunk;
@@ -64,20 +65,58 @@ struct LatentMaps {
     CUtensorMap q, rows;
 };
 
-__device__ __forceinline__ bool elect_one()
+// Four MMAs D (+)= A B whose operands, both in shared memory, are kA and kB (descriptor
+// units of 16 bytes) apart; the first one overwrites D unless `accumulate`.  All lanes
+// run it and one issues: with the election inside, the operands stay uniform, and the
+// warp issues an MMA in 24 cycles where a branch around it took 40, a branch on the
+// lane's number 64.
+template <int kA, int kB>
+__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
 {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "setp.ne.b32 q, %4, 0;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t"
+        "add.u64 x, %1, %5;\n\tadd.u64 y, %2, %6;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, 1;\n\t"
+        "add.u64 x, x, %5;\n\tadd.u64 y, y, %6;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, 1;\n\t"
+        "add.u64 x, x, %5;\n\tadd.u64 y, y, %6;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, 1;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kA), "n"(kB)
+        : "memory");
+}
+// Arrives on bar once every MMA that the elected lane issued before has completed.
+__device__ __forceinline__ void commit_elected(uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void expect_elected(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+        "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "r"(bytes)
+        : "memory");
+}
+__device__ __forceinline__ void load_elected(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+        "@p cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
 }
 
-// D (+)= A B, both from shared memory.
-template <bool kAccumulate> __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc)
-{
-    asm volatile("tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, %4;" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-                 "n"(kAccumulate ? 1 : 0));
-}
-
+// Descriptor of a 128-byte-swizzled operand.  Low word: address / 16, and from bit 16 the
+// distance / 16 of 64-element halves (M-major only).  High word: 8-row groups 1 KB apart,
+// descriptor version 1 (bit 14), layout code 2 (bit 29).
+constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) { return static_cast<uint64_t>(hi) << 32 | lo; }
 
 // 16 lanes x 8 J columns of f32 as fragments: registers 4j, 4j + 1 of a thread are row
@@ -187,20 +226,6 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// Whether a phase is over, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // A ring's position: slot and parity of its phase.
 template <int N> struct Ring {
     uint32_t at = 0, par = 0;
@@ -223,13 +248,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kHalfCols = NH / 2;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t rope_full[NR], rope_empty[NR], pair_full[NP], pair_empty[NP];
-    __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full, pv_done, o_free, drain;
+    __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], s_free[2], p_full, pv_done, o_free,
+        drain[2];
     __shared__ __align__(16) float s_red[2][4][32];  // per half and warp: maxima or sums of its heads
     __shared__ __align__(16) float s_col[NH];        // per head: a factor of its column of O^T
     __shared__ LatentWalk s_walk;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort, s_failed[2][2];
+    __shared__ int s_abort, s_never, s_failed[2][2];
     volatile int *abort = &s_abort;
+    const volatile int &no_abort = s_never;  // for what has to end before the CTA may
 
     const int warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0);
     const int lane = threadIdx.x & 31;
@@ -242,22 +269,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NR; ++i) {
-            mbar_init(&rope_full[i], 1);
+            mbar_init(&rope_full[i], kProducers);
             mbar_init(&rope_empty[i], 1);
         }
         for (int i = 0; i < NP; ++i) {
-            mbar_init(&pair_full[i], 1);
+            mbar_init(&pair_full[i], kProducers);
             mbar_init(&pair_empty[i], 1);
         }
         mbar_init(&q_full, 1);
         mbar_init(&q_empty, 1);
-        mbar_init(&s_full[0], 1);
-        mbar_init(&s_full[1], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_free[i], kSoftWarps);
+            mbar_init(&drain[i], 1);
+        }
         mbar_init(&p_full, kSoftWarps);
         mbar_init(&pv_done, 1);
         mbar_init(&o_free, kSoftWarps);
-        mbar_init(&drain, 1);
-        s_abort = 0;
+        s_abort = s_never = 0;
         s_failed[0][0] = s_failed[0][1] = s_failed[1][0] = s_failed[1][1] = 0;
         fence_mbar_init();
     }
@@ -271,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0)
             s_walk = walk;
     }
-    if (warp == kMmaWarp) {
+    if (warp == kValueWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
                      "r"(Geo::kAlloc)
                      : "memory");
@@ -285,8 +314,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = s_tmem;
     LatentWalk walk = s_walk;
 
-    if (warp == kProducerWarp) {
+    if (warp == kProducerWarp || warp == kProducerWarp + 1) {
         // ------------------------------------------------------- copies
+        // Two warps, two pages of a tile each: one alone takes 2800 cycles for the 36 boxes
+        // of a tile (R = 512), the tensor cores 1900.
+        const int half = warp - kProducerWarp;
         Ring<NR> rope;
         Ring<NP> pair;
         uint32_t ropes = 0, pairs = 0, pieces = 0;
@@ -297,14 +329,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             if (piece.len == 0)
                 continue;
-            if (pieces > 0)
-                ok = warp_wait(&q_empty, (pieces - 1) & 1, abort);
-            if (!ok)
-                break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&q_full, Geo::kQ);
+            if (half == 0) {
+                if (pieces > 0)
+                    ok = warp_wait(&q_empty, (pieces - 1) & 1, abort);
+                if (!ok)
+                    break;
+                expect_elected(&q_full, Geo::kQ);
+#pragma unroll 1
                 for (int c = 0; c <= R / 64; ++c)
-                    tma_load_3d(smem + c * NH * 128, &maps.q, 64 * c, h0, piece.s, &q_full);
+                    load_elected(smem0 + c * NH * 128, &maps.q, 64 * c, h0, piece.s, &q_full);
             }
             ++pieces;
             const int32_t *table = p.block_tables + static_cast<size_t>(piece.s) * p.max_blocks;
@@ -325,32 +358,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     next_ids = j + 8 < piece.last ? ids_at(j + 8) : 0;
                 }
-                const int there = min(kPages, pages - j * kPages);
-                const int page = lane & 3;
-                const int id = __shfl_sync(kFullMask, ids, in8 * kPages + page);
+                const int there = max(0, min(2, pages - j * kPages - 2 * half));
+                const int id0 = __shfl_sync(kFullMask, ids, in8 * kPages + 2 * half);
+                const int id1 = __shfl_sync(kFullMask, ids, in8 * kPages + 2 * half + 1);
                 ok = warp_wait(&rope_empty[rope.at], rope.par ^ 1, abort);
                 if (!ok)
                     break;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&rope_full[rope.at], there * 2048);
-                __syncwarp();
-                if (lane < there && !(p.drop_first_copy && blockIdx.x == 0 && ropes == 0 && lane == 0))
-                    tma_load_3d(smem + kRopeOff + rope.at * kChunk + page * 2048, &maps.rows, R, 0, id,
-                                &rope_full[rope.at]);
-                __syncwarp();
+                {
+                    uint64_t *bar = &rope_full[rope.at];
+                    const uint32_t dst = smem0 + kRopeOff + rope.at * kChunk + half * 4096;
+                    expect_elected(bar, there * 2048);
+                    if (there > 0 && !(p.drop_first_copy && blockIdx.x == 0 && ropes == 0 && half == 0))
+                        load_elected(dst, &maps.rows, R, 0, id0, bar);
+                    if (there > 1)
+                        load_elected(dst + 2048, &maps.rows, R, 0, id1, bar);
+                }
                 rope.step();
                 ++ropes;
+#pragma unroll 1
                 for (int m = 0; m < kPairs; ++m) {
                     ok = warp_wait(&pair_empty[pair.at], pair.par ^ 1, abort);
                     if (!ok)
                         break;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(&pair_full[pair.at], 2 * there * 2048);
-                    __syncwarp();
-                    if (lane < 8 && page < there)
-                        tma_load_3d(smem + kPairOff + pair.at * kPair + (lane >> 2) * kChunk + page * 2048,
-                                    &maps.rows, 128 * m + 64 * (lane >> 2), 0, id, &pair_full[pair.at]);
-                    __syncwarp();
+                    uint64_t *bar = &pair_full[pair.at];
+                    const uint32_t dst = smem0 + kPairOff + pair.at * kPair + half * 4096;
+                    expect_elected(bar, there * 4096);
+                    if (there > 0) {
+                        load_elected(dst, &maps.rows, 128 * m, 0, id0, bar);
+                        load_elected(dst + kChunk, &maps.rows, 128 * m + 64, 0, id0, bar);
+                    }
+                    if (there > 1) {
+                        load_elected(dst + 2048, &maps.rows, 128 * m, 0, id1, bar);
+                        load_elected(dst + kChunk + 2048, &maps.rows, 128 * m + 64, 0, id1, bar);
+                    }
                     pair.step();
                     ++pairs;
                 }
@@ -365,143 +405,111 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Every copy still in flight lands before the CTA exits.
         if (lane == 0) {
             for (uint32_t c = ropes > NR ? ropes - NR : 0; c < ropes; ++c)
-                mbar_wait_bounded(&rope_full[c % NR], (c / NR) & 1, kWaitLimitNs);
+                tc_wait(&rope_full[c % NR], (c / NR) & 1, &no_abort);
             for (uint32_t c = pairs > NP ? pairs - NP : 0; c < pairs; ++c)
-                mbar_wait_bounded(&pair_full[c % NP], (c / NP) & 1, kWaitLimitNs);
-            if (pieces > 0)
-                mbar_wait_bounded(&q_full, (pieces - 1) & 1, kWaitLimitNs);
+                tc_wait(&pair_full[c % NP], (c / NP) & 1, &no_abort);
+            if (pieces > 0 && half == 0)
+                tc_wait(&q_full, (pieces - 1) & 1, &no_abort);
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------- MMA issue
-        constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;  // 8-row groups 1 KB apart, 128-byte swizzle
+    } else if (warp == kScoreWarp) {
+        // ------------------------------------------------- MMA issue: scores
+        // A warp for the scores and one for P V, each with its own waits: one warp that
+        // took whichever was ready spent as long on looking as on issuing.
         const uint32_t id_s = tc_idesc(kTok, NH, false) | (p.negate ? 1u << 13 : 0u);
-        constexpr uint32_t kIdPV = tc_idesc(128, NH, false) | 1u << 15;  // A is M-major
-        const uint32_t qlo = (smem0 >> 4) | 1u << 16, plo = ((smem0 + kPOff) >> 4) | 1u << 16;
-        const uint32_t rlo = ((smem0 + kRopeOff) >> 4) | 1u << 16, klo = ((smem0 + kPairOff) >> 4) | 1u << 16;
-        const uint32_t vlo = ((smem0 + kPairOff) >> 4) | (kChunk >> 4) << 16;  // 64-dim halves one chunk apart
+        const uint64_t qd = desc64((smem0 >> 4) | 1u << 16, kHi);
+        const uint64_t rd = desc64(((smem0 + kRopeOff) >> 4) | 1u << 16, kHi);
+        const uint64_t kd = desc64(((smem0 + kPairOff) >> 4) | 1u << 16, kHi);
         Ring<NR> rope;
-        Ring<NP> kp, vp;                     // pairs as keys, as values
-        uint32_t tiles = 0, pieces = 0;      // scored
-        uint32_t pvs = 0, pv_pieces = 0;     // multiplied with P
-        bool pend = false, pend_first = false;
+        Ring<NP> pair;
+        uint32_t tiles = 0, pieces = 0;
         bool ok = true;
-        auto ready = [&](uint64_t *bar, uint32_t par) { return __all_sync(kFullMask, mbar_test(bar, par)); };
-        // 4 steps of 16 dims of 64 tokens' scores.
-        auto scores = [&](uint32_t d, uint32_t a, uint32_t b, bool first) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (first && k == 0)
-                    mma_ss<false>(d, desc64(a, kHi), desc64(b, kHi), id_s);
-                else
-                    mma_ss<true>(d, desc64(a + 2 * k, kHi), desc64(b + 2 * k, kHi), id_s);
-            }
-        };
-        auto issue_pv = [&] {
-            tc_fence_after();
-#pragma unroll 1
-            for (int m = 0; m < kPairs; ++m) {
-                if (elect_one()) {
-                    const uint32_t d = tmem + Geo::kOCol + m * NH, a = vlo + vp.at * (kPair >> 4);
-#pragma unroll
-                    for (int k = 0; k < kTok / 16; ++k) {
-                        const uint64_t ad = desc64(a + k * (2048 >> 4), kHi), bd = desc64(plo + 2 * k, kHi);
-                        if (k == 0 && pend_first)
-                            mma_ss<false>(d, ad, bd, kIdPV);
-                        else
-                            mma_ss<true>(d, ad, bd, kIdPV);
-                    }
-                    tc_commit(&pair_empty[vp.at]);
-                }
-                __syncwarp();
-                vp.step();
-            }
-            if (elect_one())
-                tc_commit(&pv_done);
-            __syncwarp();
-            ++pvs;
-            if (pend_first)
-                ++pv_pieces;
-            pend = false;
-        };
-        auto pv_ready = [&] {
-            return ready(&p_full, pvs & 1) && (!pend_first || pv_pieces == 0 || ready(&o_free, (pv_pieces - 1) & 1));
-        };
         for (;;) {
             const LatentPiece piece = walk.next(p);
             if (piece.s < 0 || !ok)
                 break;
             if (piece.len == 0)
                 continue;
+            ok = warp_wait(&q_full, pieces & 1, abort);
             for (int j = piece.first; j < piece.last && ok; ++j) {
                 const uint32_t d = tmem + (tiles & 1) * NH;
-                int u = 0;  // pieces of the scores issued: the rotated part, then the pairs
-                uint64_t t0 = 0;
-                while (u <= kPairs || pend) {
-                    if (pend && pv_ready()) {
-                        issue_pv();
-                        t0 = 0;
-                    } else if (u <= kPairs &&
-                               (u == 0 ? (j > piece.first || ready(&q_full, pieces & 1)) &&
-                                             ready(&rope_full[rope.at], rope.par)
-                                       : ready(&pair_full[kp.at], kp.par))) {
-                        if (u == 0) {
-                            if (elect_one()) {
-                                scores(d, rlo + rope.at * (kChunk >> 4), qlo + R / 64 * (NH * 128 >> 4), true);
-                                tc_commit(&rope_empty[rope.at]);
-                            }
-                            rope.step();
-                        } else {
-                            if (elect_one()) {
-                                const uint32_t a = klo + kp.at * (kPair >> 4);
-                                const uint32_t b = qlo + 2 * (u - 1) * (NH * 128 >> 4);
-                                scores(d, a, b, false);
-                                scores(d, a + (kChunk >> 4), b + (NH * 128 >> 4), false);
-                                if (u == kPairs) {
-                                    tc_commit(&s_full[tiles & 1]);
-                                    if (j + 1 == piece.last)
-                                        tc_commit(&q_empty);
-                                }
-                            }
-                            kp.step();
-                        }
-                        __syncwarp();
-                        ++u;
-                        t0 = 0;
-                    } else {
-                        const uint64_t now = globaltimer_ns();
-                        if (t0 == 0)
-                            t0 = now;
-                        ok = __all_sync(kFullMask, !*abort && now - t0 <= kWaitLimitNs);
-                        if (!ok)
-                            break;
-                    }
+                // The softmax has read the buffer's last scores.
+                if (tiles > 1)
+                    ok = warp_wait(&s_free[tiles & 1], ((tiles >> 1) - 1) & 1, abort);
+                ok = ok && warp_wait(&rope_full[rope.at], rope.par, abort);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                mma4<2, 2>(d, rd + rope.at * (kChunk >> 4), qd + R / 64 * (NH * 128 >> 4), id_s, false);
+                commit_elected(&rope_empty[rope.at]);
+                rope.step();
+#pragma unroll 1
+                for (int m = 0; m < kPairs; ++m) {
+                    ok = warp_wait(&pair_full[pair.at], pair.par, abort);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint64_t a = kd + pair.at * (kPair >> 4), b = qd + 2 * m * (NH * 128 >> 4);
+                    mma4<2, 2>(d, a, b, id_s, true);
+                    mma4<2, 2>(d, a + (kChunk >> 4), b + (NH * 128 >> 4), id_s, true);
+                    pair.step();
                 }
                 if (!ok)
                     break;
-                pend = true;
-                pend_first = j == piece.first;
+                commit_elected(&s_full[tiles & 1]);
                 ++tiles;
             }
-            ++pieces;
-        }
-        if (ok && pend) {
-            ok = warp_wait(&p_full, pvs & 1, abort);
-            if (ok && pend_first && pv_pieces > 0)
-                ok = warp_wait(&o_free, (pv_pieces - 1) & 1, abort);
             if (ok)
-                issue_pv();
+                commit_elected(&q_empty);
+            ++pieces;
         }
         if (!ok && lane == 0) {
             set_status(p.status, PKV_ERR_TIMEOUT);
             *abort = 1;
         }
         // Every MMA issued has completed before TMEM is freed.
-        if (elect_one()) {
-            tc_commit(&drain);
-            mbar_wait_bounded(&drain, 0, kWaitLimitNs);
+        commit_elected(&drain[0]);
+        warp_wait(&drain[0], 0, &no_abort);
+    } else if (warp == kValueWarp) {
+        // ------------------------------------------------- MMA issue: P V
+        constexpr uint32_t kIdPV = tc_idesc(128, NH, false) | 1u << 15;  // A is M-major
+        const uint64_t pd = desc64(((smem0 + kPOff) >> 4) | 1u << 16, kHi);
+        const uint64_t vd = desc64(((smem0 + kPairOff) >> 4) | (kChunk >> 4) << 16, kHi);  // 64-dim halves one chunk apart
+        Ring<NP> pair;
+        uint32_t tiles = 0, pieces = 0;
+        bool ok = true;
+        for (;;) {
+            const LatentPiece piece = walk.next(p);
+            if (piece.s < 0 || !ok)
+                break;
+            if (piece.len == 0)
+                continue;
+            for (int j = piece.first; j < piece.last; ++j) {
+                ok = warp_wait(&p_full, tiles & 1, abort);
+                // The last piece's sums have been read.
+                if (j == piece.first && pieces > 0)
+                    ok = ok && warp_wait(&o_free, (pieces - 1) & 1, abort);
+                if (!ok)
+                    break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int m = 0; m < kPairs; ++m) {
+                    mma4<(2048 >> 4), 2>(tmem + Geo::kOCol + m * NH, vd + pair.at * (kPair >> 4), pd, kIdPV,
+                                         j > piece.first);
+                    commit_elected(&pair_empty[pair.at]);
+                    pair.step();
+                }
+                commit_elected(&pv_done);
+                ++tiles;
+            }
+            ++pieces;
         }
-        __syncwarp();
+        if (!ok && lane == 0) {
+            set_status(p.status, PKV_ERR_TIMEOUT);
+            *abort = 1;
+        }
+        commit_elected(&drain[1]);
+        warp_wait(&drain[1], 0, &no_abort);
     } else {
         // ------------------------------------------------------- softmax
         const int g = warp >> 2, quad = warp & 3;
@@ -543,6 +551,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 float x[4 * J];
                 tmem_ld_rows<J>(tmem + lanes + (cnt & 1) * NH + g * kHalfCols, x);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&s_free[cnt & 1]);
                 const int valid = piece.len - j * kTok;  // tokens of the tile
                 const bool tail = valid < kTok;
                 if (tail) {
@@ -711,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kMmaWarp) {
+    if (warp == kValueWarp) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Geo::kAlloc)
                      : "memory");
     }
