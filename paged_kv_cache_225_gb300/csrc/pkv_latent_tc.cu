@@ -13,11 +13,12 @@
 //    K-major operand of the one and the M-major operand of the other.
 //  * A CTA (one per SM) has up to 64 heads and walks a range of tiles of 64 tokens
 //    (pkv_latent.cuh).  Warps 0-7 compute the softmax, four for each half of the heads;
-//    warps 8 and 9 issue the TMA loads (a box per page and 64 dims).
+//    warps 8 to 11 issue the TMA loads, one for each page of a tile.
 //  * TMEM: two buffers of S^T, and O^T.  P^T goes through shared memory.
-//  * The rings hold the rotated part of a tile (8 KB) and pairs of 64 dims (16 KB)
-//    on their own: the scores start with the first that lands, and a pair's slot is
-//    filled again when its part of O^T is done.
+//  * A tile comes in two parts, each with a ring of its own: the scores start with the
+//    first that lands, and a part's slot is filled again when its half of O^T is done.
+//    A box is 8 tokens of one page x half the dims: groups of 8 tokens then lie a fixed
+//    distance apart, whatever the pages, which is all that the operands ask for.
 //  * A warp issues the scores' MMAs, another those of P V, which free the ring.
 //  * The reference of a head's weights is raised only when a score exceeds it by 2^8;
 //    O^T is then rescaled in TMEM.  All weights of a head and tile share it, so the
@@ -36,33 +37,37 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 448;
 constexpr int kSoftWarps = 8;
-constexpr int kProducerWarp = 8;  // and 9
-constexpr int kProducers = 2;
-constexpr int kScoreWarp = 10;
-constexpr int kValueWarp = 11;
+constexpr int kProducerWarp = 8;  // one for each page of a tile
 constexpr int kTok = kLatentTokens;
-constexpr int kChunk = kTok * 128;  // bytes of 64 tokens x 64 dims
-constexpr int kPair = 2 * kChunk;
 constexpr int kPages = kTok / kBlockSize;
+constexpr int kScoreWarp = kProducerWarp + kPages;
+constexpr int kValueWarp = kScoreWarp + 1;
+constexpr int kAtom = 1024;  // bytes of 8 tokens x 64 dims
 
+// A tile lies in shared memory in two parts, chunks (of 64 dims) 0 .. CA - 1 and the rest
+// with the rotated chunk: [8 groups of 8 tokens][chunks][8 tokens][64 dims].
 template <int R, int NH> struct LtGeom {
-    static constexpr int kPairs = R / 128;               // per tile
-    static constexpr int kQ = (R / 64 + 1) * NH * 128;   // bytes of the queries
+    static constexpr int CA = R / 128, CB = R / 128 + 1;
+    static constexpr int kTilesA = CA / 2, kTilesB = CA - kTilesA;  // 128-dim tiles of O^T in each part
+    static constexpr int kA = 8 * CA * kAtom, kB = 8 * CB * kAtom;
+    static constexpr int kQ = (R / 64 + 1) * NH * 128;  // bytes of the queries
     static constexpr int kP = NH * 128;
-    static constexpr int kRoom = 229 * 1024 - kQ - kP - 4096;  // for the rings, 1 KB of alignment taken off
-    static constexpr int NR = NH == 64 && R == 512 ? 2 : 3;    // slots of rotated parts
-    static constexpr int NP = (kRoom - NR * kChunk) / kPair < 12 ? (kRoom - NR * kChunk) / kPair : 12;
-    static constexpr int kSmem = 1024 + kQ + kP + NR * kChunk + NP * kPair;
+    // Slots of each part: as many as fit.
+    static constexpr int kRoom = 229 * 1024 - 4096 - kQ - kP;
+    static constexpr int kBoth = kRoom / (kA + kB);
+    static constexpr int NA = kBoth;
+    static constexpr int NB = kBoth + (kRoom - kBoth * (kA + kB) >= kB ? 1 : 0);
+    static constexpr int kSmem = 1024 + kQ + kP + NA * kA + NB * kB;
     static constexpr int kOCol = 2 * NH;
-    static constexpr int kCols = kOCol + kPairs * NH;    // TMEM columns
+    static constexpr int kCols = kOCol + CA * NH;  // TMEM columns
     static constexpr int kAlloc = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-    static_assert(NP >= kPairs + 1 && kCols <= 512, "a tile and a half fit");
+    static_assert(kBoth >= 2 && kCols <= 512, "two tiles fit");
 };
 
 struct LatentMaps {
-    CUtensorMap q, rows;
+    CUtensorMap q, a, b;
 };
 
 // Four MMAs D (+)= A B whose operands, both in shared memory, are kA and kB (descriptor
@@ -103,21 +108,24 @@ __device__ __forceinline__ void expect_elected(uint64_t *bar, uint32_t bytes)
         "r"(bytes)
         : "memory");
 }
-__device__ __forceinline__ void load_elected(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar)
+// One box of 64 numbers x rows x chunks.
+__device__ __forceinline__ void load_elected(uint32_t dst, const CUtensorMap *map, int row, int chunk, int outer, uint64_t *bar)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
-        "@p cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        "@p cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(chunk), "r"(outer), "r"(smem_u32(bar))
         : "memory");
 }
 
-// Descriptor of a 128-byte-swizzled operand.  Low word: address / 16, and from bit 16 the
-// distance / 16 of 64-element halves (M-major only).  High word: 8-row groups 1 KB apart,
-// descriptor version 1 (bit 14), layout code 2 (bit 29).
-constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;
-__device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) { return static_cast<uint64_t>(hi) << 32 | lo; }
+// Descriptor of a 128-byte-swizzled operand at a shared-memory address, its 8-row groups
+// `groups` bytes apart and, M-major, its 64-element halves `halves` bytes apart.  From bit
+// 46 the version (1), from bit 61 the layout code (2).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t groups, uint32_t halves = 16)
+{
+    return static_cast<uint64_t>(groups >> 4 | 1u << 14 | 2u << 29) << 32 | (addr >> 4 | halves >> 4 << 16);
+}
 
 // 16 lanes x 8 J columns of f32 as fragments: registers 4j, 4j + 1 of a thread are row
 // lane / 4, columns 8j + 2 (lane % 4) and the next; 4j + 2, 4j + 3 the same of row + 8.
@@ -243,11 +251,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     latent_tc_kernel(const __grid_constant__ LatentDecodeParams p, const __grid_constant__ LatentMaps maps)
 {
     using Geo = LtGeom<R, NH>;
-    constexpr int NR = Geo::NR, NP = Geo::NP, kPairs = Geo::kPairs;
+    constexpr int NA = Geo::NA, NB = Geo::NB, CA = Geo::CA, CB = Geo::CB;
+    constexpr int kTiles = CA;          // 128-dim tiles of O^T
     constexpr int J = NH / 16;          // octets of columns per half
     constexpr int kHalfCols = NH / 2;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t rope_full[NR], rope_empty[NR], pair_full[NP], pair_empty[NP];
+    __shared__ __align__(8) uint64_t a_full[NA], a_empty[NA], b_full[NB], b_empty[NB];
     __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], s_free[2], p_full, pv_done, o_free,
         drain[2];
     __shared__ __align__(16) float s_red[2][4][32];  // per half and warp: maxima or sums of its heads
@@ -263,18 +272,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t smem0 = (raw + 1023u) & ~1023u;
     unsigned char *smem = smem_raw + (smem0 - raw);
-    constexpr int kPOff = Geo::kQ, kRopeOff = kPOff + Geo::kP, kPairOff = kRopeOff + NR * kChunk;
+    constexpr int kPOff = Geo::kQ, kAOff = kPOff + Geo::kP, kBOff = kAOff + NA * Geo::kA;
     const int team = blockIdx.x / p.head_tiles, ht = blockIdx.x % p.head_tiles;
     const int h0 = ht * NH;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NR; ++i) {
-            mbar_init(&rope_full[i], kProducers);
-            mbar_init(&rope_empty[i], 1);
+        for (int i = 0; i < NA; ++i) {
+            mbar_init(&a_full[i], kPages);
+            mbar_init(&a_empty[i], 1);
         }
-        for (int i = 0; i < NP; ++i) {
-            mbar_init(&pair_full[i], kProducers);
-            mbar_init(&pair_empty[i], 1);
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(&b_full[i], kPages);
+            mbar_init(&b_empty[i], 1);
         }
         mbar_init(&q_full, 1);
         mbar_init(&q_empty, 1);
@@ -291,8 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     if (warp == kProducerWarp) {
-        if (lane < 2) {
-            const CUtensorMap *map = lane == 0 ? &maps.q : &maps.rows;
+        if (lane < 3) {
+            const CUtensorMap *map = lane == 0 ? &maps.q : lane == 1 ? &maps.a : &maps.b;
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
         }
         LatentWalk walk;
@@ -314,14 +323,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = s_tmem;
     LatentWalk walk = s_walk;
 
-    if (warp == kProducerWarp || warp == kProducerWarp + 1) {
+    if (warp >= kProducerWarp && warp < kProducerWarp + kPages) {
         // ------------------------------------------------------- copies
-        // Two warps, two pages of a tile each: one alone takes 2800 cycles for the 36 boxes
-        // of a tile (R = 512), the tensor cores 1900.
-        const int half = warp - kProducerWarp;
-        Ring<NR> rope;
-        Ring<NP> pair;
-        uint32_t ropes = 0, pairs = 0, pieces = 0;
+        // A warp for each page of a tile: a warp issues a box only every 150 to 400 cycles,
+        // by its size (one warp 22 bytes a cycle, four 80).
+        const int mine = warp - kProducerWarp;
+        Ring<NA> a;
+        Ring<NB> b;
+        uint32_t tiles = 0, b_tiles = 0, pieces = 0;
         bool ok = true;
         for (;;) {
             const LatentPiece piece = walk.next(p);
@@ -329,73 +338,63 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             if (piece.len == 0)
                 continue;
-            if (half == 0) {
+            if (mine == 0) {
                 if (pieces > 0)
                     ok = warp_wait(&q_empty, (pieces - 1) & 1, abort);
                 if (!ok)
                     break;
                 expect_elected(&q_full, Geo::kQ);
-#pragma unroll 1
-                for (int c = 0; c <= R / 64; ++c)
-                    load_elected(smem0 + c * NH * 128, &maps.q, 64 * c, h0, piece.s, &q_full);
+                load_elected(smem0, &maps.q, h0, 0, piece.s, &q_full);
             }
             ++pieces;
             const int32_t *table = p.block_tables + static_cast<size_t>(piece.s) * p.max_blocks;
             const int pages = (piece.len + kBlockSize - 1) / kBlockSize;
-            // Eight tiles' block ids at a time, a lane each, the next eight on their way.
+            // This warp's block ids of 32 tiles, a lane each, the next 32 on their way.
             auto ids_at = [&](int j) {
-                const int page = j * kPages + lane;
+                const int page = (j + lane) * kPages + mine;
                 return page < pages ? __ldg(table + page) : 0;
             };
             int ids = 0, next_ids = ids_at(piece.first);
             for (int j = piece.first; j < piece.last; ++j) {
-                const int in8 = (j - piece.first) & 7;
-                if (in8 == 0) {
+                const int at = (j - piece.first) & 31;
+                if (at == 0) {
                     ids = next_ids;
                     if (static_cast<unsigned>(ids) >= static_cast<unsigned>(p.num_blocks)) {
                         set_status(p.status, PKV_ERR_OUT_OF_RANGE);
                         ids = p.num_blocks;  // past the map: zeros
                     }
-                    next_ids = j + 8 < piece.last ? ids_at(j + 8) : 0;
+                    next_ids = j + 32 < piece.last ? ids_at(j + 32) : 0;
                 }
-                const int there = max(0, min(2, pages - j * kPages - 2 * half));
-                const int id0 = __shfl_sync(kFullMask, ids, in8 * kPages + 2 * half);
-                const int id1 = __shfl_sync(kFullMask, ids, in8 * kPages + 2 * half + 1);
-                ok = warp_wait(&rope_empty[rope.at], rope.par ^ 1, abort);
+                const bool there = j * kPages + mine < pages;
+                const int id = __shfl_sync(kFullMask, ids, at);
+                ok = warp_wait(&a_empty[a.at], a.par ^ 1, abort);
                 if (!ok)
                     break;
                 {
-                    uint64_t *bar = &rope_full[rope.at];
-                    const uint32_t dst = smem0 + kRopeOff + rope.at * kChunk + half * 4096;
-                    expect_elected(bar, there * 2048);
-                    if (there > 0 && !(p.drop_first_copy && blockIdx.x == 0 && ropes == 0 && half == 0))
-                        load_elected(dst, &maps.rows, R, 0, id0, bar);
-                    if (there > 1)
-                        load_elected(dst + 2048, &maps.rows, R, 0, id1, bar);
+                    uint64_t *bar = &a_full[a.at];
+                    const uint32_t dst = smem0 + kAOff + a.at * Geo::kA + mine * (Geo::kA / kPages);
+                    expect_elected(bar, there ? Geo::kA / kPages : 0);
+                    if (there && !(p.drop_first_copy && blockIdx.x == 0 && tiles == 0 && mine == 0))
+                        load_elected(dst, &maps.a, 0, 0, id, bar);
+                    if (there)
+                        load_elected(dst + CA * kAtom, &maps.a, 8, 0, id, bar);
                 }
-                rope.step();
-                ++ropes;
-#pragma unroll 1
-                for (int m = 0; m < kPairs; ++m) {
-                    ok = warp_wait(&pair_empty[pair.at], pair.par ^ 1, abort);
-                    if (!ok)
-                        break;
-                    uint64_t *bar = &pair_full[pair.at];
-                    const uint32_t dst = smem0 + kPairOff + pair.at * kPair + half * 4096;
-                    expect_elected(bar, there * 4096);
-                    if (there > 0) {
-                        load_elected(dst, &maps.rows, 128 * m, 0, id0, bar);
-                        load_elected(dst + kChunk, &maps.rows, 128 * m + 64, 0, id0, bar);
-                    }
-                    if (there > 1) {
-                        load_elected(dst + 2048, &maps.rows, 128 * m, 0, id1, bar);
-                        load_elected(dst + kChunk + 2048, &maps.rows, 128 * m + 64, 0, id1, bar);
-                    }
-                    pair.step();
-                    ++pairs;
-                }
+                a.step();
+                ++tiles;
+                ok = warp_wait(&b_empty[b.at], b.par ^ 1, abort);
                 if (!ok)
                     break;
+                {
+                    uint64_t *bar = &b_full[b.at];
+                    const uint32_t dst = smem0 + kBOff + b.at * Geo::kB + mine * (Geo::kB / kPages);
+                    expect_elected(bar, there ? Geo::kB / kPages : 0);
+                    if (there) {
+                        load_elected(dst, &maps.b, 0, CA, id, bar);
+                        load_elected(dst + CB * kAtom, &maps.b, 8, CA, id, bar);
+                    }
+                }
+                b.step();
+                ++b_tiles;
             }
         }
         if (!ok && lane == 0) {
@@ -404,11 +403,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // Every copy still in flight lands before the CTA exits.
         if (lane == 0) {
-            for (uint32_t c = ropes > NR ? ropes - NR : 0; c < ropes; ++c)
-                tc_wait(&rope_full[c % NR], (c / NR) & 1, &no_abort);
-            for (uint32_t c = pairs > NP ? pairs - NP : 0; c < pairs; ++c)
-                tc_wait(&pair_full[c % NP], (c / NP) & 1, &no_abort);
-            if (pieces > 0 && half == 0)
+            for (uint32_t c = tiles > NA ? tiles - NA : 0; c < tiles; ++c)
+                tc_wait(&a_full[c % NA], (c / NA) & 1, &no_abort);
+            for (uint32_t c = b_tiles > NB ? b_tiles - NB : 0; c < b_tiles; ++c)
+                tc_wait(&b_full[c % NB], (c / NB) & 1, &no_abort);
+            if (pieces > 0 && mine == 0)
                 tc_wait(&q_full, (pieces - 1) & 1, &no_abort);
         }
         __syncwarp();
@@ -417,11 +416,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A warp for the scores and one for P V, each with its own waits: one warp that
         // took whichever was ready spent as long on looking as on issuing.
         const uint32_t id_s = tc_idesc(kTok, NH, false) | (p.negate ? 1u << 13 : 0u);
-        const uint64_t qd = desc64((smem0 >> 4) | 1u << 16, kHi);
-        const uint64_t rd = desc64(((smem0 + kRopeOff) >> 4) | 1u << 16, kHi);
-        const uint64_t kd = desc64(((smem0 + kPairOff) >> 4) | 1u << 16, kHi);
-        Ring<NR> rope;
-        Ring<NP> pair;
+        const uint64_t qd = operand(smem0, kAtom);
+        const uint64_t ad = operand(smem0 + kAOff, CA * kAtom), bd = operand(smem0 + kBOff, CB * kAtom);
+        Ring<NA> a;
+        Ring<NB> b;
         uint32_t tiles = 0, pieces = 0;
         bool ok = true;
         for (;;) {
@@ -436,26 +434,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The softmax has read the buffer's last scores.
                 if (tiles > 1)
                     ok = warp_wait(&s_free[tiles & 1], ((tiles >> 1) - 1) & 1, abort);
-                ok = ok && warp_wait(&rope_full[rope.at], rope.par, abort);
+                ok = ok && warp_wait(&a_full[a.at], a.par, abort);
                 if (!ok)
                     break;
                 tc_fence_after();
-                mma4<2, 2>(d, rd + rope.at * (kChunk >> 4), qd + R / 64 * (NH * 128 >> 4), id_s, false);
-                commit_elected(&rope_empty[rope.at]);
-                rope.step();
-#pragma unroll 1
-                for (int m = 0; m < kPairs; ++m) {
-                    ok = warp_wait(&pair_full[pair.at], pair.par, abort);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    const uint64_t a = kd + pair.at * (kPair >> 4), b = qd + 2 * m * (NH * 128 >> 4);
-                    mma4<2, 2>(d, a, b, id_s, true);
-                    mma4<2, 2>(d, a + (kChunk >> 4), b + (NH * 128 >> 4), id_s, true);
-                    pair.step();
-                }
+                const uint64_t x = ad + a.at * (Geo::kA >> 4), y = bd + b.at * (Geo::kB >> 4);
+#pragma unroll
+                for (int c = 0; c < CA; ++c)
+                    mma4<2, 2>(d, x + c * (kAtom >> 4), qd + c * (NH * 128 >> 4), id_s, c > 0);
+                a.step();
+                ok = warp_wait(&b_full[b.at], b.par, abort);
                 if (!ok)
                     break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < CB; ++c)
+                    mma4<2, 2>(d, y + c * (kAtom >> 4), qd + (CA + c) * (NH * 128 >> 4), id_s, true);
+                b.step();
                 commit_elected(&s_full[tiles & 1]);
                 ++tiles;
             }
@@ -473,9 +468,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kValueWarp) {
         // ------------------------------------------------- MMA issue: P V
         constexpr uint32_t kIdPV = tc_idesc(128, NH, false) | 1u << 15;  // A is M-major
-        const uint64_t pd = desc64(((smem0 + kPOff) >> 4) | 1u << 16, kHi);
-        const uint64_t vd = desc64(((smem0 + kPairOff) >> 4) | (kChunk >> 4) << 16, kHi);  // 64-dim halves one chunk apart
-        Ring<NP> pair;
+        const uint64_t pd = operand(smem0 + kPOff, kAtom);
+        const uint64_t ad = operand(smem0 + kAOff, CA * kAtom, kAtom), bd = operand(smem0 + kBOff, CB * kAtom, kAtom);
+        Ring<NA> a;
+        Ring<NB> b;
         uint32_t tiles = 0, pieces = 0;
         bool ok = true;
         for (;;) {
@@ -492,13 +488,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok)
                     break;
                 tc_fence_after();
-#pragma unroll 1
-                for (int m = 0; m < kPairs; ++m) {
-                    mma4<(2048 >> 4), 2>(tmem + Geo::kOCol + m * NH, vd + pair.at * (kPair >> 4), pd, kIdPV,
-                                         j > piece.first);
-                    commit_elected(&pair_empty[pair.at]);
-                    pair.step();
-                }
+                const uint64_t x = ad + a.at * (Geo::kA >> 4), y = bd + b.at * (Geo::kB >> 4);
+                // 16 tokens to a step: two groups.
+#pragma unroll
+                for (int m = 0; m < Geo::kTilesA; ++m)
+                    mma4<(2 * CA * kAtom >> 4), 2>(tmem + Geo::kOCol + m * NH, x + 2 * m * (kAtom >> 4), pd, kIdPV,
+                                                   j > piece.first);
+                commit_elected(&a_empty[a.at]);
+                a.step();
+#pragma unroll
+                for (int m = 0; m < Geo::kTilesB; ++m)
+                    mma4<(2 * CB * kAtom >> 4), 2>(tmem + Geo::kOCol + (Geo::kTilesA + m) * NH,
+                                                   y + 2 * m * (kAtom >> 4), pd, kIdPV, j > piece.first);
+                commit_elected(&b_empty[b.at]);
+                b.step();
                 commit_elected(&pv_done);
                 ++tiles;
             }
@@ -607,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         failed = !warp_wait(&pv_done, (cnt - 1) & 1, abort) || failed;
                         tc_fence_after();
 #pragma unroll 1
-                        for (int t = 0; t < kPairs; ++t)
+                        for (int t = 0; t < kTiles; ++t)
 #pragma unroll
                             for (int c0 = 0; c0 < kHalfCols; c0 += 8) {
                                 float o[8];
@@ -652,11 +655,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (tail) {
                     // Rows past the end may hold anything.
                     const int rows = kTok - valid;
-                    for (int e = threadIdx.x; e < rows * kPairs * 16; e += 32 * kSoftWarps) {
-                        const int row = valid + e % rows, piece16 = e / rows % 8, chunk = e / rows / 8;
-                        const uint32_t n = cnt * kPairs + (chunk >> 1);
-                        *reinterpret_cast<uint4 *>(smem + kPairOff + (n % NP) * kPair + (chunk & 1) * kChunk + row * 128 +
-                                                   piece16 * 16) = make_uint4(0, 0, 0, 0);
+                    unsigned char *pa = smem + kAOff + cnt % NA * Geo::kA, *pb = smem + kBOff + cnt % NB * Geo::kB;
+                    for (int e = threadIdx.x; e < rows * (CA + CB) * 8; e += 32 * kSoftWarps) {
+                        const int row = valid + e / (8 * (CA + CB)), x = e % (8 * (CA + CB));  // 16-byte pieces
+                        unsigned char *at = x < 8 * CA ? pa + (row >> 3) * (CA * kAtom) + (x >> 3) * kAtom
+                                                       : pb + (row >> 3) * (CB * kAtom) + ((x >> 3) - CA) * kAtom;
+                        *reinterpret_cast<uint4 *>(at + (row & 7) * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
                 }
                 fence_proxy_async();
@@ -697,12 +701,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int mine = min(kHalfCols, heads - h);
                 const float *f = s_col + h;
                 if (whole)
-                    store_heads<kPairs, NH, kHalfCols>(ocol, mine, [&](int t, int e, float x) {
+                    store_heads<kTiles, NH, kHalfCols>(ocol, mine, [&](int t, int e, float x) {
                         static_cast<__nv_bfloat16 *>(p.out)[(static_cast<size_t>(piece.s) * p.num_heads + h0 + h + e) * R +
                                                             128 * t + d] = __float2bfloat16(x * f[e]);
                     });
                 else
-                    store_heads<kPairs, NH, kHalfCols>(ocol, mine, [&](int t, int e, float x) {
+                    store_heads<kTiles, NH, kHalfCols>(ocol, mine, [&](int t, int e, float x) {
                         p.part[(slot + h + e) * R + 128 * t + d] = x;
                     });
             }
@@ -731,17 +735,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ host
 
-// [outer][rows][numbers] bf16, dense: boxes of 64 numbers x `box_rows` rows in the
-// 128-byte swizzle mode; zeros past the edges.
-bool encode_rows(EncodeTiledFn enc, CUtensorMap *map, const void *base, int numbers, int rows, int64_t outer,
-                 int box_rows)
+// [outer][rows][numbers] bf16, dense, as [outer][chunks][rows][64]: boxes of `box_rows` rows
+// x `box_chunks` chunks in the 128-byte swizzle mode; zeros past the edges.
+bool encode_chunks(EncodeTiledFn enc, CUtensorMap *map, const void *base, int numbers, int rows, int64_t outer,
+                   int box_rows, int box_chunks)
 {
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(numbers), static_cast<cuuint64_t>(rows),
+    const cuuint64_t row = static_cast<cuuint64_t>(numbers) * 2;
+    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(numbers / 64),
                                 static_cast<cuuint64_t>(outer)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(numbers) * 2, static_cast<cuuint64_t>(numbers) * 2 * rows};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
-    const cuuint32_t es[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+    const cuuint64_t strides[3] = {row, 128, row * rows};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_chunks), 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -763,8 +768,11 @@ template <int R, int NH> pkv_status launch_tc(const LatentDecodeParams &p, cudaS
     if (!enc)
         return PKV_ERR_UNSUPPORTED;
     LatentMaps maps;
-    if (!encode_rows(enc, &maps.q, p.q, R + kRopeDim, p.num_heads, p.num_seqs, NH) ||
-        !encode_rows(enc, &maps.rows, p.cache, R + kRopeDim, kBlockSize, p.num_blocks, kBlockSize))
+    using Geo = LtGeom<R, NH>;
+    constexpr int kRow = R + kRopeDim;
+    if (!encode_chunks(enc, &maps.q, p.q, kRow, p.num_heads, p.num_seqs, NH, kRow / 64) ||
+        !encode_chunks(enc, &maps.a, p.cache, kRow, kBlockSize, p.num_blocks, 8, Geo::CA) ||
+        !encode_chunks(enc, &maps.b, p.cache, kRow, kBlockSize, p.num_blocks, 8, Geo::CB))
         return PKV_ERR_INVALID_ARG;
     latent_tc_kernel<R, NH><<<p.teams * p.head_tiles, kThreads, LtGeom<R, NH>::kSmem, stream>>>(p, maps);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
