@@ -4,7 +4,8 @@
 // another, are cut into one contiguous range per team (a team: the CTAs of a
 // sequence's head tiles), as equal as whole tiles allow, whatever the lengths.
 // A sequence cut by a range's end leaves partial sums, which a second kernel
-// joins; the others are written at once.
+// joins; the others are written at once.  Short sequences are not cut: a range then
+// has the sequences that begin in it.
 #pragma once
 
 #include "pkv_common.cuh"
@@ -62,8 +63,17 @@ struct LatentWalk {
         s = j = 0;
         if (team >= teams)
             return;
-        const long begin = total * team / teams, end = total * (team + 1) / teams;
-        left = end - begin;
+        // The first total % teams teams have a tile more.
+        long each, extra;
+        if (total >> 31 == 0) {
+            each = static_cast<unsigned>(total) / static_cast<unsigned>(teams);
+            extra = static_cast<unsigned>(total) % static_cast<unsigned>(teams);
+        } else {
+            each = total / teams;
+            extra = total % teams;
+        }
+        const long begin = each * team + min(static_cast<long>(team), extra);
+        left = each + (team < extra ? 1 : 0);
         const unsigned past = __ballot_sync(kFullMask, upto > begin);
         const int at = __ffs(past) - 1;
         if (lane == at) {
@@ -79,6 +89,12 @@ struct LatentWalk {
         }
         s = __shfl_sync(kFullMask, s, at);
         j = __shfl_sync(kFullMask, j, at);
+        if (p.whole && j > 0) {
+            // Sequences are not cut: they belong to the team whose range they begin in.
+            left -= latent_tiles(latent_len(p, s, false)) - j;
+            ++s;
+            j = 0;
+        }
     }
 
     // The next piece; s = -1 when the range is used up.
@@ -93,7 +109,7 @@ struct LatentWalk {
         r.len = latent_len(p, s, false);
         r.tiles = latent_tiles(r.len);
         r.first = j;
-        r.last = static_cast<int>(min(static_cast<long>(r.tiles), j + left));
+        r.last = p.whole ? r.tiles : static_cast<int>(min(static_cast<long>(r.tiles), j + left));
         left -= r.last - r.first;
         ++s;
         j = 0;

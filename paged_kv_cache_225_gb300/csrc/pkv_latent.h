@@ -64,6 +64,7 @@ struct LatentDecodeParams {
     int drop_first_copy; // test hook: never issue the first copy of CTA 0
     // The schedule (latent_plan).
     int tile_heads, head_tiles, teams;
+    int whole;           // sequences are not cut
     float *part;         // [2 teams][head tiles][tile_heads][R] sums of weights times rows
     float2 *part_ml;     // [2 teams][head tiles][tile_heads] reference of the weights (log2), their sum
     int2 *pieces;        // [teams] sequence cut by a team's start, by its end (-1: none)

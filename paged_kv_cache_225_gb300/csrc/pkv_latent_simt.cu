@@ -261,46 +261,48 @@ constexpr int kMergeWarps = 8;
 
 // Joins the pieces of cut sequences.  blockIdx.x is a sequence (fewer sequences than
 // teams) or a team but the first, which stands for the sequence that its start cuts if
-// that begins in the team before.  A warp has 128 dims of one head:
+// that begins in the team before.  For one head and 128 of its dims
 //   M = max_i m_i,  out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i
-// over the pieces i in order, so the result does not depend on who wrote first.  With a
-// whole head to a warp there were too few loads under way when few sequences have many
-// pieces.
-template <typename T, int R>
+// over the pieces i.  A warp takes all pieces of its head and dims, or, with many
+// pieces to a sequence (kShared), the block's warps take every eighth piece of one head
+// and dims and add up in order.  Either way the result does not depend on who wrote first.
+template <typename T, int R, bool kShared>
 __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const LatentDecodeParams p, int by_sequence)
 {
     constexpr int kParts = R / 128;
-    const int lane = threadIdx.x & 31;
-    const int unit = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+    __shared__ float4 s_sum[kMergeWarps][32];
+    __shared__ float s_total[kMergeWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int unit = kShared ? blockIdx.y : blockIdx.y * kMergeWarps + warp;
     const int h = unit / kParts, d = unit % kParts * 128 + 4 * lane;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (h >= p.num_heads)
         return;
-    int s, team;  // the first team that goes on with s
-    if (by_sequence) {
-        s = blockIdx.x;
-        team = p.teams;
-        for (int t = 0; t < p.teams && team == p.teams; t += 32) {
-            const unsigned same = __ballot_sync(kFullMask, t + lane < p.teams && p.pieces[t + lane].x == s);
-            if (same)
-                team = t + __ffs(same) - 1;
-        }
-        if (team == p.teams)
-            return;
-    } else {
-        team = blockIdx.x + 1;
+    // The sequence that a team's start cuts, five lanes' worth: the teams are at most 304.
+    constexpr int kMost = (2 * 152 + 31) / 32;
+    int cut[kMost];
+#pragma unroll
+    for (int i = 0; i < kMost; ++i)
+        cut[i] = 32 * i + lane < p.teams ? p.pieces[32 * i + lane].x : -1;
+    int s = blockIdx.x;
+    if (!by_sequence) {
+        const int team = blockIdx.x + 1;
         s = p.pieces[team].x;
         // The piece before starts the sequence if nothing before that one belongs to it.
         if (s < 0 || p.pieces[team - 1].x == s)
             return;
     }
-    int last = team;  // the last team with a piece
-    for (int t = team; t < p.teams; t += 32) {
-        const unsigned same = __ballot_sync(kFullMask, t + lane < p.teams && p.pieces[t + lane].x == s);
-        last = t + __popc(same) - 1;  // its teams are neighbours
-        if (same != kFullMask)
-            break;
+    int team = p.teams, count = 0;  // the first team that goes on with s, and how many do
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const unsigned same = __ballot_sync(kFullMask, cut[i] == s);
+        if (same && count == 0)
+            team = 32 * i + __ffs(same) - 1;
+        count += __popc(same);  // its teams are neighbours
     }
+    if (count == 0)
+        return;
+    const int last = team + count - 1;
     const int ht = h / p.tile_heads, hh = h % p.tile_heads;
     auto row = [&](int t) {  // t = team - 1: the piece the sequence starts with
         const size_t slot = t < team ? 2 * t + 1 : 2 * t;
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const La
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     float total = 0.f;
 #pragma unroll 8
-    for (int t = team - 1; t <= last; ++t) {
+    for (int t = team - 1 + (kShared ? warp : 0); t <= last; t += kShared ? kMergeWarps : 1) {
         const float2 ml = p.part_ml[row(t)];
         const float4 x = *reinterpret_cast<const float4 *>(p.part + row(t) * R + d);
         const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
@@ -324,6 +326,23 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const La
         sum.y = fmaf(w, x.y, sum.y);
         sum.z = fmaf(w, x.z, sum.z);
         sum.w = fmaf(w, x.w, sum.w);
+    }
+    if constexpr (kShared) {
+        s_sum[warp][lane] = sum;
+        if (lane == 0)
+            s_total[warp] = total;
+        __syncthreads();
+        if (warp > 0)
+            return;
+#pragma unroll
+        for (int i = 1; i < kMergeWarps; ++i) {
+            const float4 x = s_sum[i][lane];
+            sum.x += x.x;
+            sum.y += x.y;
+            sum.z += x.z;
+            sum.w += x.w;
+            total += s_total[i];
+        }
     }
     const size_t at = (static_cast<size_t>(s) * p.num_heads + h) * R + d;
     const float4 y = make_float4(sum.x / total, sum.y / total, sum.z / total, sum.w / total);
@@ -351,12 +370,13 @@ template <int R> pkv_status launch_simt(const LatentDecodeParams &p, cudaStream_
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-template <typename T, int R> pkv_status launch_merge(const LatentDecodeParams &p, cudaStream_t stream)
+template <typename T, int R, bool kShared> pkv_status launch_merge(const LatentDecodeParams &p, cudaStream_t stream)
 {
     const int by_sequence = p.num_seqs < p.teams;
+    const int units = p.num_heads * (R / 128);
     cudaLaunchConfig_t config = {};
     config.gridDim = dim3(by_sequence ? p.num_seqs : p.teams - 1,
-                          (p.num_heads * (R / 128) + kMergeWarps - 1) / kMergeWarps);
+                          kShared ? units : (units + kMergeWarps - 1) / kMergeWarps);
     config.blockDim = dim3(32 * kMergeWarps);
     config.stream = stream;
     // Set up while the attention kernel runs.
@@ -365,11 +385,19 @@ template <typename T, int R> pkv_status launch_merge(const LatentDecodeParams &p
     early.val.programmaticStreamSerializationAllowed = 1;
     config.attrs = &early;
     config.numAttrs = 1;
-    return cudaLaunchKernelEx(&config, latent_merge_kernel<T, R>, p, by_sequence) == cudaSuccess ? PKV_OK
-                                                                                                 : PKV_ERR_CUDA;
+    return cudaLaunchKernelEx(&config, latent_merge_kernel<T, R, kShared>, p, by_sequence) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+template <typename T, int R> pkv_status launch_merge_by(const LatentDecodeParams &p, cudaStream_t stream)
+{
+    // Eight pieces to a sequence and more.
+    return p.teams >= 8 * p.num_seqs ? launch_merge<T, R, true>(p, stream) : launch_merge<T, R, false>(p, stream);
 }
 
 }  // namespace
+
+constexpr long kWholeTiles = 8;
 
 size_t latent_plan(LatentDecodeParams &p, int dtype)
 {
@@ -380,7 +408,10 @@ size_t latent_plan(LatentDecodeParams &p, int dtype)
     const long tiles = (static_cast<long>(p.max_len) + kLatentTokens - 1) / kLatentTokens;
     const long units = static_cast<long>(p.num_seqs) * (tiles > 1 ? tiles : 1);
     const long most = ctas / p.head_tiles;
-    p.teams = static_cast<int>(units < most ? units : most);
+    // A sequence of up to kWholeTiles is not worth the second kernel.
+    p.whole = tiles <= kWholeTiles;
+    const long want = p.whole ? p.num_seqs : units;
+    p.teams = static_cast<int>(want < most ? want : most);
     const size_t rows = 2 * static_cast<size_t>(p.teams) * p.head_tiles * p.tile_heads;
     return (rows * (p.latent_dim * sizeof(float) + sizeof(float2)) + p.teams * sizeof(int2) + 255) / 256 * 256;
 }
@@ -392,13 +423,12 @@ pkv_status launch_latent_decode_simt(const LatentDecodeParams &p, cudaStream_t s
 
 pkv_status launch_latent_merge(const LatentDecodeParams &p, int dtype, cudaStream_t stream)
 {
-    // A sequence of one tile is never cut.
-    if (p.teams <= 1 || p.max_len <= kLatentTokens)
+    if (p.teams <= 1 || p.whole)
         return PKV_OK;
     if (dtype == PKV_F32)
-        return p.latent_dim == 512 ? launch_merge<float, 512>(p, stream) : launch_merge<float, 256>(p, stream);
-    return p.latent_dim == 512 ? launch_merge<__nv_bfloat16, 512>(p, stream)
-                               : launch_merge<__nv_bfloat16, 256>(p, stream);
+        return p.latent_dim == 512 ? launch_merge_by<float, 512>(p, stream) : launch_merge_by<float, 256>(p, stream);
+    return p.latent_dim == 512 ? launch_merge_by<__nv_bfloat16, 512>(p, stream)
+                               : launch_merge_by<__nv_bfloat16, 256>(p, stream);
 }
 
 }  // namespace pkv

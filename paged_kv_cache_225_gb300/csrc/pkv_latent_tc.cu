@@ -13,7 +13,7 @@
 //    K-major operand of the one and the M-major operand of the other.
 //  * A CTA (one per SM) has up to 64 heads and walks a range of tiles of 64 tokens
 //    (pkv_latent.cuh).  Warps 0-7 compute the softmax, four for each half of the heads;
-//    warps 8 to 11 issue the TMA loads, one for each page of a tile.
+//    warps 8 to 15 issue the TMA loads, one for each 8 tokens of a tile.
 //  * TMEM: two buffers of S^T, and O^T.  P^T goes through shared memory.
 //  * A tile comes in two parts, each with a ring of its own: the scores start with the
 //    first that lands, and a part's slot is filled again when its half of O^T is done.
@@ -37,13 +37,16 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 448;
+constexpr int kThreads = 608;
 constexpr int kSoftWarps = 8;
-constexpr int kProducerWarp = 8;  // one for each page of a tile
+constexpr int kProducerWarp = 8;  // one for each group of 8 tokens
+constexpr int kGroups = kLatentTokens / 8;
 constexpr int kTok = kLatentTokens;
 constexpr int kPages = kTok / kBlockSize;
-constexpr int kScoreWarp = kProducerWarp + kPages;
+constexpr int kScoreWarp = kProducerWarp + kGroups;
 constexpr int kValueWarp = kScoreWarp + 1;
+constexpr int kAheadWarp = kValueWarp + 1;
+constexpr int kAhead = 2;  // tiles asked of HBM ahead of the rings
 constexpr int kAtom = 1024;  // bytes of 8 tokens x 64 dims
 
 // A tile lies in shared memory in two parts, chunks (of 64 dims) 0 .. CA - 1 and the rest
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(16) float s_red[2][4][32];  // per half and warp: maxima or sums of its heads
     __shared__ __align__(16) float s_col[NH];        // per head: a factor of its column of O^T
     __shared__ LatentWalk s_walk;
-    __shared__ uint32_t s_tmem;
+    __shared__ uint32_t s_tmem, s_issued;  // tiles whose copies have been issued
     __shared__ int s_abort, s_never, s_failed[2][2];
     volatile int *abort = &s_abort;
     const volatile int &no_abort = s_never;  // for what has to end before the CTA may
@@ -276,27 +279,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int team = blockIdx.x / p.head_tiles, ht = blockIdx.x % p.head_tiles;
     const int h0 = ht * NH;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < NA; ++i) {
-            mbar_init(&a_full[i], kPages);
-            mbar_init(&a_empty[i], 1);
+    if (warp == 0) {
+        // A lane for each barrier.
+        if (lane < NA) {
+            mbar_init(&a_full[lane], kGroups);
+            mbar_init(&a_empty[lane], 1);
         }
-        for (int i = 0; i < NB; ++i) {
-            mbar_init(&b_full[i], kPages);
-            mbar_init(&b_empty[i], 1);
+        if (lane < NB) {
+            mbar_init(&b_full[lane], kGroups);
+            mbar_init(&b_empty[lane], 1);
         }
-        mbar_init(&q_full, 1);
-        mbar_init(&q_empty, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&s_free[i], kSoftWarps);
-            mbar_init(&drain[i], 1);
+        if (lane < 2) {
+            mbar_init(&s_full[lane], 1);
+            mbar_init(&s_free[lane], kSoftWarps);
+            mbar_init(&drain[lane], 1);
+            s_failed[lane][0] = s_failed[lane][1] = 0;
         }
-        mbar_init(&p_full, kSoftWarps);
-        mbar_init(&pv_done, 1);
-        mbar_init(&o_free, kSoftWarps);
-        s_abort = s_never = 0;
-        s_failed[0][0] = s_failed[0][1] = s_failed[1][0] = s_failed[1][1] = 0;
+        if (lane == 2) {
+            mbar_init(&q_full, 1);
+            mbar_init(&q_empty, 1);
+            mbar_init(&p_full, kSoftWarps);
+        }
+        if (lane == 3) {
+            mbar_init(&pv_done, 1);
+            mbar_init(&o_free, kSoftWarps);
+            s_abort = s_never = 0;
+            s_issued = 0;
+        }
         fence_mbar_init();
     }
     if (warp == kProducerWarp) {
@@ -323,10 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = s_tmem;
     LatentWalk walk = s_walk;
 
-    if (warp >= kProducerWarp && warp < kProducerWarp + kPages) {
+    if (warp >= kProducerWarp && warp < kProducerWarp + kGroups) {
         // ------------------------------------------------------- copies
-        // A warp for each page of a tile: a warp issues a box only every 150 to 400 cycles,
-        // by its size (one warp 22 bytes a cycle, four 80).
+        // A warp for each group of 8 tokens: a warp issues a box only every 150 to 400
+        // cycles, by its size (one warp 22 bytes a cycle, four 80).
         const int mine = warp - kProducerWarp;
         Ring<NA> a;
         Ring<NB> b;
@@ -351,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pages = (piece.len + kBlockSize - 1) / kBlockSize;
             // This warp's block ids of 32 tiles, a lane each, the next 32 on their way.
             auto ids_at = [&](int j) {
-                const int page = (j + lane) * kPages + mine;
+                const int page = (j + lane) * kPages + mine / 2;
                 return page < pages ? __ldg(table + page) : 0;
             };
             int ids = 0, next_ids = ids_at(piece.first);
@@ -365,33 +374,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     next_ids = j + 32 < piece.last ? ids_at(j + 32) : 0;
                 }
-                const bool there = j * kPages + mine < pages;
+                const bool there = j * kTok + 8 * mine < piece.len;
                 const int id = __shfl_sync(kFullMask, ids, at);
                 ok = warp_wait(&a_empty[a.at], a.par ^ 1, abort);
                 if (!ok)
                     break;
                 {
                     uint64_t *bar = &a_full[a.at];
-                    const uint32_t dst = smem0 + kAOff + a.at * Geo::kA + mine * (Geo::kA / kPages);
-                    expect_elected(bar, there ? Geo::kA / kPages : 0);
+                    expect_elected(bar, there ? Geo::kA / kGroups : 0);
                     if (there && !(p.drop_first_copy && blockIdx.x == 0 && tiles == 0 && mine == 0))
-                        load_elected(dst, &maps.a, 0, 0, id, bar);
-                    if (there)
-                        load_elected(dst + CA * kAtom, &maps.a, 8, 0, id, bar);
+                        load_elected(smem0 + kAOff + a.at * Geo::kA + mine * (Geo::kA / kGroups), &maps.a,
+                                     8 * (mine & 1), 0, id, bar);
                 }
                 a.step();
                 ++tiles;
+                if (mine == 0 && lane == 0)
+                    *static_cast<volatile uint32_t *>(&s_issued) = tiles;
                 ok = warp_wait(&b_empty[b.at], b.par ^ 1, abort);
                 if (!ok)
                     break;
                 {
                     uint64_t *bar = &b_full[b.at];
-                    const uint32_t dst = smem0 + kBOff + b.at * Geo::kB + mine * (Geo::kB / kPages);
-                    expect_elected(bar, there ? Geo::kB / kPages : 0);
-                    if (there) {
-                        load_elected(dst, &maps.b, 0, CA, id, bar);
-                        load_elected(dst + CB * kAtom, &maps.b, 8, CA, id, bar);
-                    }
+                    expect_elected(bar, there ? Geo::kB / kGroups : 0);
+                    if (there)
+                        load_elected(smem0 + kBOff + b.at * Geo::kB + mine * (Geo::kB / kGroups), &maps.b,
+                                     8 * (mine & 1), CA, id, bar);
                 }
                 b.step();
                 ++b_tiles;
@@ -411,6 +418,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_wait(&q_full, (pieces - 1) & 1, &no_abort);
         }
         __syncwarp();
+    } else if (warp == kAheadWarp && p.head_tiles > 1) {
+        // --------------------------------------------- HBM, ahead of the rings
+        // Two tiles are too little to have under way for HBM's latency at its rate: their
+        // pages are fetched into L2 while the rings are still full.  Two tiles at a time,
+        // a lane for each page; head tiles share the pages out.
+        const volatile uint32_t *issued = &s_issued;
+        uint32_t tiles = 0;
+        for (bool on = true; on;) {
+            const LatentPiece piece = walk.next(p);
+            if (piece.s < 0)
+                break;
+            const int32_t *table = p.block_tables + static_cast<size_t>(piece.s) * p.max_blocks;
+            const int pages = min((piece.len + kBlockSize - 1) / kBlockSize, piece.last * kPages);
+            const int tile_count = piece.len > 0 ? piece.last - piece.first : 0;
+            for (int j = 0; j < tile_count; j += 2, tiles += 2) {
+                const int page = (piece.first + j) * kPages + lane;
+                const int id = lane < 2 * kPages && page < pages && page % p.head_tiles == ht ? __ldg(table + page) : -1;
+                while (on && static_cast<int>(tiles - *issued) > kAhead) {
+                    on = !*abort;
+                    __nanosleep(100);
+                }
+                on = __all_sync(kFullMask, on);
+                if (!on)
+                    break;
+                constexpr int kLines = kBlockSize * (R + kRopeDim) * 2 / 128;
+#pragma unroll 1
+                for (int i = 0; i < 2 * kPages; ++i) {
+                    const int one = __shfl_sync(kFullMask, id, i);
+                    if (static_cast<unsigned>(one) >= static_cast<unsigned>(p.num_blocks))
+                        continue;
+                    const char *at = static_cast<const char *>(p.cache) + static_cast<size_t>(one) * (kLines * 128);
+                    for (int x = lane; x < kLines; x += 32)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + x * 128));
+                }
+            }
+            tiles -= tile_count & 1;
+        }
     } else if (warp == kScoreWarp) {
         // ------------------------------------------------- MMA issue: scores
         // A warp for the scores and one for P V, each with its own waits: one warp that
@@ -513,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         commit_elected(&drain[1]);
         warp_wait(&drain[1], 0, &no_abort);
-    } else {
+    } else if (warp < kSoftWarps) {
         // ------------------------------------------------------- softmax
         const int g = warp >> 2, quad = warp & 3;
         const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
