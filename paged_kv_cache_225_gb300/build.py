@@ -19,10 +19,10 @@ LIB = os.path.join(BUILD, "libpkv.so")
 UNITS = ["pkv_api.cu", "pkv_cache.cu", "pkv_merge.cu", "pkv_decode_simt.cu",
          "pkv_decode_simt_fp8.cu", "pkv_decode_mma.cu",
          "pkv_noalloc.cu", "pkv_prefill.cu", "pkv_prefill_tc.cu", "pkv_prompt.cu", "pkv_prompt_tc.cu",
-         "pkv_tables.cu", "pkv_ops_api.cu", "pkv_rope.cu", "pkv_latent_simt.cu", "pkv_latent_tc.cu", "pkv_latent_prompt.cu",
+         "pkv_tables.cu", "pkv_ops_api.cu", "pkv_rope.cu", "pkv_latent_simt.cu", "pkv_latent_tc.cu", "pkv_latent_prompt.cu", "pkv_latent_prompt_tc.cu",
          "pkv_latent_api.cu", "pkv_block_manager.cpp"]
 HEADERS = ["pkv_common.cuh", "pkv_convert.cuh", "pkv_decode.cuh", "pkv_merge.cuh",
-           "pkv_streamk.cuh", "pkv_prefill.cuh", "pkv_prompt.cuh", "pkv_tc.cuh", "pkv_internal.h",
+           "pkv_streamk.cuh", "pkv_prefill.cuh", "pkv_prompt.cuh", "pkv_prompt_tc.cuh", "pkv_tc.cuh", "pkv_internal.h",
            "pkv_ops.h", "pkv_latent.h", "pkv_latent.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]

@@ -93,7 +93,7 @@ size_t latent_plan(LatentDecodeParams &p, int dtype);
 pkv_status launch_latent_decode_simt(const LatentDecodeParams &p, cudaStream_t stream);
 pkv_status launch_latent_decode_tc(const LatentDecodeParams &p, cudaStream_t stream);
 pkv_status launch_latent_merge(const LatentDecodeParams &p, int dtype, cudaStream_t stream);
-pkv_status launch_latent_prompt_simt(const LatentPromptParams &p, int dtype, cudaStream_t stream);
+pkv_status launch_latent_prompt_simt(const LatentPromptParams &p, cudaStream_t stream);
 pkv_status launch_latent_prompt_tc(const LatentPromptParams &p, cudaStream_t stream);
 pkv_status launch_rope_append(const RopeAppendParams &p, cudaStream_t stream);
 pkv_status launch_latent_append(const LatentAppendParams &p, cudaStream_t stream);

@@ -304,7 +304,8 @@ pkv_status pkv_latent_prompt_attn(const void *q, const void *k, const void *k_ro
     p.items.score_scale = score_factor(scale);
     p.items.negate = scale < 0.f ? 1 : 0;
     p.drop_first_copy = (flags & PKV_FLAG_TEST_DROP_FIRST_COPY) ? 1 : 0;
-    return launch_latent_prompt_simt(p, dtype, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dtype == PKV_F32 ? launch_latent_prompt_simt(p, st) : launch_latent_prompt_tc(p, st);
 }
 
 }  // extern "C"

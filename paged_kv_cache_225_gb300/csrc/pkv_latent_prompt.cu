@@ -54,15 +54,7 @@ __device__ __forceinline__ float2 unpair(uint64_t v)
     return r;
 }
 
-// 4 numbers into shared memory as f32.
-__device__ __forceinline__ void copy4(float *dst, const float *src) { cp_async_16(dst, src); }
-__device__ __forceinline__ void copy4(float *dst, const __nv_bfloat16 *src)
-{
-    const uint2 x = *reinterpret_cast<const uint2 *>(src);
-    *reinterpret_cast<float4 *>(dst) = make_float4(bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y));
-}
-
-template <typename T, int DN>
+template <int DN>
 __global__ void __launch_bounds__(kSimtThreads, 2) latent_prompt_simt_kernel(const LatentPromptParams p)
 {
     using Geo = LpGeom<DN>;
@@ -73,8 +65,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_prompt_simt_kernel(con
     __shared__ PromptItem s_item;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const T *q = static_cast<const T *>(p.q), *k = static_cast<const T *>(p.k);
-    const T *kr = static_cast<const T *>(p.k_rope), *v = static_cast<const T *>(p.v);
+    const float *q = static_cast<const float *>(p.q), *k = static_cast<const float *>(p.k);
+    const float *kr = static_cast<const float *>(p.k_rope), *v = static_cast<const float *>(p.v);
     const int H = p.items.num_kv_heads;
     const float c = p.items.negate ? -p.items.score_scale : p.items.score_scale;
 
@@ -98,7 +90,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_prompt_simt_kernel(con
         for (int e = threadIdx.x; e < kRows * (kDk / 4); e += kSimtThreads) {
             const int r = e / (kDk / 4), d = 4 * (e % (kDk / 4));
             if (r < nt)
-                copy4(sq + r * kLd + d, q + (static_cast<int64_t>(it.row0) + t0 + r) * p.q_stride +
+                cp_async_16(sq + r * kLd + d, q + (static_cast<int64_t>(it.row0) + t0 + r) * p.q_stride +
                                             static_cast<int64_t>(it.hkv) * kDk + d);
             else
                 *reinterpret_cast<float4 *>(sq + r * kLd + d) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -127,16 +119,16 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_prompt_simt_kernel(con
                 if (k0 + r >= end)
                     *reinterpret_cast<float4 *>(dk) = make_float4(0.f, 0.f, 0.f, 0.f);
                 else if (d < DN)
-                    copy4(dk, k + row * p.k_stride + it.hkv * p.k_head + d);
+                    cp_async_16(dk, k + row * p.k_stride + it.hkv * p.k_head + d);
                 else
-                    copy4(dk, kr + row * p.k_rope_stride + d - DN);
+                    cp_async_16(dk, kr + row * p.k_rope_stride + d - DN);
             }
             cp_async_commit();
             for (int e = threadIdx.x; e < kKeys * (DN / 4); e += kSimtThreads) {
                 const int r = e / (DN / 4), d = 4 * (e % (DN / 4));
                 float *dv = sv + r * DN + d;
                 if (k0 + r < end)
-                    copy4(dv, v + (static_cast<int64_t>(it.row0) + k0 + r) * p.v_stride + it.hkv * p.v_head + d);
+                    cp_async_16(dv, v + (static_cast<int64_t>(it.row0) + k0 + r) * p.v_stride + it.hkv * p.v_head + d);
                 else
                     *reinterpret_cast<float4 *>(dv) = make_float4(0.f, 0.f, 0.f, 0.f);
             }
@@ -268,25 +260,21 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_prompt_simt_kernel(con
             for (int x = 0; x < kCols; ++x) {
                 const size_t off = orow + 4 * tx + 64 * x;
                 const float2 a = unpair(o[i][2 * x]), b = unpair(o[i][2 * x + 1]);
-                const float4 y = make_float4(a.x / sum, a.y / sum, b.x / sum, b.y / sum);
-                if constexpr (sizeof(T) == 4)
-                    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + off) = y;
-                else
-                    *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(p.out) + off) =
-                        make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + off) =
+                    make_float4(a.x / sum, a.y / sum, b.x / sum, b.y / sum);
             }
         }
         __syncthreads();  // the item and its rows are read before the next ones are written
     }
 }
 
-template <typename T, int DN> pkv_status launch_lp(LatentPromptParams p, cudaStream_t stream)
+template <int DN> pkv_status launch_lp(LatentPromptParams p, cudaStream_t stream)
 {
     static ContextCache cache;
     int set = 0;
     const pkv_status rc = cache.get(&set, [](int *out) -> pkv_status {
         *out = 1;
-        return cudaFuncSetAttribute(latent_prompt_simt_kernel<T, DN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(latent_prompt_simt_kernel<DN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     LpGeom<DN>::kSmem) == cudaSuccess
                    ? PKV_OK
                    : PKV_ERR_CUDA;
@@ -301,18 +289,16 @@ template <typename T, int DN> pkv_status launch_lp(LatentPromptParams p, cudaStr
     p.items.max_items = static_cast<unsigned>(items);
     // Two CTAs to an SM; the costliest items go first, one at a time.
     const long slots = 2L * device_sm_count();
-    latent_prompt_simt_kernel<T, DN><<<static_cast<unsigned>(items < slots ? items : slots), kSimtThreads,
+    latent_prompt_simt_kernel<DN><<<static_cast<unsigned>(items < slots ? items : slots), kSimtThreads,
                                        LpGeom<DN>::kSmem, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // namespace
 
-pkv_status launch_latent_prompt_simt(const LatentPromptParams &p, int dtype, cudaStream_t stream)
+pkv_status launch_latent_prompt_simt(const LatentPromptParams &p, cudaStream_t stream)
 {
-    if (dtype == PKV_F32)
-        return p.nope == 128 ? launch_lp<float, 128>(p, stream) : launch_lp<float, 64>(p, stream);
-    return p.nope == 128 ? launch_lp<__nv_bfloat16, 128>(p, stream) : launch_lp<__nv_bfloat16, 64>(p, stream);
+    return p.nope == 128 ? launch_lp<128>(p, stream) : launch_lp<64>(p, stream);
 }
 
 }  // namespace pkv

@@ -106,6 +106,52 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
+// Descriptor of a 128-byte-swizzled operand at a shared-memory address, its 8-row groups
+// `groups` bytes apart and, M-major, its 64-element halves `halves` bytes apart.  From bit
+// 46 the version (1), from bit 61 the layout code (2).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t groups, uint32_t halves = 16)
+{
+    return static_cast<uint64_t>(groups >> 4 | 1u << 14 | 2u << 29) << 32 | (addr >> 4 | halves >> 4 << 16);
+}
+
+// Four MMAs D (+)= A B whose operands, both in shared memory, are kA and kB (descriptor
+// units of 16 bytes) apart; the first one overwrites D unless `accumulate`.  All lanes
+// run it and one issues: with the election inside, the operands stay uniform, and the
+// warp issues an MMA in 24 cycles where a branch around it took 40, a branch on the
+// lane's number 64.
+template <int kA, int kB>
+__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "setp.ne.b32 q, %4, 0;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t"
+        "add.u64 x, %1, %5;\n\tadd.u64 y, %2, %6;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, 1;\n\t"
+        "add.u64 x, x, %5;\n\tadd.u64 y, y, %6;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, 1;\n\t"
+        "add.u64 x, x, %5;\n\tadd.u64 y, y, %6;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, 1;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kA), "n"(kB)
+        : "memory");
+}
+// Arrives on bar once every MMA that the elected lane issued before has completed.
+__device__ __forceinline__ void commit_elected(uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void expect_elected(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+        "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "r"(bytes)
+        : "memory");
+}
 // Bounded wait that also gives up once another role has aborted.
 __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, const volatile int *abort)
 {
