@@ -20,7 +20,7 @@
 //    the tensor cores run the other tile's products.
 //  * Q of both tiles takes 96 KB (Dn = 128), a block's K and V 80: what is left for them
 //    holds one block and a half.  So the ring's slots are single chunks of [128 keys]
-//    [64 dims], loaded and given back one by one in the order of their use.  The two
+//    [64 dims], in the order of their use: K, V, the next K.  The two
 //    halves of V may lie at either end of the ring: their distance goes into the operand,
 //    and the half with the lower dims into the lower slot.
 //  * Tiles begin at multiples of 128 tokens, so a tile sees its last block by a triangle
@@ -51,6 +51,7 @@ constexpr int kParts = 2;  // a block's P is handed to the MMAs in parts
 constexpr int kPart = kM / kParts;
 constexpr int kQueue = 4;  // items looked up ahead
 constexpr int kChunk = kM * 128;  // bytes of [128 rows][64 bf16]
+constexpr int kTurns = 4;  // barriers of the blocks in turn: more than any role is ahead of another
 constexpr unsigned kNone = 0xffffu;
 
 template <int DN> struct LpGeom {
@@ -60,7 +61,7 @@ template <int DN> struct LpGeom {
     static constexpr int kOCol = 2 * kM;
     static_assert(kOCol + 2 * DN <= 512 && NS >= CK + CV && NS % kProducers == 0, "TMEM and the ring");
     struct Small {
-        uint64_t full[NS], empty[NS];
+        uint64_t k_full[kTurns], v_full[kTurns], k_done[kTurns], v_done[kTurns];  // block by block
         uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][kParts], o_full[2], o_free[2], l_full[2];
         uint64_t item_full[kQueue], item_empty[kQueue], drain;
         uint64_t done[2], out_sync;  // an item's outputs are written; the output warps meet
@@ -169,9 +170,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     if (warp == 0) {
-        if (lane < NS) {
-            mbar_init(&sm.full[lane], 1);
-            mbar_init(&sm.empty[lane], 1);
+        if (lane < kTurns) {
+            mbar_init(&sm.k_full[lane], 1);
+            mbar_init(&sm.v_full[lane], 1);
+            mbar_init(&sm.k_done[lane], 1);
+            mbar_init(&sm.v_done[lane], 1);
         }
         if (lane < 2) {
             mbar_init(&sm.q_full[lane], 1);
@@ -228,12 +231,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kProducerWarp || warp == kProducerWarp + 1) {
         // ------------------------------------------------------- copies
-        // The ring's chunks in turn: K (its own dims, then the rotated ones) and V of a
-        // block, warp by warp; Q of tile t from warp t.
+        // One warp loads K (its own dims, then the rotated ones) and Q of tile 0, the other V
+        // and Q of tile 1.  A chunk's slot is free when the block that had it NS chunks ago
+        // has been used.
         const uint32_t mine = warp - kProducerWarp;
-        uint32_t c = 0;  // chunks, of both warps
-        uint32_t qn = 0; // Q tiles of this warp
-        uint32_t issued = 0;
+        uint32_t b = 0;   // blocks
+        uint32_t qn = 0;  // Q tiles of this warp
+        uint64_t *const filled = mine ? sm.v_full : sm.k_full;
         bool ok = true;
         for (unsigned k = 0; ok; ++k) {
             LpItem it;
@@ -253,45 +257,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  it.row0 + it.tok0 + static_cast<int>(mine) * kM, &sm.q_full[mine]);
                 ++qn;
             }
-            for (int j = 0; j < it.blocks && ok; ++j) {
-#pragma unroll 1
-                for (int i = 0; i < CB; ++i, ++c) {
-                    if (c % kProducers != mine)
+            for (int j = 0; j < it.blocks && ok; ++j, ++b) {
+                const int row = it.row0 + j * kM;
+                uint64_t *bar = &filled[b % kTurns];
+                const uint32_t v_slot = slot_of(b * CB + CK);
+                bool asked = false;
+#pragma unroll
+                for (int i = 0; i < CB; ++i) {
+                    if ((i >= CK) != (mine == 1))
                         continue;
-                    const uint32_t slot = slot_of(c);
-                    if (c >= NS)
-                        ok = warp_sleep_wait(&sm.empty[slot], (c / NS - 1) & 1, abort);
+                    const uint32_t c = b * CB + i, slot = slot_of(c);
+                    if (c >= NS && ok) {
+                        const uint32_t was = c - NS, block = was / CB;
+                        uint64_t *done = was % CB < CK ? sm.k_done : sm.v_done;
+                        ok = warp_sleep_wait(&done[block % kTurns], (block / kTurns) & 1, abort);
+                    }
                     if (!ok)
                         break;
-                    expect_elected(&sm.full[slot], kChunk);
+                    if (!asked)
+                        expect_elected(bar, (mine ? CV : CK) * kChunk);
+                    asked = true;
                     const uint32_t dst = smem0 + Geo::kRing + slot * kChunk;
-                    const int row = it.row0 + j * kM;
-                    ++issued;
                     if (p.drop_first_copy && blockIdx.x == 0 && c == 0)
                         continue;
                     if (i < CK - 1) {
-                        load_elected(dst, &maps.k, 64 * i, it.head, row, &sm.full[slot]);
+                        load_elected(dst, &maps.k, 64 * i, it.head, row, bar);
                     } else if (i == CK - 1) {
-                        load_elected(dst, &maps.kr, 0, 0, row, &sm.full[slot]);
+                        load_elected(dst, &maps.kr, 0, 0, row, bar);
                     } else {
                         // V's halves at the ends of the ring trade places.
-                        const uint32_t first = slot_of(c - (i - CK));
-                        const int half = CV == 2 && first == NS - 1 ? 1 - (i - CK) : i - CK;
-                        load_elected(dst, &maps.v, 64 * half, it.head, row, &sm.full[slot]);
+                        const int half = CV == 2 && v_slot == NS - 1 ? 1 - (i - CK) : i - CK;
+                        load_elected(dst, &maps.v, 64 * half, it.head, row, bar);
                     }
                 }
+                if (!ok && asked)
+                    ++b;  // its first copies are under way
             }
         }
         if (!ok && lane == 0) {
             set_status(pi.status, PKV_ERR_TIMEOUT);
             *abort = 1;
         }
-        // Every copy still in flight lands before the CTA exits: this warp's last NS / 2
-        // slots, whose chunks were issued in turn.
+        // Every copy still in flight lands before the CTA exits.  (One whose block was not
+        // asked for whole is waited for until the limit.)
         if (lane == 0) {
-            constexpr uint32_t kOwn = NS / kProducers;
-            for (uint32_t x = issued > kOwn ? issued - kOwn : 0; x < issued; ++x)
-                sleep_wait(&sm.full[x % kOwn * kProducers + mine], (x / kOwn) & 1, no_abort);
+            for (uint32_t x = b > kTurns ? b - kTurns : 0; x < b; ++x)
+                sleep_wait(&filled[x % kTurns], (x / kTurns) & 1, no_abort);
             if (qn > 0)
                 sleep_wait(&sm.q_full[mine], (qn - 1) & 1, no_abort);
         }
@@ -332,15 +343,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t id_s0 = tc_idesc(kM, 0, false) | (pi.negate ? 1u << 13 : 0u);
         constexpr uint32_t kIdPV = tc_idesc(kM, DN, true);
         const uint64_t qd = operand(smem0, 1024), kd = operand(smem0 + Geo::kRing, 1024);
-        uint32_t c = 0;                            // chunk of K of the block whose scores come next
+        uint32_t b = 0;                            // the block whose scores come next
         uint32_t q_par = 0, o_par = 3, p_par = 0;  // bit t
         unsigned k = 0;
         bool ok = true;
         LpItem it, next;
-        auto wait_chunk = [&](uint32_t x) {
-            return warp_sleep_wait(&sm.full[slot_of(x)], (x / NS) & 1, abort);
-        };
-        // Scores of tile t with the block at chunk c: `first` of its users waits for it,
+        // Scores of tile t with block b: `first` of its users waits for it,
         // `last` gives it back; the tile's `final` one gives Q back.
         auto scores = [&](int t, int cols, bool first, bool last, bool fresh, bool final) {
             if (fresh) {
@@ -348,19 +356,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 q_par ^= 1u << t;
             }
             const uint32_t id = id_s0 | static_cast<uint32_t>(cols >> 3) << 17;
+            if (first)
+                ok = ok && warp_sleep_wait(&sm.k_full[b % kTurns], (b / kTurns) & 1, abort);
+            if (!ok)
+                return;
+            tc_fence_after();
 #pragma unroll
-            for (int i = 0; i < CK; ++i) {
-                if (first)
-                    ok = ok && wait_chunk(c + i);
-                if (!ok)
-                    return;
-                tc_fence_after();
-                mma4<2, 2>(tmem + t * kM, qd + (t * CK + i) * (kChunk >> 4), kd + slot_of(c + i) * (kChunk >> 4), id,
-                           i > 0);
-                if (last)
-                    commit_elected(&sm.empty[slot_of(c + i)]);
-            }
+            for (int i = 0; i < CK; ++i)
+                mma4<2, 2>(tmem + t * kM, qd + (t * CK + i) * (kChunk >> 4),
+                           kd + slot_of(b * CB + i) * (kChunk >> 4), id, i > 0);
             commit_elected(&sm.s_full[t]);
+            if (last)
+                commit_elected(&sm.k_done[b % kTurns]);
             if (final)
                 commit_elected(&sm.q_empty[t]);
         };
@@ -376,8 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         while (more && ok) {
             for (int j = 0; j < it.blocks && ok; ++j) {
-                const uint32_t vc = c + CK;  // V of block j follows its K
-                c += CB;                     // and then comes the next block's
+                const uint32_t vb = b++;  // V of this block, K of the next
                 const bool end = j + 1 == it.blocks;
                 if (end) {
                     ok = next_item(k++, next);
@@ -385,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok)
                         break;
                 }
-                const uint32_t vs = slot_of(vc);
+                const uint32_t vs = slot_of(vb * CB + CK);
                 const bool split = CV == 2 && vs == NS - 1;
                 const uint64_t vd = operand(smem0 + Geo::kRing + (split ? 0 : vs) * kChunk, 1024,
                                             split ? (NS - 1) * kChunk : kChunk);
@@ -397,9 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             o_par ^= 1u << t;
                         }
                         if (t == 0 || j >= it.nb[0])
-#pragma unroll
-                            for (int i = 0; i < CV; ++i)
-                                ok = ok && wait_chunk(vc + i);
+                            ok = ok && warp_sleep_wait(&sm.v_full[vb % kTurns], (vb / kTurns) & 1, abort);
                         const int steps = cols_of(it, t, j) / 16;
                         const uint32_t d = tmem + Geo::kOCol + t * DN;
 #pragma unroll
@@ -423,9 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok)
                             break;
                         if (t == 1 || j >= it.nb[1])
-#pragma unroll
-                            for (int i = 0; i < CV; ++i)
-                                commit_elected(&sm.empty[slot_of(vc + i)]);
+                            commit_elected(&sm.v_done[vb % kTurns]);
                         if (j + 1 == it.nb[t])
                             commit_elected(&sm.o_full[t]);
                     }
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr float kLazy = MmaSoftmax::kLazy;
         uint32_t cnt = 0;    // blocks of this tile
         uint32_t items = 0;  // its items
-        uint32_t base = 0;   // chunk of the item's first K
+        uint32_t base = 0;   // the item's first block
         bool failed = false;
         for (unsigned k = 0; !failed; ++k) {
             LpItem it;
@@ -528,12 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (tail) {
                     // V of the last block: rows past the sequence become zero, and so do
                     // values that are not finite, which are noted.
-                    const uint32_t vc = base + j * CB + CK, vs = slot_of(vc);
-                    bool there = true;
-#pragma unroll
-                    for (int i = 0; i < CV; ++i)
-                        there = warp_wait(&sm.full[slot_of(vc + i)], ((vc + i) / NS) & 1, abort) && there;
-                    if (!there) {
+                    const uint32_t vb = base + j, vs = slot_of(vb * CB + CK);
+                    if (!warp_wait(&sm.v_full[vb % kTurns], (vb / kTurns) & 1, abort)) {
                         failed = true;
                         break;
                     }
@@ -598,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive(&sm.p_full[t][part]);
                 }
             }
-            base += CB * it.blocks;
+            base += it.blocks;
             if (failed)
                 break;
             if (nb == 0)
