@@ -23,6 +23,15 @@
 // fill as a whole, 64 bytes a thread; tokens of part-filled pages are written
 // element by element.  A page belongs to the CTA that has its first token, which
 // loads up to 15 tokens past its own.
+//
+// What bounds it: bytes in flight.  A row's numbers are kept as loaded until they are
+// used; with the registers that saves four CTAs fit an SM and a warp has two sets of
+// heads on their way.  A chat batch (128 prompts of 256 to 512 tokens, 64/8 heads, bf16):
+// 366 us, 5.4 TB/s (80% of a plain copy); as f32 numbers and three CTAs 417 us; one set 381,
+// four (which spill) 416 us.  With an fp8 cache of heads of 64 (37 prompts of up to 1000
+// tokens, 24/2 heads) 41 us, 4.0 TB/s.  The latent rows of 16 prompts of 512 to 4096 tokens
+// with 32 query heads: 94 us, 4.6 TB/s (their 128-byte pieces lie 384 and 1152 bytes apart);
+// two sets or four CTAs 95 to 104 us.
 #include "pkv_convert.cuh"
 #include "pkv_latent.h"
 
@@ -39,16 +48,44 @@ struct Vec8 {
     float x[8];
 };
 
+// 8 numbers as they lie in memory: rows are read once and kept so until they are used,
+// in half the registers for bf16.
+template <typename In> struct Raw8 {
+    uint4 w[sizeof(In) / 2];
+};
+__device__ __forceinline__ uint4 load_once(const void *p)
+{
+    uint4 v;
+    asm("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+template <typename In> __device__ __forceinline__ Raw8<In> load_raw(const In *p)
+{
+    Raw8<In> r;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(In)) / 2; ++i)
+        r.w[i] = load_once(reinterpret_cast<const uint4 *>(p) + i);
+    return r;
+}
+__device__ __forceinline__ Vec8 widen(const Raw8<float> &r)
+{
+    const uint4 a = r.w[0], b = r.w[1];
+    return {{__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w),
+             __uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)}};
+}
+__device__ __forceinline__ Vec8 widen(const Raw8<__nv_bfloat16> &r)
+{
+    const uint4 a = r.w[0];
+    return {{bf16_lo(a.x), bf16_hi(a.x), bf16_lo(a.y), bf16_hi(a.y), bf16_lo(a.z), bf16_hi(a.z), bf16_lo(a.w),
+             bf16_hi(a.w)}};
+}
+// 8 of the table's numbers, which neighbouring warps read too.
 __device__ __forceinline__ Vec8 load8(const float *p)
 {
     const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
     return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-}
-__device__ __forceinline__ Vec8 load8(const __nv_bfloat16 *p)
-{
-    const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    return {{bf16_lo(a.x), bf16_hi(a.x), bf16_lo(a.y), bf16_hi(a.y), bf16_lo(a.z), bf16_hi(a.z), bf16_lo(a.w),
-             bf16_hi(a.w)}};
 }
 __device__ __forceinline__ void store8(float *p, const Vec8 &v)
 {
@@ -76,10 +113,18 @@ struct Unit {
 
     __device__ __forceinline__ void init(const RopeTokens &t, int u, int pos)
     {
+        place(t, u);
+        angles(t, u, pos);
+    }
+    __device__ __forceinline__ void place(const RopeTokens &t, int u)
+    {
         turned = 16 * u < t.rot;
         const bool halves = turned && !t.interleaved;
         lo = halves ? 8 * u : 16 * u;
         hi = halves ? t.rot / 2 + 8 * u : 16 * u + 8;
+    }
+    __device__ __forceinline__ void angles(const RopeTokens &t, int u, int pos)
+    {
         if (turned) {
             const float *row = t.table + static_cast<size_t>(pos) * t.rot + 8 * u;
             c = load8(row);
@@ -120,7 +165,8 @@ __device__ __forceinline__ bool token_ok(const RopeTokens &t, int i, int64_t &sl
 }
 
 // Warp `w` of the queries' warps: token w / groups, every groups-th set of heads.
-template <typename In, int kDim>
+// kDeep: sets of heads whose loads are on their way together.
+template <typename In, int kDim, int kDeep>
 __device__ __forceinline__ void rotate_queries(const RopeTokens &t, const RopeQuery &q, int64_t w, int groups)
 {
     constexpr int kUnits = kDim / 16, kAtOnce = 32 / kUnits;  // heads in a warp
@@ -136,24 +182,24 @@ __device__ __forceinline__ void rotate_queries(const RopeTokens &t, const RopeQu
     unit.init(t, lane % kUnits, pos);
     const In *src = static_cast<const In *>(q.q) + i * q.stride;
     In *dst = static_cast<In *>(q.out) + i * q.out_stride;
-    constexpr int kDeep = 2;  // sets of heads whose loads are on their way together
     for (int h0 = group * kAtOnce + lane / kUnits; h0 < q.num_heads; h0 += kDeep * groups * kAtOnce) {
-        Vec8 a[kDeep], b[kDeep];
+        Raw8<In> ra[kDeep], rb[kDeep];
 #pragma unroll
         for (int j = 0; j < kDeep; ++j) {
             const int h = h0 + j * groups * kAtOnce;
             if (h < q.num_heads) {
-                a[j] = load8(src + h * q.head + unit.lo);
-                b[j] = load8(src + h * q.head + unit.hi);
+                ra[j] = load_raw(src + h * q.head + unit.lo);
+                rb[j] = load_raw(src + h * q.head + unit.hi);
             }
         }
 #pragma unroll
         for (int j = 0; j < kDeep; ++j) {
             const int h = h0 + j * groups * kAtOnce;
             if (h < q.num_heads) {
-                unit.apply(a[j], b[j], t.interleaved);
-                store8(dst + h * q.out_head + unit.lo, a[j]);
-                store8(dst + h * q.out_head + unit.hi, b[j]);
+                Vec8 a = widen(ra[j]), b = widen(rb[j]);
+                unit.apply(a, b, t.interleaved);
+                store8(dst + h * q.out_head + unit.lo, a);
+                store8(dst + h * q.out_head + unit.hi, b);
             }
         }
     }
@@ -311,15 +357,17 @@ __device__ __forceinline__ void write_tile(const RopeAppendParams &p, unsigned c
             continue;
         const int64_t i = t0 + e;
         Unit unit;
-        unit.init(t, lane % kUnits, s_pos[kHalo + e]);
-        Vec8 a = load8(k + i * p.k_stride + unit.lo), b = load8(k + i * p.k_stride + unit.hi);
-        const Vec8 va = load8(v + i * p.v_stride + unit.lo), vb = load8(v + i * p.v_stride + unit.hi);
+        unit.place(t, lane % kUnits);
+        const Raw8<In> ka = load_raw(k + i * p.k_stride + unit.lo), kb = load_raw(k + i * p.k_stride + unit.hi);
+        const Raw8<In> va = load_raw(v + i * p.v_stride + unit.lo), vb = load_raw(v + i * p.v_stride + unit.hi);
+        unit.angles(t, lane % kUnits, s_pos[kHalo + e]);
+        Vec8 a = widen(ka), b = widen(kb);
         unit.apply(a, b, t.interleaved);
         Code *dk = reinterpret_cast<Code *>(sk + e * kRow), *dv = reinterpret_cast<Code *>(sv + e * kRow);
         put_codes(dk + unit.lo, a, p.kv_dtype, p.k_scale);
         put_codes(dk + unit.hi, b, p.kv_dtype, p.k_scale);
-        put_codes(dv + unit.lo, va, p.kv_dtype, p.v_scale);
-        put_codes(dv + unit.hi, vb, p.kv_dtype, p.v_scale);
+        put_codes(dv + unit.lo, widen(va), p.kv_dtype, p.v_scale);
+        put_codes(dv + unit.hi, widen(vb), p.kv_dtype, p.v_scale);
     }
     __syncthreads();
 
@@ -364,8 +412,10 @@ __device__ __forceinline__ void write_tile(const RopeAppendParams &p, unsigned c
 }
 
 // CTAs [0, kv_ctas) write the caches, the others turn the queries.
+// The CTAs of an SM (four, with f32 three) are as many as the registers allow without
+// spilling more than a word.
 template <typename In, typename Code, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(In) == 2 ? 4 : 3)
     rope_append_kernel(const RopeAppendParams p, int tile, int kv_ctas, int groups)
 {
     extern __shared__ __align__(16) unsigned char smem_rope[];
@@ -374,7 +424,7 @@ __global__ void __launch_bounds__(kThreads)
         write_tile<In, Code, D>(p, smem_rope, b / p.num_kv_heads * tile, tile, b % p.num_kv_heads);
         return;
     }
-    rotate_queries<In, D>(p.t, p.q, static_cast<int64_t>(b - kv_ctas) * kWarps + (threadIdx.x >> 5), groups);
+    rotate_queries<In, D, sizeof(In) == 2 ? 2 : 1>(p.t, p.q, static_cast<int64_t>(b - kv_ctas) * kWarps + (threadIdx.x >> 5), groups);
 }
 
 // Sets of heads that a token's queries are shared between: one, unless there
@@ -389,9 +439,12 @@ int query_groups(int tokens, int heads, int at_once)
 template <typename In, typename Code, int D>
 pkv_status launch_append(const RopeAppendParams &p, cudaStream_t stream)
 {
-    // Tokens of a CTA: as many as leave two CTAs to an SM, at most 64.
+    // Tokens of a CTA: as many as leave two CTAs to an SM, at most 64, or 32 for f32
+    // caches, whose tiles of 64 (83 KB) leave room for two CTAs only (64 prompts of 256 to 512
+    // tokens, 32/8 heads, f32: 284 us against 256).
+    constexpr int kMost = sizeof(Code) == 4 ? kTile / 2 : kTile;
     const long want = static_cast<long>(p.t.num_tokens) * p.num_kv_heads / (2L * device_sm_count());
-    const int tile = want >= kTile ? kTile : want < 1 ? 1 : static_cast<int>(want);
+    const int tile = want >= kMost ? kMost : want < 1 ? 1 : static_cast<int>(want);
     const long kv = (static_cast<long>(p.t.num_tokens) + tile - 1) / tile * p.num_kv_heads;
     int groups = 1;
     long warps = 0;
@@ -403,7 +456,7 @@ pkv_status launch_append(const RopeAppendParams &p, cudaStream_t stream)
     if (grid > 0x7fffffffL)
         return PKV_ERR_UNSUPPORTED;
     const int smem = 2 * (tile + kHalo) * TileGeom<Code, D>::kRow;
-    constexpr int most = 2 * (kTile + kHalo) * TileGeom<Code, D>::kRow;
+    constexpr int most = 2 * (kMost + kHalo) * TileGeom<Code, D>::kRow;
     if (most > 48 * 1024) {
         static ContextCache cache;
         int set = 0;
@@ -440,12 +493,12 @@ template <typename In> pkv_status launch_append_in(const RopeAppendParams &p, cu
 // CTAs [0, row_ctas): a warp per token copies its latent vector and turns its
 // key; the others turn the queries.
 template <typename In, typename Out>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
     latent_append_kernel(const LatentAppendParams p, int row_ctas, int groups)
 {
     const int b = static_cast<int>(blockIdx.x), lane = threadIdx.x & 31;
     if (b >= row_ctas) {
-        rotate_queries<In, kRopeDim>(p.t, p.q, static_cast<int64_t>(b - row_ctas) * kWarps + (threadIdx.x >> 5),
+        rotate_queries<In, kRopeDim, 1>(p.t, p.q, static_cast<int64_t>(b - row_ctas) * kWarps + (threadIdx.x >> 5),
                                      groups);
         return;
     }
@@ -460,15 +513,15 @@ __global__ void __launch_bounds__(kThreads)
     const In *src = static_cast<const In *>(p.latent) + i * p.latent_stride;
     for (int d = 8 * lane; d < p.latent_dim; d += 256) {
         if constexpr (sizeof(In) == 2 && sizeof(Out) == 2)  // the bits
-            *reinterpret_cast<uint4 *>(dst + d) = *reinterpret_cast<const uint4 *>(src + d);
+            *reinterpret_cast<uint4 *>(dst + d) = load_once(src + d);
         else
-            store8(dst + d, load8(src + d));
+            store8(dst + d, widen(load_raw(src + d)));
     }
     if (lane < kRopeDim / 16) {
         Unit unit;
         unit.init(p.t, lane, pos);
         const In *key = static_cast<const In *>(p.k_rope) + i * p.k_rope_stride;
-        Vec8 a = load8(key + unit.lo), c = load8(key + unit.hi);
+        Vec8 a = widen(load_raw(key + unit.lo)), c = widen(load_raw(key + unit.hi));
         unit.apply(a, c, p.t.interleaved);
         store8(dst + p.latent_dim + unit.lo, a);
         store8(dst + p.latent_dim + unit.hi, c);
