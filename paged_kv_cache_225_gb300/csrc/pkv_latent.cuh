@@ -38,54 +38,46 @@ struct LatentPiece {
 
 // A team's walk over its range, by one warp.
 struct LatentWalk {
-    long left;   // tiles still to hand out
-    int s, j;    // where they begin
+    int left;  // tiles still to hand out
+    int s, j;  // where they begin
 
     __device__ __forceinline__ void init(const LatentDecodeParams &p, int team, int lane, bool report)
     {
-        // A lane has a run of neighbouring sequences.
-        const int per = (p.num_seqs + 31) / 32;
+        // A lane has a run of neighbouring sequences.  The call has less than 2^31 tiles.
+        const int per = (p.num_seqs + 31) >> 5;
         const int lo = min(per * lane, p.num_seqs), hi = min(lo + per, p.num_seqs);
-        long mine = 0;
+        unsigned mine = 0;
         for (int i = lo; i < hi; ++i)
             mine += latent_tiles(latent_len(p, i, report));
-        long upto = mine;
+        unsigned upto = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const long y = __shfl_up_sync(kFullMask, upto, d);
+            const unsigned y = __shfl_up_sync(kFullMask, upto, d);
             if (lane >= d)
                 upto += y;
         }
-        const long total = __shfl_sync(kFullMask, upto, 31);
+        const unsigned total = __shfl_sync(kFullMask, upto, 31);
         // Every team that works has a tile at least.
-        const long teams = total < p.teams ? total : p.teams;
+        const unsigned teams = min(total, static_cast<unsigned>(p.teams));
         left = 0;
         s = j = 0;
-        if (team >= teams)
+        if (team >= static_cast<int>(teams))
             return;
         // The first total % teams teams have a tile more.
-        long each, extra;
-        if (total >> 31 == 0) {
-            each = static_cast<unsigned>(total) / static_cast<unsigned>(teams);
-            extra = static_cast<unsigned>(total) % static_cast<unsigned>(teams);
-        } else {
-            each = total / teams;
-            extra = total % teams;
-        }
-        const long begin = each * team + min(static_cast<long>(team), extra);
-        left = each + (team < extra ? 1 : 0);
+        const unsigned each = total / teams, extra = total - each * teams;
+        const unsigned begin = each * team + min(static_cast<unsigned>(team), extra);
+        left = each + (team < static_cast<int>(extra) ? 1 : 0);
         const unsigned past = __ballot_sync(kFullMask, upto > begin);
         const int at = __ffs(past) - 1;
         if (lane == at) {
-            long b = begin - (upto - mine);
-            s = lo;
-            for (;; ++s) {
+            int b = begin - (upto - mine);
+            for (s = lo; per > 1; ++s) {
                 const int n = latent_tiles(latent_len(p, s, false));
                 if (b < n)
                     break;
                 b -= n;
             }
-            j = static_cast<int>(b);
+            j = b;
         }
         s = __shfl_sync(kFullMask, s, at);
         j = __shfl_sync(kFullMask, j, at);
@@ -109,7 +101,7 @@ struct LatentWalk {
         r.len = latent_len(p, s, false);
         r.tiles = latent_tiles(r.len);
         r.first = j;
-        r.last = p.whole ? r.tiles : static_cast<int>(min(static_cast<long>(r.tiles), j + left));
+        r.last = p.whole ? r.tiles : min(r.tiles, j + left);
         left -= r.last - r.first;
         ++s;
         j = 0;

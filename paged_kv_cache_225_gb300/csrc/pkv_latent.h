@@ -83,6 +83,7 @@ struct LatentPromptParams {
     int drop_first_copy; // test hook: never issue the first copy of CTA 0
 };
 
+constexpr int kLatentSms = 152;    // SMs that a plan counts on
 constexpr int kLatentTokens = 64;  // tokens of a tile: the decode's unit of work
 constexpr int kLatentMaxSeqs = 1 << 20;  // every CTA reads all lengths once
 

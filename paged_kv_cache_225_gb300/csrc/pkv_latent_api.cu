@@ -176,6 +176,9 @@ static pkv_status plan_decode(LatentDecodeParams &p, pkv_dtype dtype, int num_se
     if (!is_float(dtype) || (latent_dim != 256 && latent_dim != 512) || rope_dim != kRopeDim ||
         block_size != kBlockSize || num_q_heads > 128 || num_seqs > kLatentMaxSeqs)
         return PKV_ERR_UNSUPPORTED;
+    // Tiles are counted in 32 bits, the ends of a team's range included.
+    if (static_cast<int64_t>(num_seqs) * (max_seq_len / kLatentTokens + 1) >= INT64_C(1) << 30)
+        return PKV_ERR_UNSUPPORTED;
     p.num_seqs = num_seqs;
     p.num_heads = num_q_heads;
     p.latent_dim = latent_dim;

@@ -257,29 +257,35 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const Late
 
 // ------------------------------------------------------------------ joining
 
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 4;  // of a block in which each has a unit of its own
 
 // Joins the pieces of cut sequences.  blockIdx.x is a sequence (fewer sequences than
 // teams) or a team but the first, which stands for the sequence that its start cuts if
 // that begins in the team before.  For one head and 128 of its dims
 //   M = max_i m_i,  out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i
-// over the pieces i.  A warp takes all pieces of its head and dims, or, with many
-// pieces to a sequence (kShared), the block's warps take every eighth piece of one head
-// and dims and add up in order.  Either way the result does not depend on who wrote first.
-template <typename T, int R, bool kShared>
-__global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const LatentDecodeParams p, int by_sequence)
+// over the pieces i, four at a time.  A warp has 256 dims of a head and all pieces, or,
+// with many pieces to a sequence, kShare warps take them in turn for 128 dims and add up
+// in order.  Either way the result does not depend on who wrote first.
+//
+// What bounds it: three dependent trips to L2 and the partial sums, which are there (64
+// sequences of 64 heads, 28 MB: 8.5 us of 62; a warp to 128 dims 11.4, to 512 9).
+template <typename T, int R, int kShare>
+__global__ void __launch_bounds__(32 * (kShare > 1 ? kShare : kMergeWarps))
+    latent_merge_kernel(const LatentDecodeParams p, int by_sequence)
 {
-    constexpr int kParts = R / 128;
-    __shared__ float4 s_sum[kMergeWarps][32];
-    __shared__ float s_total[kMergeWarps];
+    constexpr bool kShared = kShare > 1;
+    constexpr int kVec = kShared ? 1 : 2;
+    constexpr int kParts = R / 128 / kVec;
+    __shared__ float4 s_sum[kShare][32];
+    __shared__ float2 s_ml[kShare];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int unit = kShared ? blockIdx.y : blockIdx.y * kMergeWarps + warp;
-    const int h = unit / kParts, d = unit % kParts * 128 + 4 * lane;
+    const int h = unit / kParts, d = unit % kParts * (128 * kVec) + 4 * lane;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (h >= p.num_heads)
         return;
-    // The sequence that a team's start cuts, five lanes' worth: the teams are at most 304.
-    constexpr int kMost = (2 * 152 + 31) / 32;
+    // The sequence that each team's start cuts, lane by lane; at most 304 teams.
+    constexpr int kMost = (2 * kLatentSms + 31) / 32;
     int cut[kMost];
 #pragma unroll
     for (int i = 0; i < kMost; ++i)
@@ -308,49 +314,85 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const La
         const size_t slot = t < team ? 2 * t + 1 : 2 * t;
         return (slot * p.head_tiles + ht) * p.tile_heads + hh;
     };
-    float top = -INFINITY;
-    for (int t = team - 1 + lane; t <= last; t += 32)
-        top = fmaxf(top, p.part_ml[row(t)].x);
+    // A few pieces at a time, their loads before anything that needs one.
+    constexpr int kDeep = 4;
+    float4 sums[kVec] = {};
+    float top = -INFINITY, total = 0.f;
+    for (int t0 = team - 1 + (kShared ? kDeep * warp : 0); t0 <= last; t0 += kDeep * kShare) {
+        float4 x[kDeep][kVec];
+        float2 ml[kDeep];
 #pragma unroll
-    for (int w = 16; w >= 1; w >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, w));
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    float total = 0.f;
-#pragma unroll 8
-    for (int t = team - 1 + (kShared ? warp : 0); t <= last; t += kShared ? kMergeWarps : 1) {
-        const float2 ml = p.part_ml[row(t)];
-        const float4 x = *reinterpret_cast<const float4 *>(p.part + row(t) * R + d);
-        const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
-        total = fmaf(w, ml.y, total);
-        sum.x = fmaf(w, x.x, sum.x);
-        sum.y = fmaf(w, x.y, sum.y);
-        sum.z = fmaf(w, x.z, sum.z);
-        sum.w = fmaf(w, x.w, sum.w);
+        for (int i = 0; i < kDeep; ++i) {
+            const int t = min(t0 + i, last);
+            ml[i] = p.part_ml[row(t)];
+#pragma unroll
+            for (int v = 0; v < kVec; ++v)
+                x[i][v] = *reinterpret_cast<const float4 *>(p.part + row(t) * R + d + 128 * v);
+        }
+        float up = top;
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i)
+            up = fmaxf(up, ml[i].x);
+        const float old = top == -INFINITY ? 0.f : exp2f(top - up);
+        top = up;
+        total *= old;
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+            sums[v].x *= old;
+            sums[v].y *= old;
+            sums[v].z *= old;
+            sums[v].w *= old;
+        }
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) {
+            if (t0 + i > last)
+                break;
+            const float w = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - up);
+            total = fmaf(w, ml[i].y, total);
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) {
+                sums[v].x = fmaf(w, x[i][v].x, sums[v].x);
+                sums[v].y = fmaf(w, x[i][v].y, sums[v].y);
+                sums[v].z = fmaf(w, x[i][v].z, sums[v].z);
+                sums[v].w = fmaf(w, x[i][v].w, sums[v].w);
+            }
+        }
     }
     if constexpr (kShared) {
-        s_sum[warp][lane] = sum;
+        s_sum[warp][lane] = sums[0];
         if (lane == 0)
-            s_total[warp] = total;
+            s_ml[warp] = make_float2(top, total);
         __syncthreads();
         if (warp > 0)
             return;
+        top = -INFINITY;
 #pragma unroll
-        for (int i = 1; i < kMergeWarps; ++i) {
+        for (int i = 0; i < kShare; ++i)
+            top = fmaxf(top, s_ml[i].x);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        total = 0.f;
+#pragma unroll
+        for (int i = 0; i < kShare; ++i) {
             const float4 x = s_sum[i][lane];
-            sum.x += x.x;
-            sum.y += x.y;
-            sum.z += x.z;
-            sum.w += x.w;
-            total += s_total[i];
+            const float w = s_ml[i].x == -INFINITY ? 0.f : exp2f(s_ml[i].x - top);
+            total = fmaf(w, s_ml[i].y, total);
+            sum.x = fmaf(w, x.x, sum.x);
+            sum.y = fmaf(w, x.y, sum.y);
+            sum.z = fmaf(w, x.z, sum.z);
+            sum.w = fmaf(w, x.w, sum.w);
         }
+        sums[0] = sum;
     }
-    const size_t at = (static_cast<size_t>(s) * p.num_heads + h) * R + d;
-    const float4 y = make_float4(sum.x / total, sum.y / total, sum.z / total, sum.w / total);
-    if constexpr (sizeof(T) == 4)
-        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = y;
-    else
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
-            make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+        const size_t at = (static_cast<size_t>(s) * p.num_heads + h) * R + d + 128 * v;
+        const float4 y = make_float4(sums[v].x / total, sums[v].y / total, sums[v].z / total, sums[v].w / total);
+        if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = y;
+        else
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
+                make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+    }
 }
 
 template <int R> pkv_status launch_simt(const LatentDecodeParams &p, cudaStream_t stream)
@@ -370,14 +412,14 @@ template <int R> pkv_status launch_simt(const LatentDecodeParams &p, cudaStream_
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-template <typename T, int R, bool kShared> pkv_status launch_merge(const LatentDecodeParams &p, cudaStream_t stream)
+template <typename T, int R, int kShare> pkv_status launch_merge(const LatentDecodeParams &p, cudaStream_t stream)
 {
     const int by_sequence = p.num_seqs < p.teams;
-    const int units = p.num_heads * (R / 128);
+    const int units = p.num_heads * (R / 128) / (kShare > 1 ? 1 : 2);
     cudaLaunchConfig_t config = {};
     config.gridDim = dim3(by_sequence ? p.num_seqs : p.teams - 1,
-                          kShared ? units : (units + kMergeWarps - 1) / kMergeWarps);
-    config.blockDim = dim3(32 * kMergeWarps);
+                          kShare > 1 ? units : (units + kMergeWarps - 1) / kMergeWarps);
+    config.blockDim = dim3(32 * (kShare > 1 ? kShare : kMergeWarps));
     config.stream = stream;
     // Set up while the attention kernel runs.
     cudaLaunchAttribute early = {};
@@ -385,33 +427,43 @@ template <typename T, int R, bool kShared> pkv_status launch_merge(const LatentD
     early.val.programmaticStreamSerializationAllowed = 1;
     config.attrs = &early;
     config.numAttrs = 1;
-    return cudaLaunchKernelEx(&config, latent_merge_kernel<T, R, kShared>, p, by_sequence) == cudaSuccess
+    return cudaLaunchKernelEx(&config, latent_merge_kernel<T, R, kShare>, p, by_sequence) == cudaSuccess
                ? PKV_OK
                : PKV_ERR_CUDA;
 }
 template <typename T, int R> pkv_status launch_merge_by(const LatentDecodeParams &p, cudaStream_t stream)
 {
-    // Eight pieces to a sequence and more.
-    return p.teams >= 8 * p.num_seqs ? launch_merge<T, R, true>(p, stream) : launch_merge<T, R, false>(p, stream);
+    // Eight pieces to a sequence and more (4 x 32K tokens, 128 heads, 19 pieces: 57 us, alone
+    // or with eight warps 59), and 32 and more (32K tokens, 32 heads, 152 pieces: 25 us, with
+    // four warps 30, alone 45).
+    return p.teams >= 32 * p.num_seqs  ? launch_merge<T, R, 8>(p, stream)
+           : p.teams >= 8 * p.num_seqs ? launch_merge<T, R, 4>(p, stream)
+                                       : launch_merge<T, R, 1>(p, stream);
 }
 
 }  // namespace
 
-constexpr long kWholeTiles = 8;
+constexpr double kCut = 4, kCutAll = 1.5;
 
 size_t latent_plan(LatentDecodeParams &p, int dtype)
 {
     // fp32: two CTAs to an SM.  bf16: one.
     p.tile_heads = dtype == PKV_F32 || p.num_heads <= 16 ? 16 : p.num_heads <= 32 ? 32 : 64;
     p.head_tiles = (p.num_heads + p.tile_heads - 1) / p.tile_heads;
-    const long ctas = dtype == PKV_F32 ? 2 * 152 : 152;
+    const long ctas = dtype == PKV_F32 ? 2 * kLatentSms : kLatentSms;
     const long tiles = (static_cast<long>(p.max_len) + kLatentTokens - 1) / kLatentTokens;
     const long units = static_cast<long>(p.num_seqs) * (tiles > 1 ? tiles : 1);
     const long most = ctas / p.head_tiles;
-    // A sequence of up to kWholeTiles is not worth the second kernel.
-    p.whole = tiles <= kWholeTiles;
-    const long want = p.whole ? p.num_seqs : units;
-    p.teams = static_cast<int>(want < most ? want : most);
+    p.teams = static_cast<int>(units < most ? units : most);
+    // Cutting evens the teams out and costs partial sums and the second kernel, in tiles
+    // of a team about kCut and, by the share of the teams that cut, kCutAll more.  Without
+    // it a team has whole sequences, of which the longest counts.  The lengths are not
+    // known here: three quarters of the bound on average are supposed.
+    const double rounds = static_cast<double>((p.num_seqs + most - 1) / most) * tiles;
+    const double even = 0.75 * p.num_seqs * tiles / most;
+    p.whole = rounds <= even + kCut + kCutAll * p.teams / most;
+    if (p.whole && p.num_seqs < p.teams)
+        p.teams = p.num_seqs > 0 ? p.num_seqs : 1;
     const size_t rows = 2 * static_cast<size_t>(p.teams) * p.head_tiles * p.tile_heads;
     return (rows * (p.latent_dim * sizeof(float) + sizeof(float2)) + p.teams * sizeof(int2) + 255) / 256 * 256;
 }

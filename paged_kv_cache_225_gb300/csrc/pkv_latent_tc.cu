@@ -262,11 +262,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_mbar_init();
     }
+    if (warp == kScoreWarp && lane < 3) {
+        const CUtensorMap *map = lane == 0 ? &maps.q : lane == 1 ? &maps.a : &maps.b;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+    }
     if (warp == kProducerWarp) {
-        if (lane < 3) {
-            const CUtensorMap *map = lane == 0 ? &maps.q : lane == 1 ? &maps.a : &maps.b;
-            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-        }
         LatentWalk walk;
         walk.init(p, team, lane, blockIdx.x == 0);
         if (lane == 0)
