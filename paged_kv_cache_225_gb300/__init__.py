@@ -722,6 +722,7 @@ def _rows(t: torch.Tensor, what: str, dtype: torch.dtype, index: int):
 
 
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
+_CACHES = {**_FLOATS, torch.float8_e5m2: FP8_E5M2, torch.float8_e4m3fn: FP8_E4M3, torch.uint8: INT4}
 
 
 def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor,
@@ -858,18 +859,28 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pos
         Hq = qshape[1]
         qp, op = q.data_ptr(), q_out.data_ptr()
     pos, tab, slots, st = _new_tokens(positions, table, slot_mapping, status, T, index)
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _check(t, name, 4, torch.device("cuda", index))
-    N, Hkv2, D2, B = _pool_dims(k_cache)
-    if (vshape != kshape or Hkv2 != Hkv or D2 != D or v_cache.shape != k_cache.shape
-            or v_cache.dtype != k_cache.dtype):
+    if not isinstance(k_cache, torch.Tensor) or not isinstance(v_cache, torch.Tensor):
+        raise TypeError("k_cache and v_cache must be torch.Tensors")
+    ctype = k_cache.dtype
+    ccode = _CACHES.get(ctype)
+    if ccode is None:
+        raise TypeError(f"k_cache: unsupported dtype {ctype}")
+    kc = _ptr(k_cache, "k_cache", 4, ctype, index)
+    if v_cache.dtype is not ctype:
+        raise ValueError("k_cache and v_cache must have the same shape and dtype")
+    vc = _ptr(v_cache, "v_cache", 4, ctype, index)
+    cshape = k_cache.shape
+    N, Hkv2, D2, B = cshape
+    if ccode == INT4:
+        B *= 2  # tokens: two to a byte
+    if vshape != kshape or Hkv2 != Hkv or D2 != D or v_cache.shape != cshape:
         raise ValueError("inconsistent shapes")
     if N > _INT_MAX:
         raise ValueError("at most 2^31 - 1 pages")
     _launch("pkv_rope_append", index, stream,
             (qp, k.data_ptr(), v.data_ptr(), code, qs, ks, vs, pos, tab, table.shape[1], table.shape[0], slots, T,
-             Hq, Hkv, D, B, N, op, qos, k_cache.data_ptr(), v_cache.data_ptr(), _dtype_code(k_cache, "k_cache"),
-             float(k_scale), float(v_scale), FLAG_ROPE_INTERLEAVED if interleaved else 0, st))
+             Hq, Hkv, D, B, N, op, qos, kc, vc, ccode, float(k_scale), float(v_scale),
+             FLAG_ROPE_INTERLEAVED if interleaved else 0, st))
     return q_out
 
 
@@ -908,10 +919,12 @@ def latent_append(latent: torch.Tensor, k_rope: torch.Tensor, positions: torch.T
         H = qshape[1]
         qp, op = q_rope.data_ptr(), q_out.data_ptr()
     pos, tab, slots, st = _new_tokens(positions, table, slot_mapping, status, T, index)
-    _check(cache, "cache", 3, torch.device("cuda", index))
+    if not isinstance(cache, torch.Tensor):
+        raise TypeError("cache must be a torch.Tensor")
     ccode = _FLOATS.get(cache.dtype)
     if ccode is None:
         raise TypeError(f"cache: unsupported dtype {cache.dtype}")
+    cp = _ptr(cache, "cache", 3, cache.dtype, index)
     N, B, row = cache.shape
     if T2 != T or row != R + rope or table.shape[1] != rope:
         raise ValueError("inconsistent shapes")
@@ -919,7 +932,7 @@ def latent_append(latent: torch.Tensor, k_rope: torch.Tensor, positions: torch.T
         raise ValueError("at most 2^31 - 1 pages")
     _launch("pkv_latent_append", index, stream,
             (latent.data_ptr(), k_rope.data_ptr(), code, ls, rs, qp, qs, qh, pos, tab, table.shape[0], slots, T, H,
-             R, rope, B, N, op, qos, qoh, cache.data_ptr(), ccode, FLAG_ROPE_INTERLEAVED if interleaved else 0,
+             R, rope, B, N, op, qos, qoh, cp, ccode, FLAG_ROPE_INTERLEAVED if interleaved else 0,
              st))
     return q_out
 

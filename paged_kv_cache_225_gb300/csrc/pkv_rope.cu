@@ -56,7 +56,8 @@ template <typename In> struct Raw8 {
 __device__ __forceinline__ uint4 load_once(const void *p)
 {
     uint4 v;
-    asm("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+    // Not volatile: what is stored where it was read (queries in place) depends on it.
+    asm("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
@@ -412,8 +413,8 @@ __device__ __forceinline__ void write_tile(const RopeAppendParams &p, unsigned c
 }
 
 // CTAs [0, kv_ctas) write the caches, the others turn the queries.
-// The CTAs of an SM (four, with f32 three) are as many as the registers allow without
-// spilling more than a word.
+// The CTAs of an SM (four, with f32 three) are as many as the registers allow with next to
+// nothing spilled.
 template <typename In, typename Code, int D>
 __global__ void __launch_bounds__(kThreads, sizeof(In) == 2 ? 4 : 3)
     rope_append_kernel(const RopeAppendParams p, int tile, int kv_ctas, int groups)

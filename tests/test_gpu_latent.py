@@ -251,6 +251,75 @@ def test_streams_graphs_and_workspaces(dtype):
         decode(*b, SCALE, workspace=ws[:need // 2])
 
 
+@pytest.mark.parametrize("H,R,n", [(16, 512, 50), (64, 512, 900), (128, 256, 3000), (32, 512, 20000)])
+def test_bounded_wait_reports_timeout_and_recovers(H, R, n):
+    a = make([n, 33], H, R, BF16, 15)
+    want = decode(*a, SCALE)
+    out = torch.empty_like(want)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkv.latent_attn_decode(*a, SCALE, out, status=status, flags=pkv.FLAG_TEST_DROP_FIRST_COPY)
+    torch.cuda.synchronize()
+    assert int(status) == 5
+    assert torch.equal(decode(*a, SCALE), want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("S,bound", [(200000, 64), (200000, 4000), (1 << 20, 64)])
+def test_many_sequences_most_of_them_empty(S, bound, dtype):
+    H, R = 1, 256
+    g = torch.Generator(device=DEV).manual_seed(16)
+    lens = torch.zeros(S, dtype=torch.int32, device=DEV)
+    at = torch.randint(0, S, (50,), generator=g, device=DEV).unique()
+    lens[at] = torch.randint(1, 60, (len(at),), generator=g, device=DEV, dtype=torch.int32)
+    cache = torch.randn((8, 16, R + ROPE), generator=g, device=DEV).to(dtype)
+    tables = torch.randint(0, 8, (S, 4), generator=g, device=DEV, dtype=torch.int32)
+    if bound > 64:
+        tables = torch.cat([tables, tables.new_full((S, bound // 16 - 4), -1)], 1)
+    q = torch.randn((S, H, R + ROPE), generator=g, device=DEV).to(dtype)
+    out = decode(q, cache, tables, lens, SCALE, max_seq_len=bound)
+    few = torch.ones(S, dtype=torch.bool, device=DEV)
+    few[at] = False
+    assert not bool(out[few].any())
+    n = lens[at].tolist()
+    ref, mass, most = decode_reference(q[at], cache, tables[at], n, SCALE)
+    near(out[at], ref, mass, most, n, R + ROPE, SCALE)
+
+
+def test_sizes_past_the_plan_are_refused():
+    size = pkv.lib().pkv_latent_attn_workspace_size
+    assert size(pkv.BF16, 1 << 20, 16, 512, 64, 16, 1 << 16) == 0
+    assert size(pkv.BF16, 1 << 10, 16, 512, 64, 16, 1 << 20) > 0
+
+
+@pytest.mark.parametrize("R", [256, 512])
+@pytest.mark.parametrize("lens", [[4096] * 30, [100, 30000, 1, 64, 6000, 65, 63, 2, 10000], [513] * 152 + [700],
+                                  [1] * 100 + [9000] + [1] * 100])
+def test_the_same_with_cut_and_whole_sequences(lens, R):
+    # A loose bound changes the plan, not the result beyond its rounding.
+    q, cache, tables, lens_t = make(lens, 48, R, BF16, 17)
+    ref, mass, most = decode_reference(q, cache, tables, lens, SCALE)
+    near(decode(q, cache, tables, lens_t, SCALE), ref, mass, most, lens, R + ROPE, SCALE)
+    wide = torch.full((len(lens), 20000), -1, dtype=torch.int32, device=DEV)
+    wide[:, :tables.shape[1]] = tables
+    near(decode(q, cache, wide, lens_t, SCALE), ref, mass, most, lens, R + ROPE, SCALE)
+
+
+@pytest.mark.parametrize("H", [16, 64, 128])
+def test_scattered_scores_of_either_infinity(H):
+    # +inf scores make a NaN row, -inf ones weigh nothing; heads do not mix.
+    lens, R = [130, 700], 512
+    q, cache, tables, lens_t = make(lens, H, R, BF16, 18)
+    ok = check(q, cache, tables, lens_t, SCALE)
+    cache[int(tables[1, 20]), 3, R] = -INF
+    q[1, :, R] = 1.0
+    q[1, H // 2, R] = -1.0                              # this head sees +inf
+    q[1, H - 1, R] = 0.0                                # and this one 0 * inf
+    out = decode(q, cache, tables, lens_t, SCALE).float()
+    assert torch.isnan(out[1, H // 2]).all() and torch.isnan(out[1, H - 1]).all()
+    rest = [h for h in range(H) if h not in (H // 2, H - 1)]
+    assert torch.isfinite(out[1, rest]).all() and torch.equal(out[0], ok[0].float())
+
+
 # ------------------------------------------------------------ whole prompts
 
 def prompt(lens, H, D, dtype, seed, tail=0):
@@ -459,6 +528,79 @@ def test_prompt_streams_and_graphs(dtype):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(oa, want_a)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_prompt_bits_do_not_change(dtype):
+    lens = [700, 3, 0, 257, 128, 129]
+    a = prompt(lens, 6, 128, dtype, 27)
+    first = attend(*a, lens, SCALE)
+    for _ in range(5):
+        assert torch.equal(attend(*a, lens, SCALE), first)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_prompt_starts_that_step_back_end(dtype):
+    # Not valid, but the call ends, reports it and leaves rows of no sequence alone.
+    q, k, kr, v = prompt([400], 2, 64, dtype, 28, tail=5)
+    start = torch.tensor([0, 300, 100, 400, 50, 380], dtype=torch.int32, device=DEV)
+    out = torch.full(v.shape, NAN, dtype=dtype, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkv.latent_prompt_attn(q, k, kr, v, start, SCALE, out, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 4 and torch.isnan(out[400:].float()).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[1], [40], [200], [300], [3000, 5]])
+def test_prompt_timeout_is_reported(lens, D):
+    a = prompt(lens, 2, D, BF16, 29)
+    want = attend(*a, lens, SCALE)
+    attend(*a, lens, SCALE, want=5, flags=pkv.FLAG_TEST_DROP_FIRST_COPY)
+    assert torch.equal(attend(*a, lens, SCALE), want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_output_on_a_16_byte_boundary(D):
+    lens, H = [300, 45], 3
+    q, k, kr, v = prompt(lens, H, D, BF16, 30)
+    want = attend(q, k, kr, v, lens, SCALE)
+    buf = torch.full((want.numel() + 16,), NAN, dtype=BF16, device=DEV)
+    out = buf[8:8 + want.numel()].view(want.shape)
+    assert out.data_ptr() % 32 == 16
+    pkv.latent_prompt_attn(q, k, kr, v, starts(lens), SCALE, out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.isnan(buf[:8]).all() and torch.isnan(buf[-8:]).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_many_items_with_values_that_are_not_finite(D, dtype):
+    # Many short prompts to a CTA, NaN in every third one's V at changing places.
+    lens = [129 + (i * 37) % 150 for i in range(600)]
+    q, k, kr, v = prompt(lens, 2, D, dtype, 31)
+    at, bad = 0, torch.zeros(v.shape, dtype=torch.bool, device=DEV)
+    for i, n in enumerate(lens):
+        if i % 3 == 0:
+            bad[at + (i * 53) % n, i % 2, (i * 7) % D] = True
+        at += n
+    clean = attend(q, k, kr, torch.where(bad, torch.zeros_like(v), v), lens, SCALE)
+    out = attend(q, k, kr, torch.where(bad, torch.full_like(v, NAN), v), lens, SCALE)
+    sees, at = torch.zeros_like(bad), 0
+    for n in lens:
+        sees[at:at + n] = bad[at:at + n].cumsum(0) > 0
+        at += n
+    assert torch.equal(torch.isnan(out.float()), sees)
+    assert torch.equal(torch.where(sees, torch.zeros_like(out), out), torch.where(sees, torch.zeros_like(out), clean))
+
+
+def test_prompt_as_many_sequences_as_there_may_be():
+    S = 1 << 20
+    lens = np.zeros(S, np.int64)
+    lens[[5, 70000, S - 1]] = [300, 17, 140]
+    q, k, kr, v = prompt([300, 17, 140], 2, 128, BF16, 32)
+    want = attend(q, k, kr, v, [300, 17, 140], SCALE)
+    assert torch.equal(attend(q, k, kr, v, lens, SCALE), want)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
