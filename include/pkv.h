@@ -631,8 +631,9 @@ pkv_status pkv_rope_append(const void *q, const void *k, const void *v, pkv_dtyp
  *                 in_dtype (F32 or BF16), rows `stride` elements apart (views of one
  *                 projection are fine); strides are multiples of 16 bytes.
  *   q_rope, q_out [num_tokens, num_q_heads, rope_dim] of in_dtype, a token stride and a
- *                 head stride each: views of wider heads are fine, such as the last
- *                 rope_dim numbers of the decode's q.  q_out may be q_rope itself.
+ *                 head stride each, at least rope_dim and multiples of 16 bytes, in
+ *                 either order (q_out's heads may not overlap): views of wider heads are
+ *                 fine, such as the last rope_dim numbers of the decode's q.  q_out may be q_rope itself.
  *                 num_q_heads 0: no queries (both NULL).
  *   cache_dtype   F32 or BF16.
  * positions, table, slot_mapping, flags, status as for pkv_rope_append.
@@ -690,7 +691,8 @@ pkv_status pkv_latent_attn_decode(const void *q, const void *cache, pkv_dtype dt
  *   q             [num_tokens, num_heads, nope_dim + rope_dim] of dtype (F32 or BF16),
  *                 heads dense, rows q_stride elements apart.
  *   k, v          [num_tokens, num_heads, nope_dim] of dtype, a token stride and a head
- *                 stride each: the halves of one up-projection's heads are fine.
+ *                 stride each, at least nope_dim, in either order: the halves of one
+ *                 up-projection's heads are fine, and so is one head after the other.
  *   k_rope        [num_tokens, rope_dim] of dtype, rotated.
  *   nope_dim      64 or 128; rope_dim 64.  Strides are multiples of 16 bytes.
  *   out           [num_tokens, num_heads, nope_dim] of dtype, dense.

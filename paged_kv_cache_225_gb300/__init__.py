@@ -23,6 +23,7 @@ current stream and the workspace allocation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -940,6 +941,12 @@ def latent_append(latent: torch.Tensor, k_rope: torch.Tensor, positions: torch.T
 _ROPE = 64  # rotated numbers of a latent row
 
 
+@functools.lru_cache(maxsize=1024)
+def _latent_need(code, S, H, R, B, max_seq_len) -> int:
+    """Workspace bytes of a decode call: a function of its sizes alone."""
+    return lib().pkv_latent_attn_workspace_size(code, S, H, R, _ROPE, B, max_seq_len)
+
+
 def latent_workspace_size(dtype: torch.dtype, num_seqs: int, num_heads: int, latent_dim: int,
                           max_seq_len: int) -> int:
     """Workspace bytes of ``latent_attn_decode`` (pkv_latent_attn_workspace_size)."""
@@ -987,10 +994,9 @@ def latent_attn_decode(q: torch.Tensor, cache: torch.Tensor, block_tables: torch
         max_seq_len = width * B
     if max(S, H, N, width, max_seq_len) > _INT_MAX:
         raise ValueError("at most 2^31 - 1 sequences, pages, entries of a row and tokens")
-    L = _lib if _lib is not None else lib()
-    need = L.pkv_latent_attn_workspace_size(code, S, H, R, _ROPE, B, max_seq_len)
     if workspace is None:
         # Of the call's own stream: the allocator hands it out again in that stream's order.
+        need = _latent_need(code, S, H, R, B, int(max_seq_len))
         if stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         else:

@@ -90,6 +90,7 @@ constexpr int kLatentMaxSeqs = 1 << 20;  // every CTA reads all lengths once
 // Heads of a tile, tiles per sequence and teams for a call: set in p.  Returns
 // the bytes of workspace, 0 for sizes without a plan.
 size_t latent_plan(LatentDecodeParams &p, int dtype);
+size_t latent_part_rows(const LatentDecodeParams &p);  // of partial sums in the workspace
 
 pkv_status launch_latent_decode_simt(const LatentDecodeParams &p, cudaStream_t stream);
 pkv_status launch_latent_decode_tc(const LatentDecodeParams &p, cudaStream_t stream);

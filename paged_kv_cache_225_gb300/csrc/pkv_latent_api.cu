@@ -21,6 +21,12 @@ bool stride_ok(int64_t stride, int64_t least, pkv_dtype dtype)
     return stride >= least && stride % (dtype == PKV_F32 ? 4 : 8) == 0 && stride < (int64_t{1} << 36);
 }
 
+// Heads of `dim` numbers, token by token or head by head, that do not overlap.
+bool heads_apart(int num_tokens, int num_heads, int64_t stride, int64_t head, int dim)
+{
+    return stride >= (num_heads - 1) * head + dim || head >= (num_tokens - 1) * stride + dim;
+}
+
 // The kernels work with a positive factor: the sign goes to the scores, and a zero
 // becomes a factor too small to tell weights apart, which keeps masked scores (-inf)
 // out all the same.
@@ -143,11 +149,10 @@ pkv_status pkv_latent_append(const void *latent, const void *k_rope, pkv_dtype i
     if (!stride_ok(latent_stride, latent_dim, in_dtype) || !stride_ok(k_rope_stride, rope_dim, in_dtype))
         return PKV_ERR_INVALID_ARG;
     if (num_q_heads > 0) {
-        // Heads do not overlap, nor do tokens.
-        const int64_t last = num_q_heads - 1;
-        if (!stride_ok(q_head_stride, rope_dim, in_dtype) || !stride_ok(q_out_head_stride, rope_dim, in_dtype) ||
-            !stride_ok(q_stride, last * q_head_stride + rope_dim, in_dtype) ||
-            !stride_ok(q_out_stride, last * q_out_head_stride + rope_dim, in_dtype))
+        for (const int64_t st : {q_stride, q_head_stride, q_out_stride, q_out_head_stride})
+            if (!stride_ok(st, rope_dim, in_dtype))
+                return PKV_ERR_INVALID_ARG;
+        if (!heads_apart(num_tokens, num_q_heads, q_out_stride, q_out_head_stride, rope_dim))
             return PKV_ERR_INVALID_ARG;
     }
     p.q.q = q_rope;
@@ -240,7 +245,7 @@ pkv_status pkv_latent_attn_decode(const void *q, const void *cache, pkv_dtype dt
     p.score_scale = score_factor(scale);
     p.negate = scale < 0.f ? 1 : 0;
     p.drop_first_copy = (flags & PKV_FLAG_TEST_DROP_FIRST_COPY) ? 1 : 0;
-    const size_t rows = 2 * static_cast<size_t>(p.teams) * p.head_tiles * p.tile_heads;
+    const size_t rows = latent_part_rows(p);
     p.part = static_cast<float *>(workspace);
     p.part_ml = reinterpret_cast<float2 *>(p.part + rows * latent_dim);
     p.pieces = reinterpret_cast<int2 *>(p.part_ml + rows);
@@ -283,12 +288,12 @@ pkv_status pkv_latent_prompt_attn(const void *q, const void *k, const void *k_ro
     for (const void *a : {q, k, k_rope, v, static_cast<const void *>(out)})
         if (!aligned(a, 16))
             return PKV_ERR_INVALID_ARG;
-    const int64_t last = num_heads - 1;
     if (!stride_ok(q_stride, static_cast<int64_t>(num_heads) * (nope_dim + rope_dim), dtype) ||
-        !stride_ok(k_rope_stride, rope_dim, dtype) || !stride_ok(k_head_stride, nope_dim, dtype) ||
-        !stride_ok(v_head_stride, nope_dim, dtype) || !stride_ok(k_stride, last * k_head_stride + nope_dim, dtype) ||
-        !stride_ok(v_stride, last * v_head_stride + nope_dim, dtype))
+        !stride_ok(k_rope_stride, rope_dim, dtype))
         return PKV_ERR_INVALID_ARG;
+    for (const int64_t st : {k_stride, k_head_stride, v_stride, v_head_stride})
+        if (!stride_ok(st, nope_dim, dtype))
+            return PKV_ERR_INVALID_ARG;
     p.q = q;
     p.k = k;
     p.k_rope = k_rope;

@@ -445,6 +445,11 @@ template <typename T, int R> pkv_status launch_merge_by(const LatentDecodeParams
 
 constexpr double kCut = 4, kCutAll = 1.5;
 
+size_t latent_part_rows(const LatentDecodeParams &p)
+{
+    return p.whole ? 0 : 2 * static_cast<size_t>(p.teams) * p.head_tiles * p.tile_heads;
+}
+
 size_t latent_plan(LatentDecodeParams &p, int dtype)
 {
     // fp32: two CTAs to an SM.  bf16: one.
@@ -464,7 +469,7 @@ size_t latent_plan(LatentDecodeParams &p, int dtype)
     p.whole = rounds <= even + kCut + kCutAll * p.teams / most;
     if (p.whole && p.num_seqs < p.teams)
         p.teams = p.num_seqs > 0 ? p.num_seqs : 1;
-    const size_t rows = 2 * static_cast<size_t>(p.teams) * p.head_tiles * p.tile_heads;
+    const size_t rows = latent_part_rows(p);
     return (rows * (p.latent_dim * sizeof(float) + sizeof(float2)) + p.teams * sizeof(int2) + 255) / 256 * 256;
 }
 

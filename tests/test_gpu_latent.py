@@ -248,7 +248,7 @@ def test_streams_graphs_and_workspaces(dtype):
     ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
     assert torch.equal(decode(*b, SCALE, workspace=ws), want_b)
     with pytest.raises(pkv.PkvError):
-        decode(*b, SCALE, workspace=ws[:need // 2])
+        decode(*b, SCALE, workspace=ws[:need // 2 // 256 * 256])
 
 
 @pytest.mark.parametrize("H,R,n", [(16, 512, 50), (64, 512, 900), (128, 256, 3000), (32, 512, 20000)])
@@ -408,6 +408,15 @@ def test_prompt_strides(D, dtype):
     kr = rows(ROPE, unit, 0, unit)[:, 2]
     check_prompt(q, k, kr, v, lens, 0.1)
     check_prompt(q, v, kr.contiguous(), k, lens, 0.1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_prompt_one_head_after_the_other(dtype):
+    lens, H = [300, 0, 131], 5
+    q, k, kr, v = prompt(lens, H, 128, dtype, 33)
+    k, v = (x.permute(1, 0, 2).contiguous().permute(1, 0, 2) for x in (k, v))
+    assert k.stride(0) == 128 and k.stride(1) == sum(lens) * 128
+    check_prompt(q, k, kr, v, lens, SCALE)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])

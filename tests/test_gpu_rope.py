@@ -225,6 +225,17 @@ def test_latent_rows(R, H, interleaved, pattern, dtype, cache):
         assert got is None
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_latent_queries_one_head_after_the_other(dtype):
+    latent, key, q, pos, slots, N = latent_case("ragged", 256, 6, dtype, 21)
+    table = rope_table(MAX_POS, ROPE, DEV)
+    c = torch.zeros((N, 16, 320), dtype=dtype, device=DEV)
+    q = q.permute(1, 0, 2).contiguous().permute(1, 0, 2)
+    out = torch.zeros((6, len(pos), ROPE), dtype=dtype, device=DEV).permute(1, 0, 2)
+    pkv.latent_append(latent, key, pos, table, slots, c, q_rope=q, q_out=out)
+    assert torch.equal(raw(out), raw(rotate(q, table, pos, False, F32).to(dtype)))
+
+
 def test_latent_rows_out_of_range_and_far():
     R, N = 512, 240000                                # 2.2 * 10^9 numbers
     latent, key, q, pos, slots, _ = latent_case("ragged", R, 4, BF16, 11)

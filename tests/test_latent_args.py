@@ -61,7 +61,8 @@ def latent(**kw):
     (dict(cache=None), INVALID), (dict(pos=None), INVALID), (dict(table=None), INVALID), (dict(slots=None), INVALID),
     (dict(c=P + 8), INVALID), (dict(kr=P + 2), INVALID), (dict(q=P + 8), INVALID), (dict(out=P + 4), INVALID),
     (dict(cache=P + 8), INVALID), (dict(cs=504), INVALID), (dict(rs=56), INVALID), (dict(qh=56), INVALID),
-    (dict(qs=15 * 192 + 56), INVALID), (dict(os=15 * 576 + 56), INVALID), (dict(oh=63), INVALID),
+    (dict(qs=60), INVALID), (dict(qs=56), INVALID), (dict(os=15 * 576 + 56), INVALID),
+    (dict(os=64, oh=9 * 64 + 56), INVALID), (dict(oh=63), INVALID),
     (dict(cs=578), INVALID), (dict(status=P + 1), INVALID),
     (dict(T=0, c=None), OK),
 ])
@@ -87,7 +88,8 @@ def decode(**kw):
     (dict(q=None), INVALID), (dict(cache=None), INVALID), (dict(tables=None), INVALID), (dict(lens=None), INVALID),
     (dict(out=None), INVALID), (dict(q=P + 8), INVALID), (dict(cache=P + 8), INVALID), (dict(out=P + 2), INVALID),
     (dict(tables=P + 2), INVALID), (dict(lens=P + 1), INVALID), (dict(status=P + 2), INVALID),
-    (dict(ws=None), WORKSPACE), (dict(bytes=1000), WORKSPACE), (dict(ws=P + 128), INVALID),
+    (dict(ws=None), WORKSPACE), (dict(bytes=100), WORKSPACE), (dict(ws=P + 128), INVALID),
+    (dict(width=600, most=9000, bytes=1 << 20), WORKSPACE),
     (dict(S=0, q=None), OK),
 ])
 def test_decode_arguments(kw, want):
@@ -123,7 +125,7 @@ def prompt(**kw):
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(kr=None), INVALID), (dict(v=None), INVALID),
     (dict(start=None), INVALID), (dict(out=None), INVALID), (dict(q=P + 8), INVALID), (dict(k=P + 2), INVALID),
     (dict(kr=P + 4), INVALID), (dict(v=P + 8), INVALID), (dict(out=P + 8), INVALID), (dict(start=P + 2), INVALID),
-    (dict(status=P + 2), INVALID), (dict(qs=16 * 192 - 8), INVALID), (dict(ks=15 * 256 + 120), INVALID),
+    (dict(status=P + 2), INVALID), (dict(qs=16 * 192 - 8), INVALID), (dict(ks=120), INVALID),
     (dict(kh=120), INVALID), (dict(kh=130), INVALID), (dict(vh=0), INVALID), (dict(vs=1 << 36), INVALID),
     (dict(rs=56), INVALID), (dict(dtype=pkv.F32, rs=66), INVALID),
     # Nothing to do.
