@@ -22,7 +22,8 @@ constexpr int kBad = -1;
 template <int R> struct LatentSimt {
     static constexpr int kRow = R + kRopeDim;
     static constexpr int kLd = kRow + 4;  // rows 4 banks apart
-    static constexpr int kSmem = 3 * 16 * kLd * 4;
+    static constexpr int kPages = R == 256 ? 4 : 2;  // in shared memory, two CTAs to an SM
+    static constexpr int kSmem = (1 + kPages) * 16 * kLd * 4;
 };
 
 __device__ __forceinline__ void fma2(uint64_t &c, uint64_t a, uint64_t b)
@@ -55,8 +56,9 @@ template <int R>
 __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const LatentDecodeParams p)
 {
     constexpr int kRow = LatentSimt<R>::kRow, kLd = LatentSimt<R>::kLd, kDims = R / kSimtThreads;
+    constexpr int kPages = LatentSimt<R>::kPages;
     extern __shared__ __align__(16) float smem_f[];
-    float *sq = smem_f, *sk = sq + 16 * kLd;  // the queries, two pages
+    float *sq = smem_f, *sk = sq + 16 * kLd;  // the queries, the pages
     __shared__ float s_half[2][16][17];       // scores of half the dims
     __shared__ __align__(16) float s_p[16][16], s_alpha[16];
     __shared__ float2 s_ml[16];
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const Late
             const bool ok = static_cast<unsigned>(block) < static_cast<unsigned>(p.num_blocks);
             if (!ok && threadIdx.x == 0)
                 set_status(p.status, PKV_ERR_OUT_OF_RANGE);
-            load_rows<R>(sk + (page & 1) * 16 * kLd,
+            load_rows<R>(sk + page % kPages * 16 * kLd,
                          static_cast<const float *>(p.cache) + static_cast<size_t>(ok ? block : 0) * 16 * kRow,
                          ok ? min(16, piece.len - 16 * page) : 0);
         };
@@ -105,20 +107,29 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const Late
         for (int i = 0; i < (kDims == 2 ? 16 : 8); ++i)
             o[i] = 0;
         float m = -INFINITY, l = 0.f;  // of head threadIdx.x / 16
-        if (from < to)
-            load_page(from);
+        // Every page counts as a group of copies, also one that is not there.
+#pragma unroll
+        for (int i = 0; i < kPages - 1; ++i) {
+            if (from + i < to)
+                load_page(from + i);
+            else
+                cp_async_commit();
+        }
         for (int page = from; page < to; ++page) {
-            cp_async_wait_all();
+            asm volatile("cp.async.wait_group %0;" ::"n"(kPages - 2) : "memory");
             __syncthreads();
-            if (page + 1 < to)
-                load_page(page + 1);
-            const float *k = sk + (page & 1) * 16 * kLd;
+            if (page + kPages - 1 < to)
+                load_page(page + kPages - 1);
+            else
+                cp_async_commit();
+            const float *k = sk + page % kPages * 16 * kLd;
             {
-                // Heads 4 (warp % 4) .., dims of half warp / 4, tokens lane / 4 and lane / 4 + 8.
+                // Heads 4 (warp % 4) .., dims of half warp / 4, tokens lane % 8 and lane % 8 + 8:
+                // the eight lanes of a load's phase lie in eight rows, 4 banks apart.
                 const int half = warp >> 2, hq = 4 * (warp & 3);
                 uint64_t acc[4][2] = {};
-                const float *kq = sq + hq * kLd + half * (kRow / 2) + 4 * (lane & 3);
-                const float *kr = k + (lane >> 2) * kLd + half * (kRow / 2) + 4 * (lane & 3);
+                const float *kq = sq + hq * kLd + half * (kRow / 2) + 4 * (lane >> 3);
+                const float *kr = k + (lane & 7) * kLd + half * (kRow / 2) + 4 * (lane >> 3);
 #pragma unroll 2
                 for (int d = 0; d < kRow / 2; d += 16) {
                     ulonglong2 kf[2];
@@ -139,10 +150,10 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const Late
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         float x = sum2(acc[i][j]);
-                        x += __shfl_xor_sync(kFullMask, x, 1);
-                        x += __shfl_xor_sync(kFullMask, x, 2);
-                        if ((lane & 3) == 0)
-                            s_half[half][hq + i][(lane >> 2) + 8 * j] = x;
+                        x += __shfl_xor_sync(kFullMask, x, 8);
+                        x += __shfl_xor_sync(kFullMask, x, 16);
+                        if (lane < 8)
+                            s_half[half][hq + i][lane + 8 * j] = x;
                     }
             }
             __syncthreads();
