@@ -30,7 +30,25 @@
 //    that see them (s_seen).  Rows past the sequence are zeroed.
 //  * Every wait is bounded; a timeout records PKV_ERR_TIMEOUT, stops every role, lets
 //    copies and MMAs in flight finish and frees TMEM.
-#include <climits>
+//
+// What bounds it.  Long prompts: the tensor cores and their power (one of 16K tokens, 32
+// heads: 1.63 to 1.73 ms, 1590 to 1690 TFLOP/s, 85 to 90% of a cuBLAS burst, 94 to 99% of what cuBLAS
+// sustains): a block takes them 2560 cycles for both tiles, a step 3600, of which the
+// issuing warp waits 570 for the softmax and 320 for K and V.  16 prompts of 512 to 4096
+// tokens: 850 us, 1170 TFLOP/s: steps of 4150 cycles, 1160 of them waiting for the softmax
+// (an item is 10 blocks, and its ends do not overlap as well).  128 prompts of 256 to 512
+// tokens: 441 us, 60% of HBM's bytes; heads of 64 + 64 (37 prompts of up to 1000 tokens,
+// 32 heads): 180 to 200 us; both are chains of load, scores, softmax, P V and store of items two
+// or three blocks long.
+//
+// V with values that are not finite, one prompt of 8192 tokens, 32 heads: 438 us without,
+// all NaN 626, the last token 440, every 10^4-th value 457.
+//
+// Measured and not kept: a barrier for each chunk instead of one for a block's K and one
+// for its V (888 us against 842 on the 16 prompts, 1863 against 1717 on the long one);
+// some of the exponentials by polynomial on the multiply-add units (852 us without, 885 to
+// 965 with one to four in eight: issue slots, not the special function units, are short);
+// the maximum with three operands to an instruction (the same).
 
 #include "pkv_latent.h"
 #include "pkv_prompt.cuh"

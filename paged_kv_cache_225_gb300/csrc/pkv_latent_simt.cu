@@ -8,7 +8,10 @@
 // A CTA of 256 threads has 16 heads of a sequence and walks its pages: scores of
 // 16 heads x 16 tokens (a warp: 4 heads, all tokens, half the dims; a lane 4 heads x
 // 2 tokens on every fourth of those dims), one pass of the softmax with a thread
-// per score, then R / 256 output dims of all heads per thread.
+// per score, then R / 256 output dims of all heads per thread.  Shared-memory loads and
+// the steps of a page bound it: 16 sequences of 4096 tokens, 32 heads, R = 512: 159 us (29
+// TFLOP/s); 8 of up to 4096, 16 heads, R = 256: 24 us.  With the four lanes of a token next to each other
+// (two rows to a load's phase, in the same banks) 213 and 29 us.
 #include "pkv_latent.cuh"
 
 namespace pkv {
@@ -446,7 +449,7 @@ template <typename T, int R> pkv_status launch_merge_by(const LatentDecodeParams
 {
     // Eight pieces to a sequence and more (4 x 32K tokens, 128 heads, 19 pieces: 57 us, alone
     // or with eight warps 59), and 32 and more (32K tokens, 32 heads, 152 pieces: 25 us, with
-    // four warps 30, alone 45).
+    // four warps 30, alone 60 with an earlier form).
     return p.teams >= 32 * p.num_seqs  ? launch_merge<T, R, 8>(p, stream)
            : p.teams >= 8 * p.num_seqs ? launch_merge<T, R, 4>(p, stream)
                                        : launch_merge<T, R, 1>(p, stream);
@@ -454,6 +457,8 @@ template <typename T, int R> pkv_status launch_merge_by(const LatentDecodeParams
 
 }  // namespace
 
+// Cut / whole, us: one sequence of 200 tokens, 32 heads 10.7 / 10.4, of 512 9.4 / 14.1; 128
+// of 256 to 512 31 / 30, of 500 to 1000 37 / 46.
 constexpr double kCut = 4, kCutAll = 1.5;
 
 size_t latent_part_rows(const LatentDecodeParams &p)
@@ -463,7 +468,8 @@ size_t latent_part_rows(const LatentDecodeParams &p)
 
 size_t latent_plan(LatentDecodeParams &p, int dtype)
 {
-    // fp32: two CTAs to an SM.  bf16: one.
+    // fp32: two CTAs to an SM.  bf16: one, with the fewest head columns that hold the heads
+    // (columns cost time, and the room they leave holds more tiles).
     p.tile_heads = dtype == PKV_F32 || p.num_heads <= 16 ? 16 : p.num_heads <= 32 ? 32 : 64;
     p.head_tiles = (p.num_heads + p.tile_heads - 1) / p.tile_heads;
     const long ctas = dtype == PKV_F32 ? 2 * kLatentSms : kLatentSms;

@@ -28,6 +28,30 @@
 //  * Every wait is bounded; a timeout records PKV_ERR_TIMEOUT, stops every role, lets
 //    copies and MMAs in flight finish and frees TMEM.  The warps of a half leave
 //    together: none waits at a barrier for one that has gone.
+//
+// What the layout costs the tensor cores (counted alone, cycles per MMA of 16 dims or
+// tokens): the scores 32, 24 and 23 for 64, 32 and 16 heads (M = 64), P V 48, 40 and 39
+// (M = 128): the larger of half or full rate and of the operands' shared-memory bytes at
+// 128 a cycle.  A tile of 64 tokens takes 1940 cycles with 64 heads, HBM 3170 to bring it.
+// Heads on the rows would take 2176 with 64 heads and as much with 16.
+//
+// What bounds it.  Few heads: HBM (256 x 4096 tokens, 16 heads: 196 us, 6.2 TB/s, 91% of a
+// plain copy).  64 heads (64 x 8192 tokens: 118 us, 5.2 TB/s): queries and weights leave
+// room for two tiles, and a tile's slot is taken for some 3300 cycles between its landing
+// and the end of P V (scores 900, softmax 1000, P V 700, hand-overs) and 2300 more until
+// the next one has landed.  128 heads are two CTAs that read the same rows
+// (128 x 4096 tokens: 171 us, 856 TFLOP/s): the same chain, with 1940 cycles of products in
+// 2800.  Short calls: about 6000 cycles until the first tile lands (the lengths and the
+// table are two dependent trips to memory) and the joining kernel (64 sequences of a
+// mean of 2900 tokens, 64 heads: 53 + 8.5 us).
+//
+// Measured and not kept: one warp for all MMAs that takes what is ready (64 x 64 heads
+// 76 us against 66 then: it looks as long as it issues); one copying warp, two, four (73,
+// 66, 63; eight 62.5 with the later steps); 16-token boxes of 64 dims instead of 8-token
+// boxes of half the row (66 against 63); two tiles of 32 heads instead of one of 64 (64 x
+// 8192 tokens 130 against 118); partial sums with the heads next to each other (32 bytes to
+// a lane: 78 against 65); the barrier of the softmax warps also telling failures apart
+// without a second look (the same).
 #include <type_traits>
 
 #include "pkv_latent.cuh"
@@ -374,9 +398,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == kAheadWarp && p.head_tiles > 1) {
         // --------------------------------------------- HBM, ahead of the rings
-        // Two tiles are too little to have under way for HBM's latency at its rate: their
-        // pages are fetched into L2 while the rings are still full.  Two tiles at a time,
-        // a lane for each page; head tiles share the pages out.
+        // With two head tiles, each row is read by two CTAs, and the rings hold half as many
+        // bytes of HBM: pages are fetched into L2 while the rings are still full.  Two tiles
+        // at a time, a lane for each page; the head tiles share the pages out.  128 x 4096
+        // tokens, 128 heads: 174 us, without 198; four tiles ahead 182.  With one head tile
+        // the rings are enough, and it costs (256 x 4096, 16 heads: 194 us without, 207 two
+        // ahead, 275 four: more than L2 keeps).
         const volatile uint32_t *issued = &s_issued;
         uint32_t tiles = 0;
         for (bool on = true; on;) {
