@@ -469,7 +469,9 @@ size_t latent_part_rows(const LatentDecodeParams &p)
 size_t latent_plan(LatentDecodeParams &p, int dtype)
 {
     // fp32: two CTAs to an SM.  bf16: one, with the fewest head columns that hold the heads
-    // (columns cost time, and the room they leave holds more tiles).
+    // (columns cost time, and the room they leave holds more tiles): 256 x 4096 tokens of 16
+    // heads take 192 us with 16 columns, 194 with 32, 202 with 64; 128 of 500 to 1000
+    // tokens, 32 heads, 36.3 with 32 columns, 38.3 with 64.
     p.tile_heads = dtype == PKV_F32 || p.num_heads <= 16 ? 16 : p.num_heads <= 32 ? 32 : 64;
     p.head_tiles = (p.num_heads + p.tile_heads - 1) / p.tile_heads;
     const long ctas = dtype == PKV_F32 ? 2 * kLatentSms : kLatentSms;
@@ -480,7 +482,7 @@ size_t latent_plan(LatentDecodeParams &p, int dtype)
     // Cutting evens the teams out and costs partial sums and the second kernel, in tiles
     // of a team about kCut and, by the share of the teams that cut, kCutAll more.  Without
     // it a team has whole sequences, of which the longest counts.  The lengths are not
-    // known here: three quarters of the bound on average are supposed.
+    // known here: three quarters of the bound on average are supposed.  (Figures: bf16.)
     const double rounds = static_cast<double>((p.num_seqs + most - 1) / most) * tiles;
     const double even = 0.75 * p.num_seqs * tiles / most;
     p.whole = rounds <= even + kCut + kCutAll * p.teams / most;

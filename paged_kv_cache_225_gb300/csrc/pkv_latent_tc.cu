@@ -39,7 +39,8 @@
 // plain copy).  64 heads (64 x 8192 tokens: 118 us, 5.2 TB/s): queries and weights leave
 // room for two tiles, and a tile's slot is taken for some 3300 cycles between its landing
 // and the end of P V (scores 900, softmax 1000, P V 700, hand-overs) and 2300 more until
-// the next one has landed.  128 heads are two CTAs that read the same rows
+// the next one has landed; that alone would leave 6.0 TB/s (16 heads in 64 columns), the
+// rest are the partial sums of cut sequences, 128 KB each.  128 heads are two CTAs that read the same rows
 // (128 x 4096 tokens: 171 us, 856 TFLOP/s): the same chain, with 1940 cycles of products in
 // 2800.  Short calls: about 6000 cycles until the first tile lands (the lengths and the
 // table are two dependent trips to memory) and the joining kernel (64 sequences of a
