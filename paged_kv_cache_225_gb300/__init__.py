@@ -706,10 +706,15 @@ def _cuda_index(t: torch.Tensor, what: str) -> int:
     return index
 
 
+def _elsewhere(t, what: str, index: int):
+    _cuda_index(t, what)
+    raise ValueError(f"{what} is on {t.device}, expected cuda:{index}")
+
+
 def _rows(t: torch.Tensor, what: str, dtype: torch.dtype, index: int):
     """(shape, row stride in elements) of a [T, H, D] tensor whose rows are dense."""
-    if _cuda_index(t, what) != index:
-        raise ValueError(f"{what} is on {t.device}, expected cuda:{index}")
+    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.is_cuda):
+        _elsewhere(t, what, index)
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {str(dtype).replace('torch.', '')} like q")
     shape = t.shape
@@ -775,38 +780,40 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torc
 
 def _heads(t: torch.Tensor, what: str, dtype: torch.dtype, index: int):
     """(shape, token stride, head stride) of a [T, H, D] tensor whose heads are dense."""
-    if _cuda_index(t, what) != index:
-        raise ValueError(f"{what} is on {t.device}, expected cuda:{index}")
+    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.is_cuda):
+        _elsewhere(t, what, index)
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {str(dtype).replace('torch.', '')}")
-    if t.dim() != 3:
-        raise ValueError(f"{what} must have 3 dims, got {tuple(t.shape)}")
-    T, H, D = t.shape
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{what} must have 3 dims, got {tuple(shape)}")
+    T, H, D = shape
     row, head, elem = t.stride()
     if T > 0 and H > 0 and D > 1 and elem != 1:
         raise ValueError(f"{what}: every head must be dense")
     if H <= 1:
         head = D
-    return t.shape, (row if T > 1 else max(H - 1, 0) * head + D), head
+    return shape, (row if T > 1 else max(H - 1, 0) * head + D), head
 
 
 def _vectors(t: torch.Tensor, what: str, dtype: torch.dtype, index: int):
     """(shape, row stride) of a [T, D] tensor whose rows are dense."""
-    if _cuda_index(t, what) != index:
-        raise ValueError(f"{what} is on {t.device}, expected cuda:{index}")
+    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.is_cuda):
+        _elsewhere(t, what, index)
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {str(dtype).replace('torch.', '')}")
-    if t.dim() != 2:
-        raise ValueError(f"{what} must have 2 dims, got {tuple(t.shape)}")
-    T, D = t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} must have 2 dims, got {tuple(shape)}")
+    T, D = shape
     row, elem = t.stride()
     if T > 0 and D > 1 and elem != 1:
         raise ValueError(f"{what}: every row must be dense")
-    return t.shape, (row if T > 1 else D)
+    return shape, (row if T > 1 else D)
 
 
 def _new_tokens(positions, table, slot_mapping, status, T, index):
-    """Pointers of what the rotating cache writes share, and the table's shape."""
+    """Pointers of what the rotating cache writes share, the table's positions and dims."""
     pos = _ptr(positions, "positions", 1, _I32, index)
     tab = _ptr(table, "table", 2, torch.float32, index)
     slots = _ptr(slot_mapping, "slot_mapping", 1, _I64, index)
@@ -815,9 +822,10 @@ def _new_tokens(positions, table, slot_mapping, status, T, index):
         raise TypeError("positions, table and slot_mapping must be tensors")
     if positions.numel() != T or slot_mapping.numel() != T or (st is not None and status.numel() != 1):
         raise ValueError("positions and slot_mapping need one entry per token, status exactly one")
-    if T > _INT_MAX or table.shape[0] > _INT_MAX:
+    most, rot = table.shape
+    if T > _INT_MAX or most > _INT_MAX:
         raise ValueError("at most 2^31 - 1 tokens and positions")
-    return pos, tab, slots, st
+    return pos, tab, slots, st, most, rot
 
 
 def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -859,7 +867,7 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pos
             raise ValueError("inconsistent shapes")
         Hq = qshape[1]
         qp, op = q.data_ptr(), q_out.data_ptr()
-    pos, tab, slots, st = _new_tokens(positions, table, slot_mapping, status, T, index)
+    pos, tab, slots, st, most, rot = _new_tokens(positions, table, slot_mapping, status, T, index)
     if not isinstance(k_cache, torch.Tensor) or not isinstance(v_cache, torch.Tensor):
         raise TypeError("k_cache and v_cache must be torch.Tensors")
     ctype = k_cache.dtype
@@ -879,7 +887,7 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pos
     if N > _INT_MAX:
         raise ValueError("at most 2^31 - 1 pages")
     _launch("pkv_rope_append", index, stream,
-            (qp, k.data_ptr(), v.data_ptr(), code, qs, ks, vs, pos, tab, table.shape[1], table.shape[0], slots, T,
+            (qp, k.data_ptr(), v.data_ptr(), code, qs, ks, vs, pos, tab, rot, most, slots, T,
              Hq, Hkv, D, B, N, op, qos, kc, vc, ccode, float(k_scale), float(v_scale),
              FLAG_ROPE_INTERLEAVED if interleaved else 0, st))
     return q_out
@@ -919,7 +927,7 @@ def latent_append(latent: torch.Tensor, k_rope: torch.Tensor, positions: torch.T
             raise ValueError("inconsistent shapes")
         H = qshape[1]
         qp, op = q_rope.data_ptr(), q_out.data_ptr()
-    pos, tab, slots, st = _new_tokens(positions, table, slot_mapping, status, T, index)
+    pos, tab, slots, st, most, rot = _new_tokens(positions, table, slot_mapping, status, T, index)
     if not isinstance(cache, torch.Tensor):
         raise TypeError("cache must be a torch.Tensor")
     ccode = _FLOATS.get(cache.dtype)
@@ -927,12 +935,12 @@ def latent_append(latent: torch.Tensor, k_rope: torch.Tensor, positions: torch.T
         raise TypeError(f"cache: unsupported dtype {cache.dtype}")
     cp = _ptr(cache, "cache", 3, cache.dtype, index)
     N, B, row = cache.shape
-    if T2 != T or row != R + rope or table.shape[1] != rope:
+    if T2 != T or row != R + rope or rot != rope:
         raise ValueError("inconsistent shapes")
     if N > _INT_MAX:
         raise ValueError("at most 2^31 - 1 pages")
     _launch("pkv_latent_append", index, stream,
-            (latent.data_ptr(), k_rope.data_ptr(), code, ls, rs, qp, qs, qh, pos, tab, table.shape[0], slots, T, H,
+            (latent.data_ptr(), k_rope.data_ptr(), code, ls, rs, qp, qs, qh, pos, tab, most, slots, T, H,
              R, rope, B, N, op, qos, qoh, cp, ccode, FLAG_ROPE_INTERLEAVED if interleaved else 0,
              st))
     return q_out
