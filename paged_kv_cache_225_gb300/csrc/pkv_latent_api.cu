@@ -1,5 +1,6 @@
 // C ABI of the rotating cache writes and of the latent attention (declared in
 // include/pkv.h): argument validation and dispatch.
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -180,6 +181,9 @@ static pkv_status plan_decode(LatentDecodeParams &p, pkv_dtype dtype, int num_se
         return PKV_ERR_INVALID_ARG;
     if (!is_float(dtype) || (latent_dim != 256 && latent_dim != 512) || rope_dim != kRopeDim ||
         block_size != kBlockSize || num_q_heads > 128 || num_seqs > kLatentMaxSeqs)
+        return PKV_ERR_UNSUPPORTED;
+    // Lengths are rounded up to whole pages and tiles in 32 bits, one clamped to the bound too.
+    if (max_seq_len > INT_MAX - kLatentTokens)
         return PKV_ERR_UNSUPPORTED;
     // Tiles are counted in 32 bits, the ends of a team's range included.
     if (static_cast<int64_t>(num_seqs) * (max_seq_len / kLatentTokens + 1) >= INT64_C(1) << 30)

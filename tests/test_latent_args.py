@@ -198,3 +198,19 @@ def test_tensors_that_do_not_fit():
                     (dict(q_start=st.long()), TypeError), (dict(v=x.transpose(0, 1)), ValueError)):
         with pytest.raises(err):
             pkv.latent_prompt_attn(**{**pr, **kw})
+
+
+# The largest bound whose lengths the kernels can round up to whole tiles of 64 in 32 bits.
+MOST = 2 ** 31 - 65
+
+
+@pytest.mark.parametrize("dtype", [pkv.F32, pkv.BF16])
+def test_bounds_whose_tiles_pass_32_bits_are_refused(dtype):
+    size = pkv.lib().pkv_latent_attn_workspace_size
+    assert size(dtype, 1, 16, 512, 64, 16, MOST) > 0
+    # The width holds the bound, nothing else is wrong: past the plan only the workspace is looked at.
+    kw = dict(S=1, dtype=dtype, width=1 << 27, bytes=0)
+    assert decode(most=MOST, **kw) == WORKSPACE
+    for bound in (MOST + 1, 2 ** 31 - 16, 2 ** 31 - 1):
+        assert size(dtype, 1, 16, 512, 64, 16, bound) == 0
+        assert decode(most=bound, **kw) == UNSUPPORTED
