@@ -593,7 +593,8 @@ pkv_status pkv_tables_fork(const int32_t *pairs, int num_pairs, int32_t *seq_len
  *
  *   q, q_out      [num_tokens, num_q_heads, head_dim] of in_dtype (F32 or BF16),
  *                 row t at q + t * q_stride elements, heads dense.  q_out may be q
- *                 itself (same pointer, same stride); it may not overlap the
+ *                 itself (same pointer, same stride; the same pointer with another
+ *                 stride is PKV_ERR_INVALID_ARG); it may not overlap the
  *                 inputs otherwise.  num_q_heads 0: no queries (both NULL).
  *   k, v          [num_tokens, num_kv_heads, head_dim] of in_dtype, rows likewise.
  *                 Strides are at least the row and a multiple of 16 bytes: views of
@@ -633,7 +634,8 @@ pkv_status pkv_rope_append(const void *q, const void *k, const void *v, pkv_dtyp
  *   q_rope, q_out [num_tokens, num_q_heads, rope_dim] of in_dtype, a token stride and a
  *                 head stride each, at least rope_dim and multiples of 16 bytes, in
  *                 either order (q_out's heads may not overlap): views of wider heads are
- *                 fine, such as the last rope_dim numbers of the decode's q.  q_out may be q_rope itself.
+ *                 fine, such as the last rope_dim numbers of the decode's q.  q_out may be q_rope itself
+ *                 (same pointer, same strides, as above); it may not overlap the inputs otherwise.
  *                 num_q_heads 0: no queries (both NULL).
  *   cache_dtype   F32 or BF16.
  * positions, table, slot_mapping, flags, status as for pkv_rope_append.

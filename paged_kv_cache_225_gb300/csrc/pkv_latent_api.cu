@@ -28,6 +28,14 @@ bool heads_apart(int num_tokens, int num_heads, int64_t stride, int64_t head, in
     return stride >= (num_heads - 1) * head + dim || head >= (num_tokens - 1) * stride + dim;
 }
 
+// Queries turned in place lie where they are read: other strides would write rows that
+// another warp has yet to read.
+bool in_place_ok(const RopeQuery &q, int num_tokens)
+{
+    return q.q != q.out || q.num_heads == 0 ||
+           ((num_tokens <= 1 || q.stride == q.out_stride) && (q.num_heads <= 1 || q.head == q.out_head));
+}
+
 // The kernels work with a positive factor: the sign goes to the scores, and a zero
 // becomes a factor too small to tell weights apart, which keeps masked scores (-inf)
 // out all the same.
@@ -110,6 +118,8 @@ pkv_status pkv_rope_append(const void *q, const void *k, const void *v, pkv_dtyp
     p.q.out_stride = q_out_stride;
     p.q.head = p.q.out_head = head_dim;
     p.q.num_heads = num_q_heads;
+    if (!in_place_ok(p.q, num_tokens))
+        return PKV_ERR_INVALID_ARG;
     p.k = k;
     p.v = v;
     p.k_stride = k_stride;
@@ -163,6 +173,8 @@ pkv_status pkv_latent_append(const void *latent, const void *k_rope, pkv_dtype i
     p.q.out_stride = q_out_stride;
     p.q.out_head = q_out_head_stride;
     p.q.num_heads = num_q_heads;
+    if (!in_place_ok(p.q, num_tokens))
+        return PKV_ERR_INVALID_ARG;
     p.latent = latent;
     p.k_rope = k_rope;
     p.latent_stride = latent_stride;

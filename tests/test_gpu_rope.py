@@ -281,3 +281,31 @@ def test_streams_graphs_and_two_calls_at_once():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(raw(oa), raw(oc)) and bool(c[0].any())
+
+
+def test_queries_in_place_with_other_strides_are_refused():
+    q, k, v, pos, slots, N = case("ragged", 4, 2, 64, BF16, 17, fused=False)
+    table = rope_table(MAX_POS, 64, DEV)
+    caches = [cache_like(N, 2, 64, BF16, i) for i in (1, 2)]
+    before = [c.clone() for c in caches]
+    T = len(pos)
+    wide = torch.zeros((T, 8, 64), dtype=BF16, device=DEV)
+    wide[:] = 1.0
+    dense = wide.view(-1)[:T * 4 * 64].view(T, 4, 64)     # at wide's address
+    for a, b in ((wide[:, :4], dense), (dense, wide[:, :4])):
+        with pytest.raises(pkv.PkvError):
+            pkv.rope_append(a, k, v, pos, table, slots, *caches, q_out=b)
+    row = torch.randn((T, 256 + ROPE), device=DEV).to(BF16)
+    cache = torch.zeros((N, 16, 256 + ROPE), dtype=BF16, device=DEV)
+    heads = wide.view(-1)[:T * 4 * 64].view(4, T, 64).permute(1, 0, 2)
+    for a, b in ((wide[:, :4], dense), (dense, heads), (heads, dense)):
+        with pytest.raises(pkv.PkvError):
+            pkv.latent_append(row[:, :256], row[:, 256:], pos, table, slots, cache, q_rope=a, q_out=b)
+    torch.cuda.synchronize()
+    assert bool((wide == 1).all()) and not bool(cache.any())
+    assert all(torch.equal(raw(x), raw(y)) for x, y in zip(caches, before))
+    # One token has no stride: the same call, which turns it where it lies.
+    one = q[:1].clone()
+    want = rotate(one, table, pos[:1], False, F32).to(BF16)
+    got = pkv.rope_append(wide[:1, :4].copy_(one), k[:1], v[:1], pos[:1], table, slots[:1], *caches, q_out=dense[:1])
+    assert torch.equal(raw(got), raw(want))

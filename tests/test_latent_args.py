@@ -214,3 +214,12 @@ def test_bounds_whose_tiles_pass_32_bits_are_refused(dtype):
     for bound in (MOST + 1, 2 ** 31 - 16, 2 ** 31 - 1):
         assert size(dtype, 1, 16, 512, 64, 16, bound) == 0
         assert decode(most=bound, **kw) == UNSUPPORTED
+
+
+def test_queries_in_place_need_their_own_strides():
+    # q_out at q's address and nothing else wrong: other strides would write rows not yet read.
+    for kw in (dict(os=33 * 128), dict(qs=64 * 128), dict(T=2, os=33 * 128)):
+        assert append(q=P, out=P, **kw) == INVALID
+    for kw in (dict(os=5 * 192, oh=192), dict(os=4 * 192, oh=64), dict(T=1, os=4 * 192, oh=64),
+               dict(H=1, os=256, oh=192)):
+        assert latent(q=P, out=P, **{**dict(H=4, qs=4 * 192, qh=192), **kw}) == INVALID
