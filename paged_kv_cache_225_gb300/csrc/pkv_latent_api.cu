@@ -22,10 +22,17 @@ bool stride_ok(int64_t stride, int64_t least, pkv_dtype dtype)
     return stride >= least && stride % (dtype == PKV_F32 ? 4 : 8) == 0 && stride < (int64_t{1} << 36);
 }
 
+// Whether `count` runs of `dim` numbers, `step` apart (positive), fit in `room`; their
+// extent may pass 64 bits.
+bool fits(int count, int64_t step, int dim, int64_t room)
+{
+    return room >= dim && (count <= 1 || step <= (room - dim) / (count - 1));
+}
+
 // Heads of `dim` numbers, token by token or head by head, that do not overlap.
 bool heads_apart(int num_tokens, int num_heads, int64_t stride, int64_t head, int dim)
 {
-    return stride >= (num_heads - 1) * head + dim || head >= (num_tokens - 1) * stride + dim;
+    return fits(num_heads, head, dim, stride) || fits(num_tokens, stride, dim, head);
 }
 
 // Queries turned in place lie where they are read: other strides would write rows that

@@ -223,3 +223,13 @@ def test_queries_in_place_need_their_own_strides():
     for kw in (dict(os=5 * 192, oh=192), dict(os=4 * 192, oh=64), dict(T=1, os=4 * 192, oh=64),
                dict(H=1, os=256, oh=192)):
         assert latent(q=P, out=P, **{**dict(H=4, qs=4 * 192, qh=192), **kw}) == INVALID
+
+
+@pytest.mark.parametrize("T,H,token,head", [
+    (10, (1 << 30) + 1, 1 << 33, 1 << 34),          # 2^64 numbers to a token's heads, 2^36 to a head's tokens
+    ((1 << 30) + 1, 10, 1 << 34, 1 << 33),
+    (1 << 29, (1 << 29) + 1, 1 << 35, 1 << 35),
+])
+def test_extents_past_64_bits_are_overlaps(T, H, token, head):
+    assert latent(T=T, H=H, qs=token, qh=head, os=token, oh=head) == INVALID
+    assert latent(T=T, H=H, qs=token, qh=head, os=token, oh=head, q=P, out=P + 16) == INVALID
