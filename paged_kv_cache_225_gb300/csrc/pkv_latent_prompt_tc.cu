@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  it.row0 + it.tok0 + static_cast<int>(mine) * kM, &sm.q_full[mine]);
                 ++qn;
             }
-            for (int j = 0; j < it.blocks && ok; ++j, ++b) {
+            for (int j = 0; j < it.blocks && ok; ++j) {
                 const int row = it.row0 + j * kM;
                 uint64_t *bar = &filled[b % kTurns];
                 const uint32_t v_slot = slot_of(b * CB + CK);
@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         load_elected(dst, &maps.v, 64 * half, it.head, row, bar);
                     }
                 }
-                if (!ok && asked)
-                    ++b;  // its first copies are under way
+                // Copies of it are under way: all or, where a wait gave up, the first.
+                b += asked ? 1 : 0;
             }
         }
         if (!ok && lane == 0) {

@@ -2,6 +2,7 @@
 formulas in 64 bits: lengths, heads, types, strides, what unseen places may hold,
 scales, device-side reports, streams and graphs, and a serving run of all of it."""
 import math
+import time
 
 import numpy as np
 import pytest
@@ -716,3 +717,17 @@ def test_serving_run(dtype):
             bound = 0.03 if dtype == BF16 else 1e-5     # roundings of q_abs, rows and out to the type
             assert float((got - dense).norm() / dense.norm()) < bound
     assert int(status) == 0 and [int(n) for n in seq] == [n + 20 for n in lens]
+
+
+@pytest.mark.parametrize("D,seconds", [(64, 3), (128, 2)])
+def test_prompt_timeout_waits_for_the_copies_in_flight(D, seconds):
+    # A wait gives up after a second.  The first copy of K never comes: the warp that copies K first
+    # waits for a slot, then, before it leaves, for block 0, which is not whole.  With heads of 64 it
+    # has also asked for the first half of block 3 by then, and that block is not whole either.
+    lens = [3000, 5]
+    a = prompt(lens, 2, D, BF16, 29)
+    want = attend(*a, lens, SCALE)
+    t0 = time.perf_counter()
+    attend(*a, lens, SCALE, want=5, flags=pkv.FLAG_TEST_DROP_FIRST_COPY)
+    assert abs(time.perf_counter() - t0 - seconds) < 0.5
+    assert torch.equal(attend(*a, lens, SCALE), want)
