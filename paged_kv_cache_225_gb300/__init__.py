@@ -959,8 +959,9 @@ def latent_workspace_size(dtype: torch.dtype, num_seqs: int, num_heads: int, lat
                           max_seq_len: int) -> int:
     """Workspace bytes of ``latent_attn_decode`` (pkv_latent_attn_workspace_size)."""
     code = _FLOATS.get(dtype)
-    n = 0 if code is None else lib().pkv_latent_attn_workspace_size(code, num_seqs, num_heads, latent_dim, _ROPE,
-                                                                    16, max_seq_len)
+    n = 0
+    if code is not None and max(abs(x) for x in (num_seqs, num_heads, latent_dim, max_seq_len)) <= _INT_MAX:
+        n = lib().pkv_latent_attn_workspace_size(code, num_seqs, num_heads, latent_dim, _ROPE, 16, max_seq_len)
     if n == 0:
         raise ValueError("sizes that latent_attn_decode does not take")
     return int(n)
@@ -1000,7 +1001,7 @@ def latent_attn_decode(q: torch.Tensor, cache: torch.Tensor, block_tables: torch
         raise ValueError("inconsistent shapes")
     if max_seq_len is None:
         max_seq_len = width * B
-    if max(S, H, N, width, max_seq_len) > _INT_MAX:
+    if max(S, H, N, width, abs(max_seq_len)) > _INT_MAX:
         raise ValueError("at most 2^31 - 1 sequences, pages, entries of a row and tokens")
     if workspace is None:
         # Of the call's own stream: the allocator hands it out again in that stream's order.
@@ -1054,7 +1055,8 @@ def latent_prompt_attn(q: torch.Tensor, k: torch.Tensor, k_rope: torch.Tensor, v
         raise ValueError("at most 2^31 - 1 rows, sequences and heads")
     _launch("pkv_latent_prompt_attn", index, stream,
             (q.data_ptr(), k.data_ptr(), k_rope.data_ptr(), v.data_ptr(), code, qs, ks, kh, rs, vs, vh, starts, S,
-             T, H, D, _ROPE, T if max_q_len is None else min(int(max_q_len), T), float(scale), o, st, int(flags)))
+             T, H, D, _ROPE, T if max_q_len is None else max(-1, min(int(max_q_len), T)), float(scale), o, st,
+             int(flags)))
     return out
 
 

@@ -233,3 +233,32 @@ def test_queries_in_place_need_their_own_strides():
 def test_extents_past_64_bits_are_overlaps(T, H, token, head):
     assert latent(T=T, H=H, qs=token, qh=head, os=token, oh=head) == INVALID
     assert latent(T=T, H=H, qs=token, qh=head, os=token, oh=head, q=P, out=P + 16) == INVALID
+
+
+def test_workspace_sizes_past_32_bits():
+    # The library counts in 32 bits: 2^32 + 100 tokens are not 100.
+    assert pkv.latent_workspace_size(torch.bfloat16, 1, 16, 512, 100) > 0
+    for far in (2 ** 32, -2 ** 32, 2 ** 40):
+        for sizes in ((1 + far, 16, 512, 100), (1, 16 + far, 512, 100), (1, 16, 512 + far, 100),
+                      (1, 16, 512, 100 + far)):
+            with pytest.raises(ValueError):
+                pkv.latent_workspace_size(torch.bfloat16, *sizes)
+
+
+@pytest.mark.gpu
+def test_bounds_past_32_bits():
+    d = dict(device="cuda")
+    tab, lens = torch.zeros((1, 2), dtype=torch.int32, **d), torch.ones(1, dtype=torch.int32, **d)
+    out = torch.full((1, 2, 256), 7.0, **d)
+    for bound in (2 ** 32 + 16, -2 ** 32 + 16, -2 ** 31):
+        with pytest.raises((ValueError, pkv.PkvError)):
+            pkv.latent_attn_decode(torch.zeros((1, 2, 320), **d), torch.zeros((3, 16, 320), **d), tab, lens, 0.1, out,
+                                   max_seq_len=bound)
+    x, start = torch.zeros((4, 2, 64), **d), torch.tensor([0, 4], dtype=torch.int32, **d)
+    rows = torch.full_like(x, 7.0)
+    for bound in (-2 ** 32 + 4, -2 ** 31, -1):
+        with pytest.raises(pkv.PkvError):
+            pkv.latent_prompt_attn(torch.zeros((4, 2, 128), **d), x, torch.zeros((4, 64), **d), x, start, 0.1, rows,
+                                   max_q_len=bound)
+    torch.cuda.synchronize()
+    assert bool((out == 7).all()) and bool((rows == 7).all())
