@@ -731,3 +731,28 @@ def test_prompt_timeout_waits_for_the_copies_in_flight(D, seconds):
     attend(*a, lens, SCALE, want=5, flags=pkv.FLAG_TEST_DROP_FIRST_COPY)
     assert abs(time.perf_counter() - t0 - seconds) < 0.5
     assert torch.equal(attend(*a, lens, SCALE), want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+def test_prompt_rows_that_do_not_see_it_keep_their_bits(bad, D, dtype):
+    # One spoilt token and spoilt rows behind the last sequence: every row before the token, and the
+    # other sequences whole, are computed from the same numbers in the same order.
+    lens = [70, 400, 45]
+    q, k, kr, v = prompt(lens, 4, D, dtype, 34, tail=9)
+    want = attend(q, k, kr, v, lens, SCALE)
+    at = 70 + 300
+    for t in (k, kr, v):
+        t[at] = bad
+        t[sum(lens):] = bad
+    out = attend(q, k, kr, v, lens, SCALE)
+    assert torch.equal(out[:at], want[:at]) and torch.equal(out[470:515], want[470:515])
+    assert torch.isnan(out[at:470].float()).all() and torch.isnan(out[515:].float()).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_bound_of_zero(dtype):
+    q, cache, tables, lens = make([5, 0, 70], 16, 256, dtype, 35)
+    assert not bool(decode(q, cache, tables, torch.zeros_like(lens), SCALE, max_seq_len=0).any())
+    assert not bool(decode(q, cache, tables, lens, SCALE, want=4, max_seq_len=0).any())  # clamped, reported

@@ -309,3 +309,63 @@ def test_queries_in_place_with_other_strides_are_refused():
     want = rotate(one, table, pos[:1], False, F32).to(BF16)
     got = pkv.rope_append(wide[:1, :4].copy_(one), k[:1], v[:1], pos[:1], table, slots[:1], *caches, q_out=dense[:1])
     assert torch.equal(raw(got), raw(want))
+
+
+@pytest.mark.parametrize("cache", CACHES)
+def test_a_replayed_graph_writes_what_a_call_writes(cache):
+    q, k, v, pos, slots, N = case("padded", 8, 2, 128, BF16, 18)
+    table = rope_table(MAX_POS, 128, DEV)
+    a = [cache_like(N, 2, 128, cache, i) for i in (1, 2)]
+    b = [x.clone() for x in a]
+    oa, ob = (torch.zeros_like(q.contiguous()) for _ in range(2))
+    scales = dict(k_scale=SCALE, v_scale=2 * SCALE)
+    warm = [x.clone() for x in a]
+    pkv.rope_append(q, k, v, pos, table, slots, *warm, q_out=ob, **scales)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkv.rope_append(q, k, v, pos, table, slots, *b, q_out=ob, **scales)
+    # Other rows, positions and slots than at the capture.
+    k.mul_(0.5)
+    v.mul_(-0.5)
+    q.mul_(0.25)
+    pos.copy_((pos + 7) % MAX_POS)
+    slots.copy_(torch.where(slots >= 0, slots ^ 16, slots))
+    pkv.rope_append(q, k, v, pos, table, slots, *a, q_out=oa, **scales)
+    ob.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(raw(oa), raw(ob))
+    good = slots >= 0
+    turned = rotate(k, table, pos, False, F32)
+    want = [cache_like(N, 2, 128, cache, i) for i in (1, 2)]
+    pkv.reshape_and_cache(turned, v.float().contiguous(), slots, *want, **scales)
+    for x, y, z in zip(a, b, want):
+        assert torch.equal(raw(x), raw(y)) and torch.equal(raw(x), raw(z))
+    assert bool(good.any())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_replayed_graph_writes_the_latent_rows_of_a_call(dtype):
+    latent, key, q, pos, slots, N = latent_case("padded", 512, 5, dtype, 19)
+    table = rope_table(MAX_POS, ROPE, DEV)
+    a, b = (torch.full((N, 16, 576), 3.0, dtype=dtype, device=DEV) for _ in range(2))
+    oa, ob = (torch.zeros((len(pos), 5, ROPE), dtype=dtype, device=DEV) for _ in range(2))
+    pkv.latent_append(latent, key, pos, table, slots, a.clone(), q_rope=q, q_out=ob)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkv.latent_append(latent, key, pos, table, slots, b, q_rope=q, q_out=ob)
+    latent.mul_(0.5)
+    key.mul_(-2.0)
+    pos.copy_((pos + 7) % MAX_POS)
+    slots.copy_(torch.where(slots >= 0, slots ^ 16, slots))
+    pkv.latent_append(latent, key, pos, table, slots, a, q_rope=q, q_out=oa)
+    ob.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    good = slots >= 0
+    want = torch.full_like(a, 3.0)
+    rows = torch.cat([latent.float(), rotate(key[:, None], table, pos, False, F32)[:, 0]], 1).to(dtype)
+    want.view(-1, 576)[slots[good]] = rows[good]
+    assert torch.equal(raw(oa), raw(ob)) and torch.equal(raw(a), raw(b)) and torch.equal(raw(b), raw(want))
