@@ -67,7 +67,7 @@ struct LatentDecodeParams {
     int whole;           // sequences are not cut
     float *part;         // [2 teams][head tiles][tile_heads][R] sums of weights times rows
     float2 *part_ml;     // [2 teams][head tiles][tile_heads] reference of the weights (log2), their sum
-    int2 *pieces;        // [teams] sequence cut by a team's start, by its end (-1: none)
+    int *pieces;         // [teams] sequence cut by a team's start (-1: none)
 };
 
 // Latent attention over whole prompts with keys and values expanded per head.

@@ -271,7 +271,7 @@ pkv_status pkv_latent_attn_decode(const void *q, const void *cache, pkv_dtype dt
     const size_t rows = latent_part_rows(p);
     p.part = static_cast<float *>(workspace);
     p.part_ml = reinterpret_cast<float2 *>(p.part + rows * latent_dim);
-    p.pieces = reinterpret_cast<int2 *>(p.part_ml + rows);
+    p.pieces = reinterpret_cast<int *>(p.part_ml + rows);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const pkv_status done = dtype == PKV_F32 ? launch_latent_decode_simt(p, st) : launch_latent_decode_tc(p, st);
     return done != PKV_OK ? done : launch_latent_merge(p, dtype, st);

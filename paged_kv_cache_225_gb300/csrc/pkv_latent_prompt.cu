@@ -33,27 +33,6 @@ template <int DN> struct LpGeom {
     static constexpr int kSmem = (kRows * kLd + kKP + kKeys * DN) * 4;
 };
 
-__device__ __forceinline__ void fma2(uint64_t &c, uint64_t a, uint64_t b)
-{
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ void mul2(uint64_t &c, uint64_t a)
-{
-    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(c) : "l"(a));
-}
-__device__ __forceinline__ uint64_t pair(float lo, float hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-
 template <int DN>
 __global__ void __launch_bounds__(kSimtThreads, 2) latent_prompt_simt_kernel(const LatentPromptParams p)
 {

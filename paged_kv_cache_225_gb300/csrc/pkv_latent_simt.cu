@@ -20,7 +20,6 @@ namespace {
 
 constexpr int kSimtThreads = 256;
 constexpr int kSimtHeads = 16;
-constexpr int kBad = -1;
 
 template <int R> struct LatentSimt {
     static constexpr int kRow = R + kRopeDim;
@@ -29,14 +28,9 @@ template <int R> struct LatentSimt {
     static constexpr int kSmem = (1 + kPages) * 16 * kLd * 4;
 };
 
-__device__ __forceinline__ void fma2(uint64_t &c, uint64_t a, uint64_t b)
-{
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
-}
 __device__ __forceinline__ float sum2(uint64_t v)
 {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    const float2 r = unpair(v);
     return r.x + r.y;
 }
 
@@ -76,7 +70,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const Late
     LatentWalk walk;
     if (warp == 0)
         walk.init(p, team, lane, blockIdx.x == 0);
-    int2 cut = make_int2(kBad, kBad);
+    int cut = -1;
     for (;;) {
         if (warp == 0) {
             const LatentPiece next = walk.next(p);
@@ -88,9 +82,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const Late
         if (piece.s < 0)
             break;
         if (piece.first > 0)
-            cut.x = piece.s;
-        if (piece.last < piece.tiles)
-            cut.y = piece.s;
+            cut = piece.s;
         load_rows<R>(sq, static_cast<const float *>(p.q) + (static_cast<size_t>(piece.s) * p.num_heads + h0) * kRow,
                      heads);
         const int from = piece.first * (kLatentTokens / 16);  // pages
@@ -177,14 +169,12 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const Late
                     s_alpha[h] = alpha;
             }
             __syncthreads();
-            // Output dims threadIdx.x (+ R / 2).
+            // Output dims 2 threadIdx.x and the next, or dim threadIdx.x.
             if constexpr (kDims == 2) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float a = s_alpha[i];
-                    uint64_t a2;
-                    asm("mov.b64 %0, {%1, %1};" : "=l"(a2) : "f"(a));
-                    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(o[i]) : "l"(a2));
+                    mul2(o[i], pair(a, a));
                 }
 #pragma unroll 4
                 for (int t = 0; t < 16; ++t) {
@@ -194,25 +184,20 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const Late
                         const float4 w = *reinterpret_cast<const float4 *>(&s_p[t][i]);
                         const float ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint64_t w2;
-                            asm("mov.b64 %0, {%1, %1};" : "=l"(w2) : "f"(ww[e]));
-                            fma2(o[i + e], w2, v);
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            fma2(o[i + e], pair(ww[e], ww[e]), v);
                     }
                 }
             } else {
                 // One dim: pairs of heads.
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const uint64_t a2 = *reinterpret_cast<const uint64_t *>(&s_alpha[2 * i]);
-                    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(o[i]) : "l"(a2));
+                    mul2(o[i], *reinterpret_cast<const uint64_t *>(&s_alpha[2 * i]));
                 }
 #pragma unroll 4
                 for (int t = 0; t < 16; ++t) {
                     const float x = k[t * kLd + threadIdx.x];
-                    uint64_t v;
-                    asm("mov.b64 %0, {%1, %1};" : "=l"(v) : "f"(x));
+                    const uint64_t v = pair(x, x);
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
                         const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(&s_p[t][2 * i]);
@@ -237,10 +222,9 @@ __global__ void __launch_bounds__(kSimtThreads, 2) latent_simt_kernel(const Late
                 break;
             float2 y;
             if constexpr (kDims == 2) {
-                asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(o[h]));
+                y = unpair(o[h]);
             } else {
-                float2 z;
-                asm("mov.b64 {%0, %1}, %2;" : "=f"(z.x), "=f"(z.y) : "l"(o[h / 2]));
+                const float2 z = unpair(o[h / 2]);
                 y.x = h & 1 ? z.y : z.x;
                 y.y = 0.f;
             }
@@ -303,13 +287,13 @@ __global__ void __launch_bounds__(32 * (kShare > 1 ? kShare : kMergeWarps))
     int cut[kMost];
 #pragma unroll
     for (int i = 0; i < kMost; ++i)
-        cut[i] = 32 * i + lane < p.teams ? p.pieces[32 * i + lane].x : -1;
+        cut[i] = 32 * i + lane < p.teams ? p.pieces[32 * i + lane] : -1;
     int s = blockIdx.x;
     if (!by_sequence) {
         const int team = blockIdx.x + 1;
-        s = p.pieces[team].x;
+        s = p.pieces[team];
         // The piece before starts the sequence if nothing before that one belongs to it.
-        if (s < 0 || p.pieces[team - 1].x == s)
+        if (s < 0 || p.pieces[team - 1] == s)
             return;
     }
     int team = p.teams, count = 0;  // the first team that goes on with s, and how many do
@@ -489,7 +473,7 @@ size_t latent_plan(LatentDecodeParams &p, int dtype)
     if (p.whole && p.num_seqs < p.teams)
         p.teams = p.num_seqs > 0 ? p.num_seqs : 1;
     const size_t rows = latent_part_rows(p);
-    return (rows * (p.latent_dim * sizeof(float) + sizeof(float2)) + p.teams * sizeof(int2) + 255) / 256 * 256;
+    return (rows * (p.latent_dim * sizeof(float) + sizeof(float2)) + p.teams * sizeof(int) + 255) / 256 * 256;
 }
 
 pkv_status launch_latent_decode_simt(const LatentDecodeParams &p, cudaStream_t stream)

@@ -53,8 +53,6 @@
 // 8192 tokens 130 against 118); partial sums with the heads next to each other (32 bytes to
 // a lane: 78 against 65); the barrier of the softmax warps also telling failures apart
 // without a second look (the same).
-#include <type_traits>
-
 #include "pkv_latent.cuh"
 #include "pkv_tc.cuh"
 
@@ -207,13 +205,6 @@ __device__ __forceinline__ bool half_any(int g, bool x)
         : "r"(g + 1), "r"(x ? 1u : 0u)
         : "memory");
     return r != 0;
-}
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // A ring's position: slot and parity of its phase.
@@ -551,16 +542,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int m_head = g * kHalfCols + 8 * (lane >> 4) + (lane & 7), m_piece = 2 * quad + ((lane >> 3) & 1);
         const uint32_t p_addr = smem0 + kPOff + m_head * 128 + ((m_piece ^ (m_head & 7)) << 4);
         uint32_t cnt = 0;  // tiles
-        int2 cut = make_int2(-1, -1);
+        int cut = -1;
         bool failed = false, gone = false;
         for (;;) {
             const LatentPiece piece = walk.next(p);
             if (piece.s < 0)
                 break;
             if (piece.first > 0)
-                cut.x = piece.s;
-            if (piece.last < piece.tiles)
-                cut.y = piece.s;
+                cut = piece.s;
             const int heads = min(NH, p.num_heads - h0);
             if (piece.len == 0) {
                 const size_t at = (static_cast<size_t>(piece.s) * p.num_heads + h0) * R;
@@ -624,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float top = fmaxf(fmaxf(s_red[g][0][col], s_red[g][1][col]),
                                                 fmaxf(s_red[g][2][col], s_red[g][3][col]));
                         const float up = fmaxf(m[i], top);
-                        alpha[i] = up == m[i] ? 1.f : ex2(m[i] - up);
+                        alpha[i] = up == m[i] ? 1.f : MmaSoftmax::ex2(m[i] - up);
                         m[i] = up;
                         l[i] *= alpha[i];
                         if (quad == 0 && lane < 4)
@@ -661,8 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 2 * J; i += 2) {
                     const float o0 = m[i] == -INFINITY ? 0.f : -m[i], o1 = m[i + 1] == -INFINITY ? 0.f : -m[i + 1];
-                    const float a0 = ex2(fmaf(x[2 * i], c, o0)), a1 = ex2(fmaf(x[2 * i + 1], c, o1));
-                    const float b0 = ex2(fmaf(x[2 * i + 2], c, o0)), b1 = ex2(fmaf(x[2 * i + 3], c, o1));
+                    const float a0 = MmaSoftmax::ex2(fmaf(x[2 * i], c, o0)), a1 = MmaSoftmax::ex2(fmaf(x[2 * i + 1], c, o1));
+                    const float b0 = MmaSoftmax::ex2(fmaf(x[2 * i + 2], c, o0)), b1 = MmaSoftmax::ex2(fmaf(x[2 * i + 3], c, o1));
                     l[i] += a0 + b0;
                     l[i + 1] += a1 + b1;
                     w[i] = pack_bf16(a0, a1);
