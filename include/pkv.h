@@ -663,7 +663,8 @@ pkv_status pkv_latent_append(const void *latent, const void *k_rope, pkv_dtype i
  *                 zero output row.  A block id outside the pool counts as 16 rows of
  *                 zeros and is reported as PKV_ERR_OUT_OF_RANGE, as is a length
  *                 outside [0, max_seq_len], which is clamped.
- *   num_seqs      up to 2^20, and num_seqs * max_seq_len below 2^36 or so (num_seqs *
+ *   num_seqs      up to 2^20 (every CTA reads all lengths: 2^17 empty sequences
+ *                 cost 0.8 ms), and num_seqs * max_seq_len below 2^36 or so (num_seqs *
  *                 (max_seq_len / 64 + 1) below 2^30), max_seq_len up to 2^31 - 65 (else
  *                 PKV_ERR_UNSUPPORTED).
  *   scale         finite, any sign.

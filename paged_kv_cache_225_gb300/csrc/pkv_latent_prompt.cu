@@ -11,6 +11,11 @@
 // shared memory, so that two CTAs fit an SM; a thread owns 4 rows x 2 keys of the
 // scores and 4 rows x Dn / 16 columns of the output; products are packed two to an
 // instruction.
+//
+// What bounds it (8 prompts of 256 to 1024 tokens, 32 heads of 128 + 64: 1.32 ms, 27
+// TFLOP/s), by its code: a block's K and V are asked for when the last one is done, so only
+// the other CTA of the SM covers their way, and sixteen packed multiply-adds of the scores
+// take six shared-memory loads.
 #include "pkv_latent.h"
 #include "pkv_prompt.cuh"
 

@@ -28,17 +28,19 @@
 //    in that block: NaN and infinities there are replaced by zeros in shared memory before
 //    the product, their first rows noted per dim, and added to the outputs of the rows
 //    that see them (s_seen).  Rows past the sequence are zeroed.
+//  * Weights are rounded to bf16 (off by 2^-8 at most), their sum is that of the f32 ones:
+//    two parts of each would double the products of P V, on the unit that bounds this.
 //  * Every wait is bounded; a timeout records PKV_ERR_TIMEOUT, stops every role, lets
 //    copies and MMAs in flight finish and frees TMEM.
 //
 // What bounds it.  Long prompts: the tensor cores and their power (one of 16K tokens, 32
-// heads: 1.63 to 1.73 ms, 1590 to 1690 TFLOP/s, 85 to 90% of a cuBLAS burst, 94 to 99% of what cuBLAS
-// sustains): a block takes them 2560 cycles for both tiles, a step 3600, of which the
+// heads: 1.63 to 1.77 ms by the box, 1550 to 1690 TFLOP/s, 83 to 90% of a cuBLAS burst, 91 to 99% of what
+// cuBLAS sustains): a block takes them 2560 cycles for both tiles, a step 3600, of which the
 // issuing warp waits 570 for the softmax and 320 for K and V.  16 prompts of 512 to 4096
-// tokens: 850 us, 1170 TFLOP/s: steps of 4150 cycles, 1160 of them waiting for the softmax
+// tokens: 855 us, 1160 TFLOP/s: steps of 4150 cycles, 1160 of them waiting for the softmax
 // (an item is 10 blocks, and its ends do not overlap as well).  128 prompts of 256 to 512
 // tokens: 441 us, 60% of HBM's bytes; heads of 64 + 64 (37 prompts of up to 1000 tokens,
-// 32 heads): 180 to 200 us; both are chains of load, scores, softmax, P V and store of items two
+// 32 heads): 181 us; both are chains of load, scores, softmax, P V and store of items two
 // or three blocks long.
 //
 // V with values that are not finite, one prompt of 8192 tokens, 32 heads: 438 us without,
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&sm.item_empty[slot]);
         return true;
     };
-    // Slot and, of V's two halves, whether they lie at the ends of the ring.
+    // Slot of chunk c, counted over all blocks.
     auto slot_of = [](uint32_t c) { return c % NS; };
 
     if (warp == kProducerWarp || warp == kProducerWarp + 1) {

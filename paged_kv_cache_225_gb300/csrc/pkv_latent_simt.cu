@@ -9,7 +9,7 @@
 // 16 heads x 16 tokens (a warp: 4 heads, all tokens, half the dims; a lane 4 heads x
 // 2 tokens on every fourth of those dims), one pass of the softmax with a thread
 // per score, then R / 256 output dims of all heads per thread.  Shared-memory loads and
-// the steps of a page bound it: 16 sequences of 4096 tokens, 32 heads, R = 512: 159 us (29
+// the steps of a page bound it: 16 sequences of 4096 tokens, 32 heads, R = 512: 157 us (29
 // TFLOP/s); 8 of up to 4096, 16 heads, R = 256: 24 us.  With the four lanes of a token next to each other
 // (two rows to a load's phase, in the same banks) 213 and 29 us.
 #include "pkv_latent.cuh"
@@ -441,7 +441,7 @@ template <typename T, int R> pkv_status launch_merge_by(const LatentDecodeParams
 
 }  // namespace
 
-// Cut / whole, us: one sequence of 200 tokens, 32 heads 10.7 / 10.4, of 512 9.4 / 14.1; 128
+// Cut / whole, us, when the rule was chosen: one sequence of 200 tokens, 32 heads 10.7 / 10.4, of 512 9.4 / 14.1; 128
 // of 256 to 512 31 / 30, of 500 to 1000 37 / 46.
 constexpr double kCut = 4, kCutAll = 1.5;
 
@@ -454,8 +454,8 @@ size_t latent_plan(LatentDecodeParams &p, int dtype)
 {
     // fp32: two CTAs to an SM.  bf16: one, with the fewest head columns that hold the heads
     // (columns cost time, and the room they leave holds more tiles): 256 x 4096 tokens of 16
-    // heads take 192 us with 16 columns, 194 with 32, 202 with 64; 128 of 500 to 1000
-    // tokens, 32 heads, 36.3 with 32 columns, 38.3 with 64.
+    // heads took 192 us with 16 columns, 194 with 32, 202 with 64 on one box; 128 of 500 to
+    // 1000 tokens, 32 heads, 36.3 with 32 columns, 38.3 with 64.
     p.tile_heads = dtype == PKV_F32 || p.num_heads <= 16 ? 16 : p.num_heads <= 32 ? 32 : 64;
     p.head_tiles = (p.num_heads + p.tile_heads - 1) / p.tile_heads;
     const long ctas = dtype == PKV_F32 ? 2 * kLatentSms : kLatentSms;

@@ -23,6 +23,9 @@
 //  * The reference of a head's weights is raised only when a score exceeds it by 2^8;
 //    O^T is then rescaled in TMEM.  All weights of a head and tile share it, so the
 //    four warps of a half agree through a barrier.
+//  * Weights are rounded to bf16 (off by 2^-8 at most), their sum is that of the f32 ones.
+//    A second part of each, for 16 bits, would double the products of P V and needs 8 KB
+//    more with 64 heads, where two tiles leave 1 KB.
 //  * Rows past the sequence's end are zeroed in shared memory before P V, which
 //    multiplies them with 0: they may hold anything.
 //  * Every wait is bounded; a timeout records PKV_ERR_TIMEOUT, stops every role, lets
@@ -41,10 +44,12 @@
 // and the end of P V (scores 900, softmax 1000, P V 700, hand-overs) and 2300 more until
 // the next one has landed; that alone would leave 6.0 TB/s (16 heads in 64 columns), the
 // rest are the partial sums of cut sequences, 128 KB each.  128 heads are two CTAs that read the same rows
-// (128 x 4096 tokens: 171 us, 856 TFLOP/s): the same chain, with 1940 cycles of products in
+// (128 x 4096 tokens: 170 us, 860 TFLOP/s): the same chain, with 1940 cycles of products in
 // 2800.  Short calls: about 6000 cycles until the first tile lands (the lengths and the
 // table are two dependent trips to memory) and the joining kernel (64 sequences of a
-// mean of 2900 tokens, 64 heads: 53 + 8.5 us).
+// mean of 2900 tokens, 64 heads: 53 + 8.5 us).  Many sequences: every CTA reads all lengths,
+// a run of neighbours to a lane (2^17 empty ones 0.8 ms, of 16 tokens and one head 2.3 ms:
+// the rest is a chain for each).
 //
 // Measured and not kept: one warp for all MMAs that takes what is ready (64 x 64 heads
 // 76 us against 66 then: it looks as long as it issues); one copying warp, two, four (73,
@@ -393,9 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // With two head tiles, each row is read by two CTAs, and the rings hold half as many
         // bytes of HBM: pages are fetched into L2 while the rings are still full.  Two tiles
         // at a time, a lane for each page; the head tiles share the pages out.  128 x 4096
-        // tokens, 128 heads: 174 us, without 198; four tiles ahead 182.  With one head tile
-        // the rings are enough, and it costs (256 x 4096, 16 heads: 194 us without, 207 two
-        // ahead, 275 four: more than L2 keeps).
+        // tokens, 128 heads, when it was added: 174 us, without 198; four tiles ahead 182.
+        // With one head tile the rings are enough, and it costs (256 x 4096, 16 heads, then:
+        // 194 us without, 207 two ahead, 275 four: more than L2 keeps).  The wait below ends
+        // with the copying warp, which issues every tile or gives up at its limit and says so.
         const volatile uint32_t *issued = &s_issued;
         uint32_t tiles = 0;
         for (bool on = true; on;) {

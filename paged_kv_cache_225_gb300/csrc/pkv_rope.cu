@@ -29,9 +29,11 @@
 // heads on their way.  A chat batch (128 prompts of 256 to 512 tokens, 64/8 heads, bf16):
 // 366 us, 5.4 TB/s (80% of a plain copy); as f32 numbers and three CTAs 417 us; one set 381,
 // four (which spill) 416 us.  With an fp8 cache of heads of 64 (37 prompts of up to 1000
-// tokens, 24/2 heads) 41 us, 4.0 TB/s.  The latent rows of 16 prompts of 512 to 4096 tokens
-// with 32 query heads: 94 us, 4.6 TB/s (their 128-byte pieces lie 384 and 1152 bytes apart);
-// two sets or four CTAs 95 to 104 us.
+// tokens, 24/2 heads) 41 us, 4.0 TB/s: 24 heads are three sets of eight, so that a warp's
+// second turn of two sets is half empty.  The latent rows of 16 prompts of 512 to 4096 tokens
+// with 32 query heads: 97 us, 4.5 TB/s (their 128-byte pieces lie 384 and 1152 bytes apart);
+// two sets or four CTAs were no faster.  The same rows in f32: 201 us, 4.3 TB/s.  There the
+// bound of five CTAs, chosen on bf16 (12 bytes spilled), spills 100 bytes.
 #include "pkv_convert.cuh"
 #include "pkv_latent.h"
 
