@@ -841,9 +841,9 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pos
     first rot dims of a head are turned); slot_mapping int64 [T] and the caches as for
     ``reshape_and_cache``.  Pairs are dims (i, i + rot / 2), or (2i, 2i + 1) if
     ``interleaved``.  The turned queries go to ``q_out`` (default: in place), which is
-    returned (at q's address it needs q's strides); q may be None.  Tokens with a negative slot are padding: nothing of them is
-    read or written.  ``status`` int32 [1] (optional) records slots and positions out of
-    range, whose tokens are skipped too.
+    returned (at q's address it needs q's strides); q may be None.  Tokens with a negative
+    slot are padding: nothing of them is read or written.  ``status`` int32 [1] (optional)
+    records slots and positions out of range, whose tokens are skipped too.
     """
     index = _cuda_index(k, "k")
     dtype = k.dtype

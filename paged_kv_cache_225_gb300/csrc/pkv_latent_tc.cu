@@ -656,8 +656,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 2 * J; i += 2) {
                     const float o0 = m[i] == -INFINITY ? 0.f : -m[i], o1 = m[i + 1] == -INFINITY ? 0.f : -m[i + 1];
-                    const float a0 = MmaSoftmax::ex2(fmaf(x[2 * i], c, o0)), a1 = MmaSoftmax::ex2(fmaf(x[2 * i + 1], c, o1));
-                    const float b0 = MmaSoftmax::ex2(fmaf(x[2 * i + 2], c, o0)), b1 = MmaSoftmax::ex2(fmaf(x[2 * i + 3], c, o1));
+                    const float a0 = MmaSoftmax::ex2(fmaf(x[2 * i], c, o0));
+                    const float a1 = MmaSoftmax::ex2(fmaf(x[2 * i + 1], c, o1));
+                    const float b0 = MmaSoftmax::ex2(fmaf(x[2 * i + 2], c, o0));
+                    const float b1 = MmaSoftmax::ex2(fmaf(x[2 * i + 3], c, o1));
                     l[i] += a0 + b0;
                     l[i + 1] += a1 + b1;
                     w[i] = pack_bf16(a0, a1);

@@ -2,7 +2,6 @@
 formulas in 64 bits: lengths, heads, types, strides, what unseen places may hold,
 scales, device-side reports, streams and graphs, and a serving run of all of it."""
 import math
-import time
 
 import numpy as np
 import pytest
@@ -727,9 +726,16 @@ def test_prompt_timeout_waits_for_the_copies_in_flight(D, seconds):
     lens = [3000, 5]
     a = prompt(lens, 2, D, BF16, 29)
     want = attend(*a, lens, SCALE)
-    t0 = time.perf_counter()
-    attend(*a, lens, SCALE, want=5, flags=pkv.FLAG_TEST_DROP_FIRST_COPY)
-    assert abs(time.perf_counter() - t0 - seconds) < 0.5
+    out, at = torch.empty_like(want), starts(lens)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    torch.cuda.synchronize()
+    begin.record()
+    pkv.latent_prompt_attn(*a, at, SCALE, out, status=status, flags=pkv.FLAG_TEST_DROP_FIRST_COPY)
+    end.record()
+    torch.cuda.synchronize()
+    assert int(status) == 5
+    assert seconds - 0.1 < begin.elapsed_time(end) / 1e3 < seconds + 0.8
     assert torch.equal(attend(*a, lens, SCALE), want)
 
 
