@@ -34,7 +34,7 @@
 //    copies and MMAs in flight finish and frees TMEM.
 //
 // What bounds it.  Long prompts: the tensor cores and their power (one of 16K tokens, 32
-// heads: 1.63 to 1.77 ms by the box, 1550 to 1690 TFLOP/s, 83 to 90% of a cuBLAS burst, 91 to 99% of what
+// heads: 1.63 to 1.77 ms by the card, 1550 to 1690 TFLOP/s, 83 to 90% of a cuBLAS burst, 91 to 99% of what
 // cuBLAS sustains): a block takes them 2560 cycles for both tiles, a step 3600, of which the
 // issuing warp waits 570 for the softmax and 320 for K and V.  16 prompts of 512 to 4096
 // tokens: 855 us, 1160 TFLOP/s: steps of 4150 cycles, 1160 of them waiting for the softmax

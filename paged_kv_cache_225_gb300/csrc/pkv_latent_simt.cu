@@ -454,7 +454,7 @@ size_t latent_plan(LatentDecodeParams &p, int dtype)
 {
     // fp32: two CTAs to an SM.  bf16: one, with the fewest head columns that hold the heads
     // (columns cost time, and the room they leave holds more tiles): 256 x 4096 tokens of 16
-    // heads took 192 us with 16 columns, 194 with 32, 202 with 64 on one box; 128 of 500 to
+    // heads took 192 us with 16 columns, 194 with 32, 202 with 64 on one card; 128 of 500 to
     // 1000 tokens, 32 heads, 36.3 with 32 columns, 38.3 with 64.
     p.tile_heads = dtype == PKV_F32 || p.num_heads <= 16 ? 16 : p.num_heads <= 32 ? 32 : 64;
     p.head_tiles = (p.num_heads + p.tile_heads - 1) / p.tile_heads;
